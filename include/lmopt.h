@@ -93,8 +93,18 @@ enum {
     OPTIM_KIND_FACTORED = 1,
     OPTIM_KIND_NADAM_F24 = 2,
     OPTIM_KIND_ADAN = 3,
-    OPTIM_KIND_ADAN_F24 = 4
+    OPTIM_KIND_ADAN_F24 = 4,
+    OPTIM_KIND_ADAMW = 5,
+    OPTIM_KIND_ADAMW_U8 = 6
 };
+/* ADAMW groups keep m and v as fp32 [numel].  ADAMW_U8 groups keep those of tensors above 4096
+ * elements in 8 bits: each buffer holds numel codes, padding up to a multiple of 16 bytes, then
+ * one fp32 constant q for each block of OPTIM_U8_BLOCK consecutive elements (the last may be
+ * short).  m = t |t| with t = (code - 128) q, v = (code q)^4, q = sqrt(max |m|) / 127 and
+ * max(v)^(1/4) / 255 over the block: the companding of the u16 codes, with a scale per block.
+ * 12.06 bytes per element per step instead of 26 (weight, residual and gradient included).  Buffers
+ * are 4-byte aligned and start as zero bytes (which decode to zero). */
+#define OPTIM_U8_BLOCK 256
 /* ADAN groups: m -> fp32 [3*P] (planes m, v, n, each P = numel rounded up to a multiple of 4
  * floats, so that every plane of a 16-byte aligned buffer is 16-byte aligned and takes the
  * 128-bit path), v -> uint16 [numel] (previous bf16 gradient), all zero at creation.
@@ -174,7 +184,7 @@ int optim_group_destroy(optim_group_t* group);
 int optim_step_nadam_kahan(optim_group_t* group, const void* const* grads_bf16, int64_t step,
                            const optim_nadam_hparams_t* hp, void* stream);
 /* Kernel launches one step of the group enqueues with these hyper-parameters (NADAM groups: 1 or
- * 2, see optim_step_nadam_kahan; NADAM_F24, ADAN, ADAN_F24: 1; hp may be NULL for those).
+ * 2, see optim_step_nadam_kahan; NADAM_F24, ADAN, ADAN_F24, ADAMW, ADAMW_U8: 1; hp may be NULL for those).
  * OPTIM_EINVAL for FACTORED groups, whose launches depend on their waves. */
 int optim_query_launches(optim_group_t* group, const optim_nadam_hparams_t* hp, int32_t* launches);
 
@@ -294,6 +304,31 @@ typedef struct {
 int optim_step_adan(optim_group_t* group, const void* const* grads_bf16, int64_t step,
                     const optim_adan_hparams_t* hp, void* stream);
 
+/* AdamW hyper-parameters (decoupled decay; stochastic_rounding / seed as in optim_nadam_hparams_t). */
+typedef struct {
+    float lr, beta1, beta2, eps, weight_decay;
+    int32_t stochastic_rounding;
+    uint64_t seed;
+} optim_adamw_hparams_t;
+
+/* One fused AdamW step of an ADAMW or ADAMW_U8 group: g' = s g, m = b1 m + (1-b1) g',
+ * v = b2 v + (1-b2) g'^2, w -= lr wd w, w -= lr m / (1-b1^t) / (sqrt(v / (1-b2^t)) + eps), stored
+ * as the other steps store it (Kahan split, stochastic or nearest rounding).  Every product, sum,
+ * root and quotient is rounded once; unlike in the other steps no multiply-add is fused.
+ *   grad_scale : device scalar s (fp32, 4-byte aligned) multiplied into every gradient -- a clip
+ *                factor or an inverse loss scale, read when the step runs -- or NULL: 1
+ * The update uses the moments before they are coded.  A positive v keeps a code of at least 1.
+ * An infinity or a NaN in a gradient does not enter its block's scale; its own moment takes the
+ * largest code and the weight it reaches is counted by optim_query_nonfinite.  Arguments as
+ * optim_step_nadam_kahan; one enqueued kernel. */
+int optim_step_adamw(optim_group_t* group, const void* const* grads_bf16, int64_t step,
+                     const optim_adamw_hparams_t* hp, const float* grad_scale, void* stream);
+/* The moments of an ADAMW or ADAMW_U8 group as fp32 values, for checkpoints of another format and for
+ * inspection: tensor i starts at element sum over j < i of numel_j rounded up to 64 of each flat
+ * DEVICE buffer (4-byte aligned; 16-byte aligned buffers take 128-bit stores); the gaps are not
+ * written.  One enqueued kernel.  OPTIM_ESTATE for offloaded groups. */
+int optim_group_unpack_state(optim_group_t* group, float* m, float* v, void* stream);
+
 /* Encodes n fp32 moments into u16 codes with the engine's codec.  scale (device, 1 float) is
  * written with max|src| (is_signed = 1, exp_avg) or max src (is_signed = 0, exp_avg_sq); codes
  * are 32768 + sgn(x) rint(32767 sqrt(|x|/S)) or rint(65535 (x/S)^(1/4)).  Two kernels. */
@@ -327,7 +362,7 @@ int optim_query_nonfinite(optim_group_t* group, uint64_t* count);
  * each parameter group's states in for its update and back out afterwards ("Amazing Flux FFT
  * quality on a 5090", sd-scripts PR #2187, first post, and its fourth post for Adan; "Kahan
  * summation for Adafactor-optimized Flux FFT", sd-scripts PR #2159, PR description).  NADAM,
- * NADAM_F24, ADAN and ADAN_F24 groups can be offloaded: their residuals and m, v buffers then
+ * NADAM_F24, ADAN, ADAN_F24, ADAMW and ADAMW_U8 groups can be offloaded: their residuals and m, v buffers then
  * live in PINNED HOST memory, while weights, gradients and the per-tensor scale records stay on
  * the device.  Each step runs on a device staging slot: the copy-in (prefetch) must precede the
  * step, the copy-out (write-back) follows it; every dependency between them is a device-side

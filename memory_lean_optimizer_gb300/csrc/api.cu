@@ -135,6 +135,10 @@ static int validate_desc(const optim_tensor_desc_t& d, int32_t i, int32_t kind) 
         size_t a = d.numel <= kSmall ? 4 : 2;
         if (!is_aligned(d.m, a) || !is_aligned(d.v, a))
             return set_error(OPTIM_EALIGN, "tensor %d: m/v not %zu-byte aligned", i, a);
+    } else if (kind == OPTIM_KIND_ADAMW || kind == OPTIM_KIND_ADAMW_U8) {
+        if (!d.m || !d.v) return set_error(OPTIM_EINVAL, "tensor %d: m or v is NULL", i);
+        if (!is_aligned(d.m, 4) || !is_aligned(d.v, 4))   // 8-bit states hold fp32 scales too
+            return set_error(OPTIM_EALIGN, "tensor %d: m/v not 4-byte aligned", i);
     } else if (kind == OPTIM_KIND_ADAN || kind == OPTIM_KIND_ADAN_F24) {
         if (!d.m || !d.v) return set_error(OPTIM_EINVAL, "tensor %d: Adan state or previous gradient is NULL", i);
         if (!is_aligned(d.m, 4) || !is_aligned(d.v, 2))
@@ -223,7 +227,8 @@ int optim_group_create(const optim_tensor_desc_t* tensors, int32_t n, int32_t ki
     *out = nullptr;
     if (!tensors || n < 1) return set_error(OPTIM_EINVAL, "need n >= 1 tensors");
     if (kind != OPTIM_KIND_NADAM && kind != OPTIM_KIND_FACTORED && kind != OPTIM_KIND_NADAM_F24 &&
-        kind != OPTIM_KIND_ADAN && kind != OPTIM_KIND_ADAN_F24)
+        kind != OPTIM_KIND_ADAN && kind != OPTIM_KIND_ADAN_F24 && kind != OPTIM_KIND_ADAMW &&
+        kind != OPTIM_KIND_ADAMW_U8)
         return set_error(OPTIM_EINVAL, "unknown group kind %d", kind);
     for (int32_t i = 0; i < n; ++i) {
         int rc = validate_desc(tensors[i], i, kind);
@@ -238,6 +243,7 @@ int optim_group_create(const optim_tensor_desc_t* tensors, int32_t n, int32_t ki
     if (!rc) {
         std::vector<TensorRec> recs(n);
         std::vector<Chunk> chunks;
+        int64_t slot64 = 0;
         for (int32_t i = 0; i < n; ++i) {
             const optim_tensor_desc_t& d = tensors[i];
             TensorRec& r = recs[i];
@@ -247,8 +253,10 @@ int optim_group_create(const optim_tensor_desc_t* tensors, int32_t n, int32_t ki
             r.v = d.v;
             r.numel = d.numel;
             r.flags = (d.numel <= kSmall ? kFlagSmall : 0) | (d.res_u16 ? kFlagRes : 0);
-            r.pad = 0;
+            r.slot64 = (int32_t)slot64;
+            slot64 += (d.numel + 63) / 64;
         }
+        if (slot64 > INT32_MAX) rc = set_error(OPTIM_EINVAL, "group too large");
         if (kind != OPTIM_KIND_FACTORED) {
             // chunks of kChunkU16 elements for NAdam u16 groups, kChunk for f24 and Adan groups;
             // a group whose chunks would not give every SM a CTA (two for the
@@ -307,7 +315,8 @@ int optim_group_create(const optim_tensor_desc_t* tensors, int32_t n, int32_t ki
             numel += tensors[i].numel;
             res += tensors[i].res_u16 != nullptr && tensors[i].numel > 0;
         }
-        static const char* const names[] = {"nadam u16", "factored", "nadam f24", "adan fp32", "adan f24"};
+        static const char* const names[] = {"nadam u16", "factored", "nadam f24", "adan fp32", "adan f24", "adamw fp32",
+                                             "adamw u8"};
         std::fprintf(stderr, "lmopt: group of %d tensors, %lld elements, %s states, Kahan residual on %lld "
                      "tensors, device %d", n, (long long)numel, names[kind], (long long)res, g->device);
         if (kind != OPTIM_KIND_FACTORED)
@@ -508,6 +517,67 @@ int optim_step_adan(optim_group_t* g, const void* const* grads, int64_t step, co
     g->last_stream = s;
     if (g->offload) return offload_step_end(g, s);
     return OPTIM_OK;
+}
+
+int optim_step_adamw(optim_group_t* g, const void* const* grads, int64_t step, const optim_adamw_hparams_t* hp,
+                     const float* grad_scale, void* stream) {
+    if (!g || !hp) return set_error(OPTIM_EINVAL, "group or hparams is NULL");
+    if (g->kind != OPTIM_KIND_ADAMW && g->kind != OPTIM_KIND_ADAMW_U8)
+        return set_error(OPTIM_EINVAL, "not an ADAMW group");
+    if (step != g->last_step + 1)
+        return set_error(OPTIM_EINVAL, "step %lld but the group expects %lld", (long long)step,
+                         (long long)(g->last_step + 1));
+    if (!finite_nonneg(hp->lr) || !(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) ||
+        !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f) || !finite_nonneg(hp->eps) || !finite_nonneg(hp->weight_decay) ||
+        (hp->stochastic_rounding != 0 && hp->stochastic_rounding != 1))
+        return set_error(OPTIM_EINVAL, "invalid AdamW hyper-parameters");
+    if (grad_scale && !is_aligned(grad_scale, 4)) return set_error(OPTIM_EALIGN, "grad_scale not 4-byte aligned");
+    int rc = check_group_device(g);
+    if (!rc) rc = validate_grads(g, grads);
+    if (rc) return rc;
+    const double b1 = hp->beta1, b2 = hp->beta2, lr = hp->lr, td = (double)step;
+    AdamWScalars k{};
+    k.b1 = hp->beta1;
+    k.omb1 = (float)(1.0 - b1);
+    k.b2 = hp->beta2;
+    k.omb2 = (float)(1.0 - b2);
+    k.eps = hp->eps;
+    k.lr_wd = (float)(lr * (double)hp->weight_decay);
+    k.k1 = (float)(lr / (1.0 - std::pow(b1, td)));
+    k.k2 = (float)(1.0 / std::sqrt(1.0 - std::pow(b2, td)));
+    k.grad_scale = grad_scale;
+    k.sr = hp->stochastic_rounding;
+    k.step = step;
+    k.seed = hp->seed;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = upload_grads(g, grads, s);
+    if (rc) return rc;
+    const TensorRec* table = g->d_tensors;
+    if (g->offload) {
+        rc = offload_step_begin(g, s, &table);
+        if (rc) return rc;
+    }
+    NadamLaunch L{table, g->d_grads, g->d_scales, g->d_chunks, g->d_nonfinite, g->n_chunks_large,
+                  g->n_chunks_total, 0, nullptr, g->chunk};
+    rc = launch_adamw_step(L, k, g->kind == OPTIM_KIND_ADAMW_U8, s);
+    if (rc) return rc;
+    g->last_step = step;
+    g->last_stream = s;
+    if (g->offload) return offload_step_end(g, s);
+    return OPTIM_OK;
+}
+
+int optim_group_unpack_state(optim_group_t* g, float* m, float* v, void* stream) {
+    if (!g || !m || !v) return set_error(OPTIM_EINVAL, "group or output is NULL");
+    if (g->kind != OPTIM_KIND_ADAMW && g->kind != OPTIM_KIND_ADAMW_U8)
+        return set_error(OPTIM_EINVAL, "not an ADAMW group");
+    if (g->offload) return set_error(OPTIM_ESTATE, "the group's states are offloaded");
+    if (!is_aligned(m, 4) || !is_aligned(v, 4)) return set_error(OPTIM_EALIGN, "m/v not 4-byte aligned");
+    int rc = check_group_device(g);
+    if (rc) return rc;
+    NadamLaunch L{g->d_tensors, g->d_grads, g->d_scales, g->d_chunks, g->d_nonfinite, g->n_chunks_large,
+                  g->n_chunks_total, 0, nullptr, g->chunk};
+    return launch_adamw_unpack(L, g->kind == OPTIM_KIND_ADAMW_U8, m, v, static_cast<cudaStream_t>(stream));
 }
 
 int optim_step_factored(optim_group_t* g, const void* const* grads, int64_t step,

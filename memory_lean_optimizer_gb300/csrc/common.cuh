@@ -35,7 +35,7 @@ struct TensorRec {
     void* v;
     int64_t numel;
     int32_t flags;
-    int32_t pad;
+    int32_t slot64;   // AdamW groups: the tensor's start in the flat fp32 moment layout, in 64 elements
 };
 
 // Per-tensor scale record of the u16 codec, double-buffered by step parity p:

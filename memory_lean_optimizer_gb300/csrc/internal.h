@@ -77,4 +77,17 @@ struct AdanScalars {
 };
 int launch_adan_step(const NadamLaunch& L, const AdanScalars& k, cudaStream_t s);
 
+// Per-step scalars of the AdamW kernel (grad_scale: a device scalar, or NULL for 1).
+struct AdamWScalars {
+    float b1, omb1, b2, omb2, eps, lr_wd, k1, k2;
+    const float* grad_scale;
+    int32_t sr;
+    int64_t step;
+    uint64_t seed;
+};
+// u8: tensors above kSmall elements keep 8-bit states (OPTIM_KIND_ADAMW_U8).
+int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& k, bool u8, cudaStream_t s);
+// Every tensor's moments as fp32, into flat buffers laid out by TensorRec::slot64.
+int launch_adamw_unpack(const NadamLaunch& L, bool u8, float* m, float* v, cudaStream_t s);
+
 }  // namespace lmo

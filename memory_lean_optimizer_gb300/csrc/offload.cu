@@ -92,6 +92,10 @@ static void state_bytes(int32_t kind, const optim_tensor_desc_t& d, size_t& res,
     switch (kind) {
     case OPTIM_KIND_NADAM: m = v = (small ? 4 : 2) * n; break;
     case OPTIM_KIND_NADAM_F24: m = v = small ? 4 * n : f24; break;
+    case OPTIM_KIND_ADAMW: m = v = 4 * n; break;
+    case OPTIM_KIND_ADAMW_U8:
+        m = v = small ? 4 * n : round16(n) + 4 * ((n + OPTIM_U8_BLOCK - 1) / OPTIM_U8_BLOCK);
+        break;
     case OPTIM_KIND_ADAN: m = 12 * ((n + 3) & ~size_t(3)); v = 2 * n; break;
     default: /* ADAN_F24 */ m = small ? 12 * ((n + 3) & ~size_t(3)) : 3 * round16(f24); v = 2 * n; break;
     }
@@ -100,7 +104,7 @@ static void state_bytes(int32_t kind, const optim_tensor_desc_t& d, size_t& res,
 
 static bool offloadable(int32_t kind) {
     return kind == OPTIM_KIND_NADAM || kind == OPTIM_KIND_NADAM_F24 || kind == OPTIM_KIND_ADAN ||
-           kind == OPTIM_KIND_ADAN_F24;
+           kind == OPTIM_KIND_ADAN_F24 || kind == OPTIM_KIND_ADAMW || kind == OPTIM_KIND_ADAMW_U8;
 }
 
 // Slot (and image) layout of a group: per tensor residual, m, v, each at a 256-byte boundary.
@@ -139,7 +143,7 @@ static int upload_tables(optim_group* g, OffloadBinding* b) {
             r.v = base + b->off_v[i];
             r.numel = d.numel;
             r.flags = (d.numel <= kSmall ? kFlagSmall : 0) | (d.res_u16 ? kFlagRes : 0);
-            r.pad = 0;
+            r.slot64 = 0;   // nothing unpacks a staged state
         }
     }
     if (!b->d_tables && cudaMalloc(reinterpret_cast<void**>(&b->d_tables), tables.size() * sizeof(TensorRec)) != cudaSuccess) {
@@ -371,7 +375,7 @@ void offload_unbind(optim_group* g) {
 }
 
 static int check_attachable(optim_group* g) {
-    if (!offloadable(g->kind)) return set_error(OPTIM_EINVAL, "only NADAM, NADAM_F24, ADAN and ADAN_F24 groups can be offloaded");
+    if (!offloadable(g->kind)) return set_error(OPTIM_EINVAL, "FACTORED groups cannot be offloaded");
     if (g->offload) return set_error(OPTIM_ESTATE, "group already attached");
     if (g->pending) return set_error(OPTIM_ESTATE, "a NAdam step was begun and not ended");
     return OPTIM_OK;
@@ -446,7 +450,7 @@ int optim_group_attach_offload(optim_group_t* g, optim_offload_t* e) {
 
 int optim_offload_layout(optim_group_t* g, int64_t* offsets, int64_t* total_bytes) {
     if (!g || !total_bytes) return set_error(OPTIM_EINVAL, "group or total_bytes is NULL");
-    if (!offloadable(g->kind)) return set_error(OPTIM_EINVAL, "only NADAM, NADAM_F24, ADAN and ADAN_F24 groups can be offloaded");
+    if (!offloadable(g->kind)) return set_error(OPTIM_EINVAL, "FACTORED groups cannot be offloaded");
     OffloadBinding* b = plan_binding(g);
     *total_bytes = (int64_t)b->need;
     if (offsets) {

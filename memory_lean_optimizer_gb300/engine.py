@@ -147,7 +147,11 @@ def offload_slot_bytes(numels: Sequence[int], kahan: bool = True, kind: int = lm
             continue
         small = n <= SMALL
         f24 = (2 * n + 15) // 16 * 16 + n
-        if kind == lmopt.OPTIM_KIND_NADAM:
+        if kind == lmopt.OPTIM_KIND_ADAMW or (kind == lmopt.OPTIM_KIND_ADAMW_U8 and small):
+            m = v = 4 * n
+        elif kind == lmopt.OPTIM_KIND_ADAMW_U8:
+            m = v = u8_state_bytes(n)
+        elif kind == lmopt.OPTIM_KIND_NADAM:
             m = v = (4 if small else 2) * n
         elif kind == lmopt.OPTIM_KIND_NADAM_F24:
             m = v = 4 * n if small else f24
@@ -451,6 +455,101 @@ class AdanGroup(_Group):
                               stochastic_rounding=hp.get("stochastic_rounding", 0), seed=hp.get("seed", 0))
         lmopt.optim_step_adan(self.handle, self._grad_ptrs(grads), self.step_count + 1, h, _stream_ptr(stream))
         self.step_count += 1
+
+    def masters(self):
+        return [kahan_merge(w, r.to(w.device)) for w, r in zip(self.weights, self.res)]
+
+
+def u8_state_bytes(n: int) -> int:
+    """Bytes of one 8-bit moment buffer of n elements: codes, padding to 16, an fp32 constant per block."""
+    return (n + 15) // 16 * 16 + 4 * ((n + lmopt.U8_BLOCK - 1) // lmopt.U8_BLOCK)
+
+
+def u8_state_views(buf: torch.Tensor, n: int):
+    """(codes, block constants) of an 8-bit moment buffer: views of n bytes and of fp32 values."""
+    return buf[:n], buf[(n + 15) // 16 * 16:u8_state_bytes(n)].view(torch.float32)
+
+
+class AdamWGroup(_Group):
+    """AdamW state for a list of bf16 weights: moments in 8 bits with a scale for each 256 elements
+    (states="u8"; tensors of up to 4096 elements keep fp32) or in fp32 (states="fp32").  The moments of all
+    tensors are views of two allocations, `flat_m` and `flat_v`; fp32 ones lie as unpack_states lays
+    them out.  With `offload` (an OffloadEngine) residuals and moments live in pinned host memory."""
+
+    def __init__(self, weights: Sequence[torch.Tensor], residuals: Sequence[torch.Tensor] | None = None,
+                 kahan: bool = True, states: str = "u8", offload: OffloadEngine | None = None):
+        super().__init__()
+        assert states in ("u8", "fp32")
+        self.kind = lmopt.OPTIM_KIND_ADAMW_U8 if states == "u8" else lmopt.OPTIM_KIND_ADAMW
+        self.weights = list(weights)
+        for w in self.weights:
+            assert w.dtype == torch.bfloat16 and w.is_cuda and w.is_contiguous()
+        dev = self.weights[0].device
+        pinned = offload is not None
+        if residuals is None:
+            residuals = [_state_buffer(w.numel(), torch.int16, dev, pinned) if kahan else None for w in self.weights]
+        elif pinned:
+            residuals = [r.cpu().pin_memory() if r is not None else None for r in residuals]
+        self.res = list(residuals)
+        spans, total = [], 0                       # bytes of each tensor's buffer, on 256-byte boundaries
+        for w in self.weights:
+            n = w.numel()
+            packed = states == "u8" and n > SMALL
+            spans.append((total, u8_state_bytes(n) if packed else 4 * n, packed))
+            total += _round256(spans[-1][1])
+        flat = [torch.zeros(total, dtype=torch.uint8, pin_memory=True) if pinned else
+                torch.zeros(total, dtype=torch.uint8, device=dev) for _ in range(2)]
+        self.m, self.v = ([x[o:o + b] if packed else x[o:o + b].view(torch.float32) for o, b, packed in spans]
+                          for x in flat)
+        self.flat_m, self.flat_v = (x.view(torch.float32) if states == "fp32" else x for x in flat)
+        descs = [_desc(w, r, m, v, w.shape) for w, r, m, v in zip(self.weights, self.res, self.m, self.v)]
+        self.handle = lmopt.optim_group_create(descs, self.kind)
+        self.offload = offload
+        if offload is not None:
+            lmopt.optim_group_attach_offload(self.handle, offload.handle)
+
+    @classmethod
+    def from_masters(cls, masters: Sequence[torch.Tensor], stream=None, states: str = "u8",
+                     offload: OffloadEngine | None = None):
+        ws, rs = [], []
+        for x in masters:
+            hi, lo = kahan_split(x.contiguous(), stream=stream)
+            ws.append(hi)
+            rs.append(lo)
+        return cls(ws, rs, states=states, offload=offload)
+
+    def attach_host(self):
+        super().attach_host()
+        self.flat_m = self.flat_v = None           # the moments are views of the image now
+
+    def step(self, grads: Sequence[torch.Tensor], hp: dict, stream=None, grad_scale: torch.Tensor | None = None):
+        """grad_scale: a device tensor of one fp32 value multiplied into every gradient (a clip factor)."""
+        if grad_scale is not None:
+            assert grad_scale.dtype == torch.float32 and grad_scale.numel() == 1 and grad_scale.is_cuda
+        h = lmopt.AdamWHparams(lr=hp["lr"], beta1=hp.get("beta1", 0.9), beta2=hp.get("beta2", 0.999),
+                               eps=hp.get("eps", 1e-8), weight_decay=hp.get("weight_decay", 0.0),
+                               stochastic_rounding=hp.get("stochastic_rounding", 0), seed=hp.get("seed", 0))
+        lmopt.optim_step_adamw(self.handle, self._grad_ptrs(grads), self.step_count + 1, h,
+                               None if grad_scale is None else grad_scale.data_ptr(), _stream_ptr(stream))
+        self.step_count += 1
+
+    def set_step(self, step: int):
+        """Sets the counter of completed steps (resuming from a checkpoint)."""
+        lmopt.optim_group_set_step(self.handle, step, 1.0)
+        self.step_count = step
+
+    def unpacked_numel(self) -> int:
+        """Elements of each flat buffer of unpack_states: every tensor on a multiple of 64."""
+        return sum((w.numel() + 63) // 64 * 64 for w in self.weights)
+
+    def unpack_states(self, m: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+        """The moments as fp32, in two flat buffers (allocated zeroed if not given)."""
+        dev = self.weights[0].device
+        m, v = (torch.zeros(self.unpacked_numel(), dtype=torch.float32, device=dev) if x is None else x for x in (m, v))
+        for x in (m, v):
+            assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.numel() >= self.unpacked_numel()
+        lmopt.optim_group_unpack_state(self.handle, m.data_ptr(), v.data_ptr(), _stream_ptr(stream))
+        return m, v
 
     def masters(self):
         return [kahan_merge(w, r.to(w.device)) for w, r in zip(self.weights, self.res)]

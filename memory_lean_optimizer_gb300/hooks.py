@@ -119,6 +119,19 @@ def attach_fused_nadam(params: Sequence[torch.nn.Parameter], n_groups: int, hp: 
     return FusedStepper(params, n_groups, hp, make, on_step)
 
 
+def attach_fused_adamw(params: Sequence[torch.nn.Parameter], n_groups: int, hp: dict, on_step=None,
+                       states: str = "u8", offload: bool = False) -> FusedStepper:
+    """The same with AdamW groups (engine.AdamWGroup, moments in 8 bits or fp32)."""
+    from .engine import AdamWGroup
+
+    def make(ps):
+        g = AdamWGroup([p.data for p in ps], states=states)
+        if offload:
+            g.attach_host()
+        return g
+    return FusedStepper(params, n_groups, hp, make, on_step)
+
+
 def attach_fused_factored(params: Sequence[torch.nn.Parameter], n_groups: int, hp: dict, on_step=None) -> FusedStepper:
     from .engine import FactoredGroup
 

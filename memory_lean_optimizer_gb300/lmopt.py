@@ -27,7 +27,10 @@ OPTIM_KIND_FACTORED = 1
 OPTIM_KIND_NADAM_F24 = 2
 OPTIM_KIND_ADAN = 3
 OPTIM_KIND_ADAN_F24 = 4
+OPTIM_KIND_ADAMW = 5
+OPTIM_KIND_ADAMW_U8 = 6
 SMALL_NUMEL = 4096
+U8_BLOCK = 256
 
 ERROR_NAMES = {OPTIM_EINVAL: "EINVAL", OPTIM_ECUDA: "ECUDA", OPTIM_ENOMEM: "ENOMEM", OPTIM_EALIGN: "EALIGN",
                OPTIM_ETIMEOUT: "ETIMEOUT", OPTIM_ENONFINITE: "ENONFINITE", OPTIM_ESTATE: "ESTATE"}
@@ -43,7 +46,7 @@ EXPORTED = (
     "optim_offload_layout", "optim_step_nadam_begin", "optim_step_nadam_end", "optim_query_launches",
     "optim_prodigy_create", "optim_prodigy_destroy", "optim_prodigy_slice_len", "optim_group_attach_prodigy",
     "optim_prodigy_end_step", "optim_prodigy_get", "optim_prodigy_set", "optim_prodigy_reduce",
-    "optim_prodigy_finish",
+    "optim_prodigy_finish", "optim_step_adamw", "optim_group_unpack_state",
 )
 
 
@@ -70,6 +73,12 @@ class AdanHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("beta3", ctypes.c_float), ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("stochastic_rounding", ctypes.c_int32), ("reserved", ctypes.c_int32), ("seed", ctypes.c_uint64)]
+
+
+class AdamWHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("stochastic_rounding", ctypes.c_int32), ("seed", ctypes.c_uint64)]
 
 
 class FactoredHparams(ctypes.Structure):
@@ -102,6 +111,8 @@ def load(path: str = LIB_PATH):
             "optim_step_factored": [P, P, I64, ctypes.POINTER(FactoredHparams), P],
             "optim_step_adan": [P, P, I64, ctypes.POINTER(AdanHparams), P],
             "optim_step_factored_noalloc": [ctypes.POINTER(TensorDesc), P, I64, ctypes.POINTER(FactoredHparams), P],
+            "optim_step_adamw": [P, P, I64, ctypes.POINTER(AdamWHparams), P, P],
+            "optim_group_unpack_state": [P, P, P, P],
             "state_pack_u16": [P, P, P, I64, I32, P],
             "state_unpack_u16": [P, P, P, I64, I32, P],
             "optim_kahan_split": [P, P, P, I64, P],
@@ -200,6 +211,16 @@ def optim_step_factored_noalloc(desc: TensorDesc, grad_ptr: int, step: int, hp: 
 
 def optim_step_adan(handle: int, grad_ptrs, step: int, hp: AdanHparams, stream: int = 0) -> None:
     check(load().optim_step_adan(handle, _ptr_array(grad_ptrs), step, ctypes.byref(hp), stream))
+
+
+def optim_step_adamw(handle: int, grad_ptrs, step: int, hp: AdamWHparams, grad_scale: int | None = None,
+                     stream: int = 0) -> None:
+    """grad_scale: device pointer to one fp32 factor of every gradient, or None."""
+    check(load().optim_step_adamw(handle, _ptr_array(grad_ptrs), step, ctypes.byref(hp), grad_scale, stream))
+
+
+def optim_group_unpack_state(handle: int, m: int, v: int, stream: int = 0) -> None:
+    check(load().optim_group_unpack_state(handle, m, v, stream))
 
 
 def state_pack_u16(src: int, codes: int, scale: int, n: int, is_signed: bool, stream: int = 0) -> None:
