@@ -424,6 +424,31 @@ int optim_offload_sync(optim_offload_t* engine, uint64_t* bytes_h2d, uint64_t* b
  * kernel, on the stream that wave runs on).  NULL turns it off. */
 int optim_group_set_profile_event(optim_group_t* group, void* event);
 
+/* ---- the last layers of a language model's training step ------------------------------------
+ * Next to the step that consumes the gradients: the norm and the loss that produce the first of
+ * them, as memory-lean as the step (nothing of the size of the logits is ever kept).  These calls
+ * take plain buffers, no handle; scratch comes from the caller (the workspace calls say how much; it
+ * carries nothing from one call to the next and may be shared by calls ordered on one stream).
+ * Row strides (ld*) are in elements. */
+enum { OPTIM_BF16 = 0, OPTIM_F32 = 1 };
+
+/* Layer norm of `rows` rows of `dim` elements: y = (x - mu) r w + b with mu the row's mean and
+ * r = 1 / sqrt(variance + eps), the variance taken around the mean.  x and y have x_type, weight and
+ * bias (NULL: 0) have w_type; mean and rstd (fp32 [rows], NULL: not kept) are what backward needs.
+ * Sums are fp32 in a fixed order; outputs are rounded once.  y may be x.  One enqueued kernel. */
+int norm_layer_forward(const void* x, int64_t ldx, const void* weight, const void* bias, void* y,
+                       int64_t ldy, float* mean, float* rstd, int64_t rows, int64_t dim, float eps,
+                       int32_t x_type, int32_t w_type, void* stream);
+/* Scratch bytes of norm_layer_backward (when dweight or dbias is asked for). */
+int norm_layer_workspace(int64_t rows, int64_t dim, size_t* bytes);
+/* Gradients of the above: dx (x_type), dweight and dbias (w_type, summed over the rows), each NULL
+ * if not wanted.  With xh = (x - mu) r and a = dy w: dx = r (a - mean a - xh mean(a xh)), dw = sum dy xh,
+ * db = sum dy.  dx may be dy.  No rows: dweight and dbias are zero.  workspace: 16-byte aligned. */
+int norm_layer_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                        const float* mean, const float* rstd, void* dx, int64_t lddx, void* dweight,
+                        void* dbias, int64_t rows, int64_t dim, int32_t x_type, int32_t w_type,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 const char* optim_last_error(void);
 
 #ifdef __cplusplus

@@ -90,4 +90,38 @@ int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& k, bool u8, cuda
 // Every tensor's moments as fp32, into flat buffers laid out by TensorRec::slot64.
 int launch_adamw_unpack(const NadamLaunch& L, bool u8, float* m, float* v, cudaStream_t s);
 
+// Layer norm over rows of dim elements (row strides ld*, in elements; types by the two flags).
+struct NormForward {
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    const void* bias;      // or NULL
+    void* y;
+    int64_t ldy;
+    float* mean;           // or NULL
+    float* rstd;           // or NULL
+    int64_t rows, dim;
+    float eps;
+    bool x_bf16, w_bf16;   // else fp32
+};
+struct NormBackward {
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    void* dx;              // or NULL
+    int64_t lddx;
+    void* dweight;         // or NULL
+    void* dbias;           // or NULL
+    float* partial;        // norm_partial_bytes
+    int64_t rows, dim;
+    bool x_bf16, w_bf16;
+};
+size_t norm_partial_bytes(int64_t rows, int64_t dim);
+int launch_norm_forward(const NormForward& a, cudaStream_t s);
+int launch_norm_backward(const NormBackward& a, cudaStream_t s);
+
 }  // namespace lmo

@@ -1,0 +1,115 @@
+"""The last layers of a language model's training step over liblmopt.so: layer norm and the softmax
+cross entropy over the vocabulary, taken straight from the hidden states so that the logits are
+never kept.  With ``engine.AdamWGroup`` (or ``hooks.attach_fused_adamw``) they are the memory-lean
+tail of a training step: hidden states -> norm -> loss -> gradients -> optimizer.
+
+The ``*_forward`` / ``*_backward`` functions are the library calls on tensors; ``layer_norm`` is the
+same with autograd.  Each takes ``stream`` (a torch stream the caller has ordered after its inputs;
+default: the current one).  PyTorch supplies device memory, streams and the graph.
+"""
+from __future__ import annotations
+
+import functools
+
+import torch
+
+from . import lmopt
+from .engine import _stream_ptr
+
+_TYPES = {torch.bfloat16: lmopt.OPTIM_BF16, torch.float32: lmopt.OPTIM_F32}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _on_stream(fn):
+    """Runs a call's copies, allocations and kernels on its `stream` argument (None: the current stream)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t as a matrix of its last dimension's rows, whose elements lie next to each other: a view where the
+    strides allow one (rows may be apart), else a copy."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU")
+    if t.dim() < 1:
+        raise ValueError(f"{name} needs at least one dimension")
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
+    # a broadcast row (stride 0) is laid out too: the calls want rows at least their length apart
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        t = t.contiguous()
+    return t
+
+
+def _vector(t: torch.Tensor, n: int, like: torch.Tensor, dtype, name: str) -> torch.Tensor:
+    if t.shape != (n,) or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {n} values of {dtype} on {like.device}")
+    return t.contiguous()
+
+
+@_on_stream
+def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
+    """(y, mean, rstd) of the layer norm over x's last dimension; mean and rstd are fp32, one per row."""
+    xt, wt = _type(x, "x"), _type(weight, "weight")
+    m = _rows(x, "x")
+    rows, dim = m.shape
+    weight = _vector(weight, dim, x, weight.dtype, "weight")
+    if bias is not None:
+        bias = _vector(bias, dim, x, weight.dtype, "bias")
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+    lmopt.norm_layer_forward(m.data_ptr(), m.stride(0), weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                             y.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim, eps, xt, wt,
+                             _stream_ptr(None))
+    return y, mean, rstd
+
+
+@_on_stream
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor):
+    """(dx, dweight, dbias) from the gradient of y and what the forward call returned."""
+    xt, wt = _type(x, "x"), _type(weight, "weight")
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    m, g = _rows(x, "x"), _rows(dy, "dy")
+    rows, dim = m.shape
+    weight = _vector(weight, dim, x, weight.dtype, "weight")
+    mean, rstd = (_vector(t, rows, x, torch.float32, n) for t, n in ((mean, "mean"), (rstd, "rstd")))
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dweight, dbias = torch.empty_like(weight), torch.empty_like(weight)
+    nbytes = lmopt.norm_layer_workspace(rows, dim)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    lmopt.norm_layer_backward(g.data_ptr(), g.stride(0), m.data_ptr(), m.stride(0), weight.data_ptr(), mean.data_ptr(),
+                              rstd.data_ptr(), dx.data_ptr(), dim, dweight.data_ptr(), dbias.data_ptr(), rows, dim,
+                              xt, wt, work.data_ptr(), nbytes, _stream_ptr(None))
+    return dx, dweight, dbias
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.has_bias = bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd)
+        return dx, dweight, dbias if ctx.has_bias else None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
+    """Layer norm over x's last dimension, with autograd."""
+    return _LayerNorm.apply(x, weight, bias, eps)

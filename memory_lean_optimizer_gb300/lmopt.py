@@ -31,6 +31,8 @@ OPTIM_KIND_ADAMW = 5
 OPTIM_KIND_ADAMW_U8 = 6
 SMALL_NUMEL = 4096
 U8_BLOCK = 256
+OPTIM_BF16 = 0
+OPTIM_F32 = 1
 
 ERROR_NAMES = {OPTIM_EINVAL: "EINVAL", OPTIM_ECUDA: "ECUDA", OPTIM_ENOMEM: "ENOMEM", OPTIM_EALIGN: "EALIGN",
                OPTIM_ETIMEOUT: "ETIMEOUT", OPTIM_ENONFINITE: "ENONFINITE", OPTIM_ESTATE: "ESTATE"}
@@ -47,6 +49,7 @@ EXPORTED = (
     "optim_prodigy_create", "optim_prodigy_destroy", "optim_prodigy_slice_len", "optim_group_attach_prodigy",
     "optim_prodigy_end_step", "optim_prodigy_get", "optim_prodigy_set", "optim_prodigy_reduce",
     "optim_prodigy_finish", "optim_step_adamw", "optim_group_unpack_state",
+    "norm_layer_forward", "norm_layer_backward", "norm_layer_workspace",
 )
 
 
@@ -113,6 +116,9 @@ def load(path: str = LIB_PATH):
             "optim_step_factored_noalloc": [ctypes.POINTER(TensorDesc), P, I64, ctypes.POINTER(FactoredHparams), P],
             "optim_step_adamw": [P, P, I64, ctypes.POINTER(AdamWHparams), P, P],
             "optim_group_unpack_state": [P, P, P, P],
+            "norm_layer_forward": [P, I64, P, P, P, I64, P, P, I64, I64, F, I32, I32, P],
+            "norm_layer_workspace": [I64, I64, ctypes.POINTER(ctypes.c_size_t)],
+            "norm_layer_backward": [P, I64, P, I64, P, P, P, P, I64, P, P, I64, I64, I32, I32, P, ctypes.c_size_t, P],
             "state_pack_u16": [P, P, P, I64, I32, P],
             "state_unpack_u16": [P, P, P, I64, I32, P],
             "optim_kahan_split": [P, P, P, I64, P],
@@ -366,3 +372,23 @@ def optim_prodigy_get(pd: int):
 
 def optim_prodigy_set(pd: int, d: float, r: float) -> None:
     check(load().optim_prodigy_set(pd, d, r))
+
+
+# ------------------------------------------------------------- layer norm (plain buffers, no handle)
+def norm_layer_forward(x: int, ldx: int, weight: int, bias: int | None, y: int, ldy: int, mean: int | None,
+                       rstd: int | None, rows: int, dim: int, eps: float, x_type: int, w_type: int,
+                       stream: int = 0) -> None:
+    check(load().norm_layer_forward(x, ldx, weight, bias, y, ldy, mean, rstd, rows, dim, eps, x_type, w_type, stream))
+
+
+def norm_layer_workspace(rows: int, dim: int) -> int:
+    n = ctypes.c_size_t()
+    check(load().norm_layer_workspace(rows, dim, ctypes.byref(n)))
+    return n.value
+
+
+def norm_layer_backward(dy: int, lddy: int, x: int, ldx: int, weight: int, mean: int, rstd: int, dx: int | None,
+                        lddx: int, dweight: int | None, dbias: int | None, rows: int, dim: int, x_type: int,
+                        w_type: int, workspace: int | None, workspace_bytes: int, stream: int = 0) -> None:
+    check(load().norm_layer_backward(dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight, dbias, rows, dim,
+                                     x_type, w_type, workspace, workspace_bytes, stream))
