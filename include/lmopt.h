@@ -449,6 +449,33 @@ int norm_layer_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx
                         void* dbias, int64_t rows, int64_t dim, int32_t x_type, int32_t w_type,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* Softmax cross entropy of `rows` hidden states against a vocabulary, without the logits:
+ *   l = hidden weight^T,  lse_n = log sum_v exp l_nv,  loss_n = lse_n - l_{n, target_n}
+ * hidden [rows][dim] and weight [vocab][dim] are bf16 (the gradients of fp16 logits would underflow), the
+ * products and sums fp32, loss and lse fp32 [rows].  A row whose target is ignore_index costs
+ * no product and has loss 0 and lse 0, whatever its hidden state holds; a target outside the vocabulary
+ * makes its row's loss NaN.  Scratch is the gathered rows and 8 bytes per row and 256 words.
+ * weight, ldw and the sizes of loss_xent_workspace are those of the call it is for.  workspace: 256-byte
+ * aligned.  Matrices that are not 16-byte aligned with row strides of a multiple of 8 elements are
+ * copied on the way (hidden always is; weight by pieces of the vocabulary). */
+int loss_xent_workspace(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw,
+                        int32_t backward, size_t* bytes);
+int loss_xent_forward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                      const int64_t* target, int64_t rows, int64_t dim, int64_t vocab,
+                      int64_t ignore_index, float* loss, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+/* Gradients of sum_n grad_loss_n loss_n (grad_loss fp32 [rows]): with E_nv = (exp(l_nv - lse_n) -
+ * [v = target_n]) grad_loss_n, d_hidden = E weight and d_weight = E^T hidden, bf16, each NULL if
+ * not wanted.  lse is what forward gave.  The logits of a piece of the vocabulary at a time (256 MiB of
+ * E, 8192 words at least) are formed again, E is rounded to bf16 for the products, d_hidden is
+ * summed over the pieces in fp32.  Rows that are ignored or have grad_loss 0 are left out, whatever they hold; a target outside
+ * the vocabulary makes what it reaches NaN.  Deterministic.  No rows: d_weight is zero. */
+int loss_xent_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                       const int64_t* target, const float* lse, const float* grad_loss, int64_t rows,
+                       int64_t dim, int64_t vocab, int64_t ignore_index, void* d_hidden,
+                       int64_t lddh, void* d_weight, int64_t lddw, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 const char* optim_last_error(void);
 
 #ifdef __cplusplus

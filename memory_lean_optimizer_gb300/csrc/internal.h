@@ -124,4 +124,26 @@ size_t norm_partial_bytes(int64_t rows, int64_t dim);
 int launch_norm_forward(const NormForward& a, cudaStream_t s);
 int launch_norm_backward(const NormBackward& a, cudaStream_t s);
 
+// Softmax cross entropy of hidden [rows][dim] against weight [vocab][dim] (bf16, row strides ld*).
+struct XentCall {
+    const void* hidden;
+    int64_t ldh;
+    const void* weight;
+    int64_t ldw;
+    const int64_t* target;
+    int64_t rows, dim, vocab, ignore_index;
+    float* loss;              // forward: output
+    float* lse;               // forward: output; backward: input
+    const float* grad_loss;   // backward: factor of each row's loss
+    bool backward;
+    void* d_hidden;           // backward, or NULL
+    int64_t lddh;
+    void* d_weight;           // backward, or NULL
+    int64_t lddw;
+    void* workspace;
+    size_t workspace_bytes;
+};
+size_t xent_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw, bool backward);
+int launch_xent(const XentCall& c, cudaStream_t s);
+
 }  // namespace lmo

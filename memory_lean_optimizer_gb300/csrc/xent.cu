@@ -1,0 +1,828 @@
+// xent.cu -- softmax cross entropy over a vocabulary, straight from the hidden states: the logits
+// l = H W^T exist only as accumulators in tensor memory and, in the backward pass, as one piece of
+// the vocabulary's worth of bf16 gradients.
+//   lse_n = log sum_v exp l_nv,  loss_n = lse_n - l_{n,t_n}
+//   E_nv = (exp(l_nv - lse_n) - [v = t_n]) c_n,  dH = E W,  dW = E^T H
+// Rows whose target is ignore_index are gathered away first (k_xent_rows, k_xent_gather): they
+// cost no products, and whatever they hold, NaN included, meets no product.  The number of rows
+// left stays on the device; the product kernels read it and skip what lies past it.
+//
+// One product kernel (k_product) in four roles, which differ in their operands' major axes and in
+// what is done with the accumulators:
+//   kStats  H W^T   -> per row and 256 columns the maximum and the sum of exponentials, and l_{n,t_n}
+//   kGrad   H W^T   -> E (bf16), one piece of the vocabulary
+//   kHidden E W     -> dH, summed in fp32 over the pieces
+//   kWeight E^T H   -> dW of the piece, finished
+// E is the one rounding to fewer bits before an output: its entries meet bf16 operands in the tensor
+// cores, which want both operands of one type.
+#include <algorithm>
+
+#include "internal.h"
+#include "tensor.cuh"
+
+namespace lmo {
+namespace {
+
+constexpr int kTileN = 256;       // accumulator columns
+constexpr int kTileK = 64;        // one 128-byte swizzle row of bf16
+constexpr int kStages = 4;
+constexpr int kProductThreads = 256;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-7 finish
+constexpr uint32_t kTmemColumns = 512; // two accumulators of 256 columns
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum { kStats = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
+
+// First words of the workspace.
+struct XentHead {
+    int32_t rows;      // rows with a target
+    int32_t gave_up;   // a wait of a product kernel ran out: results are NaN
+};
+
+struct ProductArgs {
+    const XentHead* head;
+    int32_t m_tiles, n_tiles;   // tiles of the whole problem (rows: at most)
+    int32_t k_blocks;           // K in blocks of 64 (kWeight: at most; the rows decide)
+    int32_t splits;             // parts of K, each with its own output (kHidden)
+    int32_t b_off;              // where the piece starts in B's map: first row (kStats, kGrad) or K row (kHidden)
+    int32_t v_off;              // where it starts in the vocabulary
+    int32_t vocab, dim;
+    int64_t rows_pad;           // rows of the per-row arrays
+    const int32_t* target;      // per gathered row
+    const float* lse;           // kGrad
+    const float* scale;         // kGrad
+    float2* part;               // kStats: [tile][rows_pad]
+    float* target_logit;        // kStats
+    uint16_t* e;                // kGrad: [rows_pad][lde]
+    int64_t lde;
+    float* acc;                 // kHidden: [splits][rows_pad][ldacc]
+    int64_t ldacc;
+    int32_t first;              // kHidden: the first piece (store, not add)
+    uint16_t* dw;               // kWeight: dW, row b_off + m
+    int64_t lddw;
+    int32_t dw_aligned;         // kWeight: rows of dW start on 16 bytes
+    int32_t* gave_up;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Loads one K block of an operand: `rows` rows of M or N from `mn`, 64 of K from `k`.
+template <bool kMn, int kRows, int kCta>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int mn, int k, uint32_t bar) {
+    if (!kMn) {
+        tma_load<kCta>(dst, map, k, mn, bar);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRows / 64; ++i) tma_load<kCta>(dst + i * 8192, map, mn + 64 * i, k, bar);
+    }
+}
+
+// D = A B over tiles of 128 kCta x 256, one CTA (or a pair on one tile, kCta = 2) per SM, persistent.
+// Roles by warp: TMA into a ring of stages; tcgen05.mma from them into one of two accumulators;
+// four warps take the other accumulator out.  Every wait is bounded (mbar_wait); one that runs out
+// raises gave_up, each role stops at its next wait, copies and products in flight are waited
+// for (bounded too), and the kernel returns with tensor memory freed.
+template <int kMode, int kCta>
+__global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ CUtensorMap map_a,
+                                                                const __grid_constant__ CUtensorMap map_b,
+                                                                const ProductArgs p) {
+    constexpr bool kAMn = kMode == kWeight, kBMn = kMode == kHidden || kMode == kWeight;
+    constexpr int kRowsB = kTileN / kCta;
+    constexpr uint32_t kBytesA = 128 * kTileK * 2, kBytesB = kRowsB * kTileK * 2, kStage = kBytesA + kBytesB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * kStages + 4];
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up;
+    const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, done0 = empty0 + 8 * kStages, free0 = done0 + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCta == 2 ? cluster_rank() : 0u;
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(done0 + 8 * i, 1);
+            mbar_init(free0 + 8 * i, 4 * kCta);
+        }
+        mbar_init_fence();
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+    }
+    if (warp == 2) tmem_alloc<kCta>(smem_u32(&tmem_base), kTmemColumns);
+    tc_fence_before();
+    __syncthreads();
+    if (kCta == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    const int rows = p.head->rows;
+    const int m_tiles = kMode == kWeight ? p.m_tiles : (rows + 128 * kCta - 1) / (128 * kCta);
+    const int k_blocks = kMode == kWeight ? (rows + kTileK - 1) / kTileK : p.k_blocks;
+    const int per_split = (k_blocks + p.splits - 1) / p.splits;
+    const int units = m_tiles * p.n_tiles * p.splits;
+    const int first_unit = (int)blockIdx.x / kCta, stride = (int)gridDim.x / kCta;
+    // unit -> split, then tiles in strips of 8 columns, rows of tiles within a strip: the units in
+    // flight at one time share their rows of A and columns of B in L2
+    auto unit_tile = [&](int u, int& m, int& n, int& k0, int& k1, int& split) {
+        const int per = m_tiles * p.n_tiles;
+        split = u / per;
+        u -= split * per;
+        const int strip = u / (m_tiles * 8), in = u - strip * m_tiles * 8;
+        const int width = min(8, p.n_tiles - strip * 8);
+        m = in / width;
+        n = strip * 8 + in % width;
+        k0 = min(k_blocks, split * per_split);
+        k1 = min(k_blocks, k0 + per_split);
+    };
+
+    if (warp == 0 && elect_lane()) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        bool ok = true;
+        for (int u = first_unit; ok && u < units; u += stride) {
+            int m, n, k0, k1, split;
+            unit_tile(u, m, n, k0, k1, split);
+            const int am = (m * kCta + (int)rank) * 128, bn = n * kTileN + (int)rank * kRowsB;
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, &gave_up);
+                if (!ok) break;
+                const uint32_t bar = kCta == 2 ? cluster_addr(full0 + 8 * stage, 0) : full0 + 8 * stage;
+                if (rank == 0) mbar_expect_tx(full0 + 8 * stage, kStage * kCta);
+                const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
+                load_operand<kAMn, 128, kCta>(a, &map_a, am, kb * kTileK, bar);
+                if (kMode == kHidden)
+                    load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn, p.b_off + kb * kTileK, bar);
+                else
+                    load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn + (kMode == kWeight ? 0 : p.b_off), kb * kTileK, bar);
+                ++issued;
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+        }
+        // copies still in flight land before the CTA ends: on giving up nobody else waits for them
+        if (!ok && rank == 0) {
+            int never = 0;
+            for (int i = 0; i < min(issued, kStages); ++i) {
+                if (--stage < 0) stage = kStages - 1, phase ^= 1u;
+                mbar_wait(full0 + 8 * stage, phase, &never);
+                never = 0;
+            }
+        }
+    } else if (warp == 1 && rank == 0 && elect_lane()) {
+        constexpr uint32_t idesc = mma_desc(128 * kCta, kTileN, kAMn, kBMn);
+        constexpr uint32_t step_a = kAMn ? 2048u : 32u, step_b = kBMn ? 2048u : 32u;
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true;
+        for (int u = first_unit; ok && u < units; u += stride) {
+            int m, n, k0, k1, split;
+            unit_tile(u, m, n, k0, k1, split);
+            ok = mbar_wait(free0 + 8 * buf, buf_phase ^ 1u, &gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = mbar_wait(full0 + 8 * stage, phase, &gave_up);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
+#pragma unroll
+                for (int j = 0; j < kTileK / 16; ++j)
+                    mma_bf16<kCta>(tmem + buf * kTileN, operand_desc(a + j * step_a, 8192, 1024),
+                                   operand_desc(b + j * step_b, 8192, 1024), idesc, kb > k0 || j > 0);
+                mma_commit<kCta>(empty0 + 8 * stage);
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            mma_commit<kCta>(done0 + 8 * buf);
+            if (++buf == 2) buf = 0, buf_phase ^= 1u;
+        }
+        if (!ok) {   // products in flight end before tensor memory is freed
+            int never = 0;
+            mma_commit<kCta>(done0 + 8 * buf);
+            mbar_wait(done0 + 8 * buf, buf_phase, &never);
+        }
+    } else if (warp >= 4) {
+        const int w = warp & 3;
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        for (int u = first_unit; u < units; u += stride) {
+            int m, n, k0, k1, split;
+            unit_tile(u, m, n, k0, k1, split);
+            if (!mbar_wait(done0 + 8 * buf, buf_phase, &gave_up)) break;
+            tc_fence_after();
+            const int row = (m * kCta + (int)rank) * 128 + 32 * w + lane;   // this thread's row of the tile
+            const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(32 * w) << 16);
+            const bool none = k0 == k1;                                     // no products: the tile is zero
+            if (kMode == kStats) {
+                const int t = row < rows ? p.target[row] : -1;
+                const int v0 = p.v_off + n * kTileN;
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < kTileN; c += 32) {
+                    if (v0 + c >= p.vocab) break;
+                    uint32_t r[32];
+                    tmem_load32(acc + c, r);
+                    tmem_wait(r);
+                    float best = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x = v0 + c + j < p.vocab ? __uint_as_float(r[j]) : -INFINITY;
+                        r[j] = __float_as_uint(x);
+                        best = fmaxf(best, x);
+                        if (t == v0 + c + j) p.target_logit[row] = x;
+                    }
+                    const float up = fmaxf(top, best);
+                    const float base = up == -INFINITY ? 0.0f : up * kLog2e;
+                    sum *= exp2_approx(fmaf(top, kLog2e, -base));
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum += exp2_approx(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                    top = up;
+                }
+                if (row < rows) p.part[(int64_t)(v0 / kTileN) * p.rows_pad + row] = make_float2(top, sum);
+            } else if (kMode == kGrad) {
+                const bool live = row < rows;
+                const int t = live ? p.target[row] - p.v_off - n * kTileN : -1;   // the target's column of this tile
+                const float g = live ? p.scale[row] : 0.0f;
+                const float base = live ? p.lse[row] * kLog2e : 0.0f;
+                uint16_t* const out = p.e + row * p.lde + n * kTileN;
+#pragma unroll 1
+                for (int c = 0; c < kTileN; c += 32) {
+                    uint32_t r[32];
+                    tmem_load32(acc + c, r);
+                    tmem_wait(r);
+                    const int left = p.vocab - (p.v_off + n * kTileN + c);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float x = exp2_approx(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                        if (t == c + j) x -= 1.0f;
+                        // a row without weight is zero whatever it holds; so are columns past the vocabulary
+                        r[j] = __float_as_uint(live && j < left && g != 0.0f ? x * g : 0.0f);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 o;
+                        o.x = bf16_pair(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]));
+                        o.y = bf16_pair(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
+                        o.z = bf16_pair(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
+                        o.w = bf16_pair(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
+                        *reinterpret_cast<uint4*>(out + c + 8 * q) = o;
+                    }
+                }
+            } else if (kMode == kHidden) {
+                float* const out = p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + n * kTileN;
+#pragma unroll 1
+                for (int c = 0; c < kTileN; c += 32) {
+                    if (n * kTileN + c >= p.ldacc) break;
+                    uint32_t r[32];
+                    tmem_load32(acc + c, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        if (row >= rows) break;
+                        float4 x = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                        : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                                      __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+                        float4* const o = reinterpret_cast<float4*>(out + c) + q;
+                        if (!p.first) {   // one launch per piece, one thread per element: the order is the pieces'
+                            const float4 y = *o;
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        *o = x;
+                    }
+                    __syncwarp();
+                }
+            } else {
+                const int v = p.v_off + row;
+                uint16_t* const out = p.dw + v * p.lddw + n * kTileN;
+#pragma unroll 1
+                for (int c = 0; c < kTileN; c += 32) {
+                    const int left = p.dim - (n * kTileN + c);
+                    if (left <= 0) break;
+                    uint32_t r[32];
+                    tmem_load32(acc + c, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        r[j / 2] = none ? 0u : bf16_pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                    if (v >= p.vocab) {
+                    } else if (p.dw_aligned && left >= 32) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4*>(out + c + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left) out[c + j] = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
+            if (++buf == 2) buf = 0, buf_phase ^= 1u;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (kCta == 2) cluster_sync();
+    tc_fence_after();
+    if (threadIdx.x == 0 && gave_up) *p.gave_up = 1;
+    if (warp == 2) tmem_free<kCta>(tmem, kTmemColumns);
+}
+
+// ---- rows -------------------------------------------------------------------------------------
+struct RowArgs {
+    const int64_t* target;
+    int64_t rows, rows_pad, ignore;
+    int32_t vocab;
+    XentHead* head;
+    int32_t* row_of;        // gathered row -> row
+    int32_t* pos_of;        // row -> gathered row, or -1
+    int32_t* target_of;     // per gathered row; -1 for a target outside the vocabulary
+    float* loss;            // forward: outputs, zeroed for rows without a target
+    float* lse;
+    const float* lse_in;    // backward
+    const float* grad;
+    float* lse_of;
+    float* scale_of;
+};
+
+// Which rows have a target, in order: one CTA, eight rows a thread at a time (the prefix sum over all rows
+// is a few microseconds; the copy of the rows themselves follows on the whole GPU).
+__global__ void __launch_bounds__(1024) k_xent_rows(const RowArgs a) {
+    __shared__ int sums[33];
+    constexpr int kPer = 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int base = 0;
+    for (int64_t n0 = 0; n0 < a.rows; n0 += 1024 * kPer) {
+        const int64_t first = n0 + (int64_t)threadIdx.x * kPer;
+        int64_t t[kPer];
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            t[i] = first + i < a.rows ? a.target[first + i] : a.ignore;
+            if (a.grad && first + i < a.rows && a.grad[first + i] == 0.0f) t[i] = a.ignore;   // nothing to add
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) count += t[i] != a.ignore;
+        int run = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (lane >= o) run += up;
+        }
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        if (warp == 0) {
+            int s = sums[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, s, o);
+                if (lane >= o) s += up;
+            }
+            sums[lane] = s;
+        }
+        __syncthreads();
+        int pos = base + run - count + (warp ? sums[warp - 1] : 0);
+        base += sums[31];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t n = first + i;
+            if (n >= a.rows) break;
+            if (t[i] == a.ignore) {
+                a.pos_of[n] = -1;
+                if (a.loss) a.loss[n] = 0.0f;
+                if (a.lse) a.lse[n] = 0.0f;
+                continue;
+            }
+            const bool in = t[i] >= 0 && t[i] < a.vocab;
+            a.pos_of[n] = pos;
+            a.row_of[pos] = (int32_t)n;
+            a.target_of[pos] = in ? (int32_t)t[i] : -1;
+            if (a.grad) {
+                a.lse_of[pos] = a.lse_in[n];
+                a.scale_of[pos] = in ? a.grad[n] : __int_as_float(0x7FC00000);
+            }
+            ++pos;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        a.head->rows = base;
+        a.head->gave_up = 0;
+    }
+}
+
+// Rows of a matrix copied side by side: dst row c = src row row_of[c] (NULL: src row c), zero from
+// dim to ldd and, past the head's row count, up to the next `round` rows (NULL head: `rows` rows).
+// kVec: both sides in 16-byte vectors.
+template <bool kVec>
+__global__ void __launch_bounds__(kThreads) k_xent_gather(const XentHead* head, const int32_t* __restrict__ row_of,
+                                                          const uint16_t* __restrict__ src, int64_t lds,
+                                                          uint16_t* __restrict__ dst, int64_t ldd, int64_t rows, int dim,
+                                                          int round) {
+    const int64_t have = head ? head->rows : rows;
+    const int64_t limit = head ? min(rows, (have + round - 1) / round * round) : rows;
+    for (int64_t c = blockIdx.x; c < limit; c += gridDim.x) {
+        const uint16_t* s = src + (c < have && row_of ? (int64_t)row_of[c] : c) * lds;
+        uint16_t* d = dst + c * ldd;
+        if (kVec) {
+            for (int i = threadIdx.x * 8; i < ldd; i += kThreads * 8)
+                *reinterpret_cast<uint4*>(d + i) = c < have ? *reinterpret_cast<const uint4*>(s + i) : make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = threadIdx.x; i < ldd; i += kThreads) d[i] = c < have && i < dim ? s[i] : (uint16_t)0;
+        }
+    }
+}
+
+// Joins a row's (maximum, sum) pairs of all vocabulary tiles: 32 rows a CTA, 8 threads a row, a fixed order.
+__global__ void __launch_bounds__(kThreads) k_xent_loss(const XentHead* head, const float2* __restrict__ part, int tiles,
+                                                        int64_t rows_pad, const float* __restrict__ target_logit,
+                                                        const int32_t* __restrict__ target, const int32_t* __restrict__ row_of,
+                                                        float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ float2 red[8][32];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int rows = head->rows;
+    auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x);
+        if (m == -INFINITY) return make_float2(m, a.y + b.y);
+        return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+    };
+    for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
+        const int64_t c = r0 + tx;
+        float2 s = make_float2(-INFINITY, 0.0f);
+        if (c < rows)
+            for (int k = ty; k < tiles; k += 8) s = join(s, part[k * rows_pad + c]);
+        red[ty][tx] = s;
+        __syncthreads();
+        if (ty == 0 && c < rows) {
+            for (int k = 1; k < 8; ++k) s = join(s, red[k][tx]);
+            const bool bad = head->gave_up != 0;
+            const float l = bad ? __int_as_float(0x7FC00000) : s.x + logf(s.y);
+            const int64_t n = row_of[c];
+            lse[n] = l;
+            loss[n] = target[c] < 0 ? __int_as_float(0x7FC00000) : l - target_logit[c];
+        }
+        __syncthreads();
+    }
+}
+
+// dH rows from the fp32 sums of the gathered rows (the parts of a split K in order); zero where ignored.
+__global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, const int32_t* __restrict__ pos_of,
+                                                          const float* __restrict__ acc, int splits, int64_t rows_pad,
+                                                          int64_t ldacc, uint16_t* __restrict__ dh, int64_t lddh, int64_t rows,
+                                                          int dim, bool vec) {
+    const bool bad = head->gave_up != 0;
+    for (int64_t n = blockIdx.x; n < rows; n += gridDim.x) {
+        const int64_t c = pos_of[n];
+        for (int i = threadIdx.x * 4; i < dim; i += kThreads * 4) {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c >= 0) {
+                for (int s = 0; s < splits; ++s) {
+                    const float4 y = *reinterpret_cast<const float4*>(acc + ((int64_t)s * rows_pad + c) * ldacc + i);
+                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                }
+            }
+            if (bad) x.x = x.y = x.z = x.w = __int_as_float(0x7FC00000);
+            uint16_t* const o = dh + n * lddh + i;
+            const uint32_t lo = bf16_pair(x.x, x.y), hi = bf16_pair(x.z, x.w);
+            if (vec && i + 4 <= dim) {
+                *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+            } else {
+                const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+                for (int j = 0; j < 4 && i + j < dim; ++j) o[j] = h[j];
+            }
+        }
+    }
+}
+
+// ---- host -------------------------------------------------------------------------------------
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Sizes and workspace layout of a call.
+struct XentPlan {
+    int64_t rows, dim, vocab;
+    bool pack_w;                // the weight's rows cannot be addressed by TMA: copied piece by piece
+    int cta;                    // CTAs on a tile
+    int64_t rows_pad, ldh, piece, ldacc;
+    int splits;
+    size_t row_of, pos_of, target_of, lse_of, scale_of, target_logit, hc, wc, part, e, acc, bytes;
+};
+
+// How much of the vocabulary's gradient exists at a time (bytes of E, of a copied piece of the weight).
+constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int64_t kPieceMin = 8192;
+
+XentPlan plan_xent(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw, bool backward) {
+    XentPlan p{};
+    p.rows = rows;
+    p.dim = dim;
+    p.vocab = vocab;
+    p.pack_w = !is_aligned(weight, 16) || ldw % 8 != 0;
+    p.cta = 1;
+    p.rows_pad = up(std::max<int64_t>(rows, 1), 128 * p.cta);
+    p.ldh = up(dim, 8);
+    int64_t piece = up(vocab, kTileN);
+    if (backward) piece = std::min(piece, std::max(kPieceMin, kPieceBytes / (2 * p.rows_pad) / kTileN * kTileN));
+    if (p.pack_w) piece = std::min(piece, std::max(kPieceMin, kPieceBytes / (2 * p.ldh) / kTileN * kTileN));
+    p.piece = piece;
+    p.ldacc = up(dim, 32);
+    // few rows leave dH few tiles: K (the piece) is split until the tiles fill the GPU, 512 columns at least
+    const int64_t tiles = p.rows_pad / (128 * p.cta) * ((dim + kTileN - 1) / kTileN);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({152 / p.cta / tiles, p.piece / 512, 64}));
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at = (at + bytes + 255) & ~(size_t)255;
+        return o;
+    };
+    p.row_of = take(4 * p.rows_pad);
+    p.pos_of = take(4 * p.rows_pad);
+    p.target_of = take(4 * p.rows_pad);
+    p.hc = take(2 * p.rows_pad * p.ldh);
+    if (p.pack_w) p.wc = take(2 * p.piece * p.ldh);
+    if (backward) {
+        p.lse_of = take(4 * p.rows_pad);
+        p.scale_of = take(4 * p.rows_pad);
+        p.e = take(2 * p.rows_pad * p.piece);
+        p.acc = take(4 * p.splits * p.rows_pad * p.ldacc);
+    } else {
+        p.target_logit = take(4 * p.rows_pad);
+        p.part = take(8 * (up(vocab, kTileN) / kTileN) * p.rows_pad);
+    }
+    p.bytes = at;
+    return p;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult st;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+            st != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Map of a [rows][cols] bf16 matrix (row stride ld elements) for boxes of box_rows rows of 64 elements.
+int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return set_error(OPTIM_ECUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(OPTIM_ECUDA, "tensor map of a %lld x %lld matrix: error %d", (long long)rows, (long long)cols, (int)r);
+    return OPTIM_OK;
+}
+
+template <int kMode, int kCta>
+int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
+    constexpr int kSmem = 1024 + kStages * (128 + kTileN / kCta) * kTileK * 2;
+    auto kernel = k_product<kMode, kCta>;
+    static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    int rc = check_cuda(attr, "product kernel shared memory");
+    if (rc) return rc;
+    const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / kCta)) * kCta;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCta;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = kCta > 1 ? 1 : 0;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kernel, a, b, p), "product launch");
+}
+
+template <int kMode>
+int launch_product(const XentPlan& pl, const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
+    return pl.cta == 2 ? launch_product_t<kMode, 2>(a, b, p, s) : launch_product_t<kMode, 1>(a, b, p, s);
+}
+
+int gather(const XentHead* head, const int32_t* row_of, const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows,
+           int64_t dim, int round, cudaStream_t s) {
+    const bool vec = is_aligned(src, 16) && lds % 8 == 0 && dim % 8 == 0;
+    const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * 16);
+    if (vec)
+        k_xent_gather<true><<<grid, kThreads, 0, s>>>(head, row_of, static_cast<const uint16_t*>(src), lds,
+                                                      static_cast<uint16_t*>(dst), ldd, rows, (int)dim, round);
+    else
+        k_xent_gather<false><<<grid, kThreads, 0, s>>>(head, row_of, static_cast<const uint16_t*>(src), lds,
+                                                       static_cast<uint16_t*>(dst), ldd, rows, (int)dim, round);
+    return check_cuda(cudaGetLastError(), "row copy launch");
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw, bool backward) {
+    return plan_xent(rows, dim, vocab, weight, ldw, backward).bytes;
+}
+
+int launch_xent(const XentCall& c, cudaStream_t s) {
+    const XentPlan pl = plan_xent(c.rows, c.dim, c.vocab, c.weight, c.ldw, c.backward);
+    char* const ws = static_cast<char*>(c.workspace);
+    XentHead* const head = reinterpret_cast<XentHead*>(ws);
+    int32_t* const row_of = reinterpret_cast<int32_t*>(ws + pl.row_of);
+    int32_t* const pos_of = reinterpret_cast<int32_t*>(ws + pl.pos_of);
+    int32_t* const target_of = reinterpret_cast<int32_t*>(ws + pl.target_of);
+    RowArgs ra{c.target, c.rows, pl.rows_pad, c.ignore_index, (int32_t)c.vocab, head, row_of, pos_of, target_of,
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    if (c.backward) {
+        ra.lse_in = c.lse;
+        ra.grad = c.grad_loss;
+        ra.lse_of = reinterpret_cast<float*>(ws + pl.lse_of);
+        ra.scale_of = reinterpret_cast<float*>(ws + pl.scale_of);
+    } else {
+        ra.loss = c.loss;
+        ra.lse = c.lse;
+    }
+    k_xent_rows<<<1, 1024, 0, s>>>(ra);
+    int rc = check_cuda(cudaGetLastError(), "row scan launch");
+    uint16_t* const hc = reinterpret_cast<uint16_t*>(ws + pl.hc);
+    if (!rc) rc = gather(head, row_of, c.hidden, c.ldh, hc, pl.ldh, pl.rows_pad, c.dim, 128 * pl.cta, s);
+
+    ProductArgs p{};
+    p.head = head;
+    p.gave_up = &head->gave_up;
+    p.vocab = (int32_t)c.vocab;
+    p.dim = (int32_t)c.dim;
+    p.rows_pad = pl.rows_pad;
+    p.target = target_of;
+    p.lse = ra.lse_of;
+    p.scale = ra.scale_of;
+    p.part = reinterpret_cast<float2*>(ws + pl.part);
+    p.target_logit = reinterpret_cast<float*>(ws + pl.target_logit);
+    p.e = reinterpret_cast<uint16_t*>(ws + pl.e);
+    p.lde = pl.piece;
+    p.acc = reinterpret_cast<float*>(ws + pl.acc);
+    p.ldacc = pl.ldacc;
+    p.dw = static_cast<uint16_t*>(c.d_weight);
+    p.lddw = c.lddw;
+    p.dw_aligned = is_aligned(c.d_weight, 16) && c.lddw % 8 == 0;
+    const int row_tiles = (int)(pl.rows_pad / (128 * pl.cta)), dim_tiles = (int)((c.dim + kTileN - 1) / kTileN);
+    const int dim_blocks = (int)((c.dim + kTileK - 1) / kTileK);
+    const int box_b = kTileN / pl.cta;
+    CUtensorMap h_k{}, h_mn{}, e_k{}, e_mn{}, w_k{}, w_mn{};
+    if (!rc) rc = make_map(&h_k, hc, pl.rows_pad, c.dim, pl.ldh, 128);
+    if (!rc && c.backward) {
+        rc = make_map(&h_mn, hc, pl.rows_pad, c.dim, pl.ldh, 64);
+        if (!rc) rc = make_map(&e_k, p.e, pl.rows_pad, pl.piece, pl.piece, 128);
+        if (!rc) rc = make_map(&e_mn, p.e, pl.rows_pad, pl.piece, pl.piece, 64);
+    }
+    for (int64_t v0 = 0; !rc && v0 < c.vocab; v0 += pl.piece) {
+        const int64_t width = std::min(pl.piece, c.vocab - v0);
+        const uint16_t* w = static_cast<const uint16_t*>(c.weight);
+        if (pl.pack_w) {   // the piece's rows, side by side; the maps then start at the piece
+            uint16_t* const wc = reinterpret_cast<uint16_t*>(ws + pl.wc);
+            rc = gather(nullptr, nullptr, w + v0 * c.ldw, c.ldw, wc, pl.ldh, width, c.dim, 1, s);
+            w = wc;
+        }
+        if (!rc && (pl.pack_w || v0 == 0)) {
+            const int64_t map_rows = pl.pack_w ? width : c.vocab, ld = pl.pack_w ? pl.ldh : c.ldw;
+            rc = make_map(&w_k, w, map_rows, c.dim, ld, box_b);
+            if (!rc && c.backward) rc = make_map(&w_mn, w, map_rows, c.dim, ld, 64);
+        }
+        if (rc) break;
+        ProductArgs q = p;
+        q.splits = 1;
+        q.b_off = pl.pack_w ? 0 : (int32_t)v0;
+        q.v_off = (int32_t)v0;
+        q.m_tiles = row_tiles;
+        q.n_tiles = (int)((width + kTileN - 1) / kTileN);
+        q.k_blocks = dim_blocks;
+        if (!c.backward) {
+            rc = launch_product<kStats>(pl, h_k, w_k, q, s);
+            continue;
+        }
+        rc = launch_product<kGrad>(pl, h_k, w_k, q, s);
+        if (!rc && c.d_hidden) {
+            ProductArgs h = q;
+            h.n_tiles = dim_tiles;
+            h.k_blocks = (int)((width + kTileK - 1) / kTileK);
+            h.splits = pl.splits;
+            h.first = v0 == 0;
+            rc = launch_product<kHidden>(pl, e_k, w_mn, h, s);
+        }
+        if (!rc && c.d_weight) {
+            ProductArgs d = q;
+            d.m_tiles = (int)((width + 128 * pl.cta - 1) / (128 * pl.cta));
+            d.n_tiles = dim_tiles;
+            rc = launch_product<kWeight>(pl, e_mn, h_mn, d, s);
+        }
+    }
+    if (rc) return rc;
+    if (!c.backward) {
+        k_xent_loss<<<(unsigned)std::min<int64_t>((c.rows + 31) / 32, sm_count() * 8), kThreads, 0, s>>>(
+            head, p.part, (int)((c.vocab + kTileN - 1) / kTileN), pl.rows_pad, p.target_logit, target_of, row_of, c.loss, c.lse);
+        return check_cuda(cudaGetLastError(), "loss launch");
+    }
+    if (!c.d_hidden || c.rows == 0) return OPTIM_OK;
+    const bool vec = is_aligned(c.d_hidden, 8) && c.lddh % 4 == 0;
+    k_xent_hidden<<<(unsigned)std::min<int64_t>(c.rows, sm_count() * 16), kThreads, 0, s>>>(
+        head, pos_of, p.acc, pl.splits, pl.rows_pad, pl.ldacc, static_cast<uint16_t*>(c.d_hidden), c.lddh, c.rows, (int)c.dim, vec);
+    return check_cuda(cudaGetLastError(), "hidden gradient launch");
+}
+
+}  // namespace lmo
+
+using namespace lmo;
+
+static int check_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, const char* name) {
+    if (rows == 0) return OPTIM_OK;
+    if (!p) return set_error(OPTIM_EINVAL, "%s is NULL", name);
+    if (rows > 1 && ld < cols) return set_error(OPTIM_EINVAL, "%s: row stride %lld below %lld", name, (long long)ld, (long long)cols);
+    if (!is_aligned(p, 2)) return set_error(OPTIM_EALIGN, "%s not 2-byte aligned", name);
+    return OPTIM_OK;
+}
+static int check_array(const void* p, size_t align, const char* name) {
+    if (!p) return set_error(OPTIM_EINVAL, "%s is NULL", name);
+    if (!is_aligned(p, align)) return set_error(OPTIM_EALIGN, "%s not %zu-byte aligned", name, align);
+    return OPTIM_OK;
+}
+
+static int check_xent(XentCall& c) {
+    if (c.rows < 0 || c.dim < 1 || c.vocab < 1) return set_error(OPTIM_EINVAL, "need rows >= 0, dim >= 1 and vocab >= 1");
+    // tile counts and row numbers are 32-bit in the kernels
+    if (c.rows > (1 << 28) || c.dim > (1 << 24) || c.vocab > (1 << 28))
+        return set_error(OPTIM_EINVAL, "rows and vocab must be at most 2^28, dim at most 2^24");
+    int rc = check_matrix(c.hidden, c.ldh, c.rows, c.dim, "hidden");
+    if (!rc) rc = check_matrix(c.weight, c.ldw, c.vocab, c.dim, "weight");
+    if (!rc && c.rows > 0) rc = check_array(c.target, 8, "target");
+    if (!rc && c.rows > 0) rc = check_array(c.lse, 4, "lse");
+    if (rc) return rc;
+    if (c.vocab == 1) c.ldw = std::max(c.ldw, c.dim);   // the stride of a single row is anything
+    const size_t need = xent_workspace_bytes(c.rows, c.dim, c.vocab, c.weight, c.ldw, c.backward);
+    rc = check_array(c.workspace, 256, "workspace");
+    if (!rc && c.workspace_bytes < need)
+        rc = set_error(OPTIM_EINVAL, "workspace of %zu bytes, %zu needed", c.workspace_bytes, need);
+    return rc;
+}
+
+extern "C" {
+
+int loss_xent_workspace(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw, int32_t backward,
+                        size_t* bytes) {
+    if (!bytes) return set_error(OPTIM_EINVAL, "bytes is NULL");
+    if (rows < 0 || dim < 1 || vocab < 1 || rows > (1 << 28) || dim > (1 << 24) || vocab > (1 << 28))
+        return set_error(OPTIM_EINVAL, "need 0 <= rows <= 2^28, 1 <= dim <= 2^24 and 1 <= vocab <= 2^28");
+    *bytes = xent_workspace_bytes(rows, dim, vocab, weight, vocab == 1 ? std::max(ldw, dim) : ldw, backward != 0);
+    return OPTIM_OK;
+}
+
+int loss_xent_forward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, const int64_t* target, int64_t rows,
+                      int64_t dim, int64_t vocab, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    XentCall c{};
+    c.hidden = hidden, c.ldh = ldh, c.weight = weight, c.ldw = ldw, c.target = target;
+    c.rows = rows, c.dim = dim, c.vocab = vocab, c.ignore_index = ignore_index;
+    c.loss = loss, c.lse = lse, c.workspace = workspace, c.workspace_bytes = workspace_bytes;
+    int rc = check_xent(c);
+    if (!rc && rows > 0) rc = check_array(loss, 4, "loss");
+    if (rc || rows == 0) return rc;
+    return launch_xent(c, static_cast<cudaStream_t>(stream));
+}
+
+int loss_xent_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, const int64_t* target,
+                       const float* lse, const float* grad_loss, int64_t rows, int64_t dim, int64_t vocab,
+                       int64_t ignore_index, void* d_hidden, int64_t lddh, void* d_weight, int64_t lddw, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    XentCall c{};
+    c.hidden = hidden, c.ldh = ldh, c.weight = weight, c.ldw = ldw, c.target = target;
+    c.rows = rows, c.dim = dim, c.vocab = vocab, c.ignore_index = ignore_index;
+    c.lse = const_cast<float*>(lse), c.grad_loss = grad_loss, c.backward = true;
+    c.d_hidden = d_hidden, c.lddh = lddh, c.d_weight = d_weight, c.lddw = lddw;
+    c.workspace = workspace, c.workspace_bytes = workspace_bytes;
+    int rc = check_xent(c);
+    if (!rc && rows > 0) rc = check_array(grad_loss, 4, "grad_loss");
+    if (!rc && d_hidden) rc = check_matrix(d_hidden, lddh, rows, dim, "d_hidden");
+    if (!rc && d_weight) rc = check_matrix(d_weight, lddw, vocab, dim, "d_weight");
+    if (rc || (!d_hidden && !d_weight)) return rc;
+    return launch_xent(c, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -3,8 +3,8 @@ cross entropy over the vocabulary, taken straight from the hidden states so that
 never kept.  With ``engine.AdamWGroup`` (or ``hooks.attach_fused_adamw``) they are the memory-lean
 tail of a training step: hidden states -> norm -> loss -> gradients -> optimizer.
 
-The ``*_forward`` / ``*_backward`` functions are the library calls on tensors; ``layer_norm`` is the
-same with autograd.  Each takes ``stream`` (a torch stream the caller has ordered after its inputs;
+The ``*_forward`` / ``*_backward`` functions are the library calls on tensors; ``layer_norm`` and
+``linear_cross_entropy`` are the same with autograd.  Each takes ``stream`` (a torch stream the caller has ordered after its inputs;
 default: the current one).  PyTorch supplies device memory, streams and the graph.
 """
 from __future__ import annotations
@@ -113,3 +113,75 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
     """Layer norm over x's last dimension, with autograd."""
     return _LayerNorm.apply(x, weight, bias, eps)
+
+
+def _xent_args(hidden, weight, target):
+    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError(f"hidden and weight must be bfloat16, not {hidden.dtype} and {weight.dtype}")
+    h, w = _rows(hidden, "hidden"), weight
+    if w.dim() != 2 or w.shape[1] != h.shape[1]:
+        raise ValueError(f"weight must be [vocabulary, {h.shape[1]}], not {list(weight.shape)}")
+    w = _rows(w, "weight")
+    if target.dtype != torch.int64 or target.shape != hidden.shape[:-1] or target.device != hidden.device:
+        raise ValueError(f"target must be int64 {list(hidden.shape[:-1])} on {hidden.device}")
+    return h, w, target.reshape(-1).contiguous()
+
+
+@_on_stream
+def xent_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, ignore_index: int = -100):
+    """(loss, lse), fp32, one per row of hidden: the softmax cross entropy of hidden @ weight.T against target,
+    and the log of the softmax's denominator.  Rows with ignore_index have 0 for both."""
+    h, w, t = _xent_args(hidden, weight, target)
+    (rows, dim), vocab = h.shape, w.shape[0]
+    loss, lse = (torch.empty(target.shape, dtype=torch.float32, device=h.device) for _ in range(2))
+    nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), False)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
+    lmopt.loss_xent_forward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), rows, dim, vocab,
+                            ignore_index, loss.data_ptr(), lse.data_ptr(), work.data_ptr(), nbytes, _stream_ptr(None))
+    return loss, lse
+
+
+@_on_stream
+def xent_backward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                  grad_loss: torch.Tensor, ignore_index: int = -100, need_hidden: bool = True, need_weight: bool = True):
+    """(d_hidden, d_weight) of sum(grad_loss * loss), bf16; None for one that is not needed."""
+    h, w, t = _xent_args(hidden, weight, target)
+    (rows, dim), vocab = h.shape, w.shape[0]
+    lse, g = (_vector(x.reshape(-1), rows, h, torch.float32, n) for x, n in ((lse, "lse"), (grad_loss, "grad_loss")))
+    dh = torch.empty(hidden.shape, dtype=torch.bfloat16, device=h.device) if need_hidden else None
+    dw = torch.empty(weight.shape, dtype=torch.bfloat16, device=h.device) if need_weight else None
+    nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), True)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
+    lmopt.loss_xent_backward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), lse.data_ptr(),
+                             g.data_ptr(), rows, dim, vocab, ignore_index, None if dh is None else dh.data_ptr(), dim,
+                             None if dw is None else dw.data_ptr(), dim, work.data_ptr(), nbytes, _stream_ptr(None))
+    return dh, dw
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, target, ignore_index):
+        loss, lse = xent_forward(hidden, weight, target, ignore_index)
+        ctx.save_for_backward(hidden, weight, target, lse)
+        ctx.ignore_index = ignore_index
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        hidden, weight, target, lse = ctx.saved_tensors
+        dh, dw = xent_backward(hidden, weight, target, lse, grad, ctx.ignore_index, ctx.needs_input_grad[0],
+                               ctx.needs_input_grad[1])
+        return dh, dw, None, None
+
+
+def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                         reduction: str = "mean"):
+    """Softmax cross entropy of hidden @ weight.T against target, with autograd and without the logits.
+    reduction: "mean" over the rows that are not ignored (0 if there are none), "sum" or "none"."""
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError(f"unknown reduction {reduction!r}")
+    loss = _LinearCrossEntropy.apply(hidden, weight, target, ignore_index)
+    if reduction == "none":
+        return loss
+    total = loss.sum()
+    return total if reduction == "sum" else total / (target != ignore_index).sum().clamp(min=1)

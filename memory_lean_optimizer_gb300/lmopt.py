@@ -50,6 +50,7 @@ EXPORTED = (
     "optim_prodigy_end_step", "optim_prodigy_get", "optim_prodigy_set", "optim_prodigy_reduce",
     "optim_prodigy_finish", "optim_step_adamw", "optim_group_unpack_state",
     "norm_layer_forward", "norm_layer_backward", "norm_layer_workspace",
+    "loss_xent_forward", "loss_xent_backward", "loss_xent_workspace",
 )
 
 
@@ -119,6 +120,9 @@ def load(path: str = LIB_PATH):
             "norm_layer_forward": [P, I64, P, P, P, I64, P, P, I64, I64, F, I32, I32, P],
             "norm_layer_workspace": [I64, I64, ctypes.POINTER(ctypes.c_size_t)],
             "norm_layer_backward": [P, I64, P, I64, P, P, P, P, I64, P, P, I64, I64, I32, I32, P, ctypes.c_size_t, P],
+            "loss_xent_workspace": [I64, I64, I64, P, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
+            "loss_xent_forward": [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, ctypes.c_size_t, P],
+            "loss_xent_backward": [P, I64, P, I64, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, ctypes.c_size_t, P],
             "state_pack_u16": [P, P, P, I64, I32, P],
             "state_unpack_u16": [P, P, P, I64, I32, P],
             "optim_kahan_split": [P, P, P, I64, P],
@@ -392,3 +396,24 @@ def norm_layer_backward(dy: int, lddy: int, x: int, ldx: int, weight: int, mean:
                         w_type: int, workspace: int | None, workspace_bytes: int, stream: int = 0) -> None:
     check(load().norm_layer_backward(dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, dweight, dbias, rows, dim,
                                      x_type, w_type, workspace, workspace_bytes, stream))
+
+
+# ------------------------------------------- softmax cross entropy over a vocabulary (plain buffers)
+def loss_xent_workspace(rows: int, dim: int, vocab: int, weight: int, ldw: int, backward: bool) -> int:
+    n = ctypes.c_size_t()
+    check(load().loss_xent_workspace(rows, dim, vocab, weight, ldw, int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def loss_xent_forward(hidden: int, ldh: int, weight: int, ldw: int, target: int, rows: int, dim: int, vocab: int,
+                      ignore_index: int, loss: int, lse: int, workspace: int, workspace_bytes: int,
+                      stream: int = 0) -> None:
+    check(load().loss_xent_forward(hidden, ldh, weight, ldw, target, rows, dim, vocab, ignore_index, loss, lse,
+                                   workspace, workspace_bytes, stream))
+
+
+def loss_xent_backward(hidden: int, ldh: int, weight: int, ldw: int, target: int, lse: int, grad_loss: int, rows: int,
+                       dim: int, vocab: int, ignore_index: int, d_hidden: int | None, lddh: int,
+                       d_weight: int | None, lddw: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    check(load().loss_xent_backward(hidden, ldh, weight, ldw, target, lse, grad_loss, rows, dim, vocab, ignore_index,
+                                    d_hidden, lddh, d_weight, lddw, workspace, workspace_bytes, stream))
