@@ -25,8 +25,11 @@ namespace {
 
 constexpr int kTileN = 256;       // accumulator columns
 constexpr int kTileK = 64;        // one 128-byte swizzle row of bf16
-constexpr int kStages = 4;
-constexpr int kProductThreads = 256;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-7 finish
+constexpr int kChunk = 8;         // kStats: blocks of K to an accumulator (512)
+constexpr int kProductThreads = 384;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-11 finish
+// Stages of 48 KiB (one CTA: 128 rows of A, 256 of B) or 32 KiB (a pair: 128 and 128 each).
+__host__ __device__ constexpr int product_stages(int cta) { return cta == 1 ? 4 : 6; }
+constexpr int kFinishBytes = 8 * 32 * 34 * 2;   // a 32 x 32 bf16 block for each finishing warp, rows 68 bytes apart
 constexpr uint32_t kTmemColumns = 512; // two accumulators of 256 columns
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -36,6 +39,7 @@ enum { kStats = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
 struct XentHead {
     int32_t rows;      // rows with a target
     int32_t gave_up;   // a wait of a product kernel ran out: results are NaN
+    float grad_scale;  // backward: the largest |grad_loss|; E is in units of it (see k_xent_rows)
 };
 
 struct ProductArgs {
@@ -87,14 +91,20 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 
 // D = A B over tiles of 128 kCta x 256, one CTA (or a pair on one tile, kCta = 2) per SM, persistent.
 // Roles by warp: TMA into a ring of stages; tcgen05.mma from them into one of two accumulators;
-// four warps take the other accumulator out.  Every wait is bounded (mbar_wait); one that runs out
-// raises gave_up, each role stops at its next wait, copies and products in flight are waited
-// for (bounded too), and the kernel returns with tensor memory freed.
+// eight warps -- a warp per 32 rows and half of the columns -- take the other accumulator out.
+// The tensor cores cut the accumulator's low bits at each addition, always towards zero: over a
+// long K that is a drift, ten times the error of rounded fp32 sums at K = 4096, which the loss
+// would show.  kStats therefore starts a new accumulator every kChunk blocks of K and adds them up
+// in registers, rounded to nearest; the other accumulator hides the extra reading of tensor memory.
+// Every wait is bounded (mbar_wait); one that runs out raises gave_up, each role stops at its next
+// wait, copies and products in flight are waited for (bounded too), and the kernel returns with
+// tensor memory freed.
 template <int kMode, int kCta>
 __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ CUtensorMap map_a,
                                                                 const __grid_constant__ CUtensorMap map_b,
                                                                 const ProductArgs p) {
     constexpr bool kAMn = kMode == kWeight, kBMn = kMode == kHidden || kMode == kWeight;
+    constexpr int kStages = product_stages(kCta);
     constexpr int kRowsB = kTileN / kCta;
     constexpr uint32_t kBytesA = 128 * kTileK * 2, kBytesB = kRowsB * kTileK * 2, kStage = kBytesA + kBytesB;
     extern __shared__ uint8_t smem_raw[];
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(done0 + 8 * i, 1);
-            mbar_init(free0 + 8 * i, 4 * kCta);
+            mbar_init(free0 + 8 * i, 8 * kCta);
         }
         mbar_init_fence();
         tma_prefetch_map(&map_a);
@@ -145,129 +155,167 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         k0 = min(k_blocks, split * per_split);
         k1 = min(k_blocks, k0 + per_split);
     };
+    // blocks of K that share an accumulator
+    auto chunk_end = [&](int k, int k1) { return kMode == kStats ? min(k1, k + kChunk) : k1; };
 
-    if (warp == 0 && elect_lane()) {
-        int stage = 0;
-        uint32_t phase = 0;
-        int issued = 0;
-        bool ok = true;
-        for (int u = first_unit; ok && u < units; u += stride) {
-            int m, n, k0, k1, split;
-            unit_tile(u, m, n, k0, k1, split);
-            const int am = (m * kCta + (int)rank) * 128, bn = n * kTileN + (int)rank * kRowsB;
-            for (int kb = k0; kb < k1; ++kb) {
-                ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, &gave_up);
-                if (!ok) break;
-                const uint32_t bar = kCta == 2 ? cluster_addr(full0 + 8 * stage, 0) : full0 + 8 * stage;
-                if (rank == 0) mbar_expect_tx(full0 + 8 * stage, kStage * kCta);
-                const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
-                load_operand<kAMn, 128, kCta>(a, &map_a, am, kb * kTileK, bar);
-                if (kMode == kHidden)
-                    load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn, p.b_off + kb * kTileK, bar);
-                else
-                    load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn + (kMode == kWeight ? 0 : p.b_off), kb * kTileK, bar);
-                ++issued;
-                if (++stage == kStages) stage = 0, phase ^= 1u;
+    if (warp < 4) {
+        if (kMode == kStats) regs_down<40>();
+        if (warp == 0 && elect_lane()) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            bool ok = true;
+            for (int u = first_unit; ok && u < units; u += stride) {
+                int m, n, k0, k1, split;
+                unit_tile(u, m, n, k0, k1, split);
+                const int am = (m * kCta + (int)rank) * 128, bn = n * kTileN + (int)rank * kRowsB;
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, &gave_up);
+                    if (!ok) break;
+                    const uint32_t bar = kCta == 2 ? cluster_addr(full0 + 8 * stage, 0) : full0 + 8 * stage;
+                    if (rank == 0) mbar_expect_tx(full0 + 8 * stage, kStage * kCta);
+                    const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
+                    load_operand<kAMn, 128, kCta>(a, &map_a, am, kb * kTileK, bar);
+                    if (kMode == kHidden)
+                        load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn, p.b_off + kb * kTileK, bar);
+                    else
+                        load_operand<kBMn, kRowsB, kCta>(b, &map_b, bn + (kMode == kWeight ? 0 : p.b_off), kb * kTileK, bar);
+                    ++issued;
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
             }
-        }
-        // copies still in flight land before the CTA ends: on giving up nobody else waits for them
-        if (!ok && rank == 0) {
-            int never = 0;
-            for (int i = 0; i < min(issued, kStages); ++i) {
-                if (--stage < 0) stage = kStages - 1, phase ^= 1u;
-                mbar_wait(full0 + 8 * stage, phase, &never);
-                never = 0;
+            // copies still in flight land before the CTA ends: on giving up nobody else waits for them
+            if (!ok && rank == 0) {
+                for (int i = 0; i < min(issued, kStages); ++i) {
+                    if (--stage < 0) stage = kStages - 1, phase ^= 1u;
+                    int never = 0;
+                    mbar_wait(full0 + 8 * stage, phase, &never);
+                }
             }
-        }
-    } else if (warp == 1 && rank == 0 && elect_lane()) {
-        constexpr uint32_t idesc = mma_desc(128 * kCta, kTileN, kAMn, kBMn);
-        constexpr uint32_t step_a = kAMn ? 2048u : 32u, step_b = kBMn ? 2048u : 32u;
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, buf_phase = 0;
-        bool ok = true;
-        for (int u = first_unit; ok && u < units; u += stride) {
-            int m, n, k0, k1, split;
-            unit_tile(u, m, n, k0, k1, split);
-            ok = mbar_wait(free0 + 8 * buf, buf_phase ^ 1u, &gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            for (int kb = k0; kb < k1; ++kb) {
-                ok = mbar_wait(full0 + 8 * stage, phase, &gave_up);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
+        } else if (warp == 1 && rank == 0 && elect_lane()) {
+            constexpr uint32_t idesc = mma_desc(128 * kCta, kTileN, kAMn, kBMn);
+            constexpr uint32_t step_a = kAMn ? 2048u : 32u, step_b = kBMn ? 2048u : 32u;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            bool ok = true;
+            for (int u = first_unit; ok && u < units; u += stride) {
+                int m, n, k0, k1, split;
+                unit_tile(u, m, n, k0, k1, split);
+                int k = k0;
+                do {
+                    const int end = chunk_end(k, k1);
+                    ok = mbar_wait(free0 + 8 * buf, buf_phase ^ 1u, &gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int kb = k; kb < end; ++kb) {
+                        ok = mbar_wait(full0 + 8 * stage, phase, &gave_up);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
 #pragma unroll
-                for (int j = 0; j < kTileK / 16; ++j)
-                    mma_bf16<kCta>(tmem + buf * kTileN, operand_desc(a + j * step_a, 8192, 1024),
-                                   operand_desc(b + j * step_b, 8192, 1024), idesc, kb > k0 || j > 0);
-                mma_commit<kCta>(empty0 + 8 * stage);
-                if (++stage == kStages) stage = 0, phase ^= 1u;
+                        for (int j = 0; j < kTileK / 16; ++j)
+                            mma_bf16<kCta>(tmem + buf * kTileN, operand_desc(a + j * step_a, 8192, 1024),
+                                           operand_desc(b + j * step_b, 8192, 1024), idesc, kb > k || j > 0);
+                        mma_commit<kCta>(empty0 + 8 * stage);
+                        if (++stage == kStages) stage = 0, phase ^= 1u;
+                    }
+                    if (!ok) break;
+                    mma_commit<kCta>(done0 + 8 * buf);
+                    if (++buf == 2) buf = 0, buf_phase ^= 1u;
+                    k = end;
+                } while (k < k1);
             }
-            if (!ok) break;
-            mma_commit<kCta>(done0 + 8 * buf);
-            if (++buf == 2) buf = 0, buf_phase ^= 1u;
+            if (!ok) {   // products in flight end before tensor memory is freed
+                int never = 0;
+                mma_commit<kCta>(done0 + 8 * buf);
+                mbar_wait(done0 + 8 * buf, buf_phase, &never);
+            }
         }
-        if (!ok) {   // products in flight end before tensor memory is freed
-            int never = 0;
-            mma_commit<kCta>(done0 + 8 * buf);
-            mbar_wait(done0 + 8 * buf, buf_phase, &never);
-        }
-    } else if (warp >= 4) {
-        const int w = warp & 3;
+        __syncwarp();
+    } else {
+        if (kMode == kStats) regs_up<232>();
+        const int w = warp & 3, half = (warp >> 2) - 1;   // tensor memory lanes are dealt to warps by warp % 4
+        const uint32_t lanes = (uint32_t)(32 * w) << 16;
+        uint16_t(*const stage)[34] = reinterpret_cast<uint16_t(*)[34]>(
+            smem_raw + (tiles - smem_u32(smem_raw)) + kStages * kStage + (warp - 4) * 32 * 34 * 2);
         int buf = 0;
         uint32_t buf_phase = 0;
-        for (int u = first_unit; u < units; u += stride) {
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
+            if (++buf == 2) buf = 0, buf_phase ^= 1u;
+        };
+        bool ok = true;
+        for (int u = first_unit; ok && u < units; u += stride) {
             int m, n, k0, k1, split;
             unit_tile(u, m, n, k0, k1, split);
-            if (!mbar_wait(done0 + 8 * buf, buf_phase, &gave_up)) break;
-            tc_fence_after();
             const int row = (m * kCta + (int)rank) * 128 + 32 * w + lane;   // this thread's row of the tile
-            const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(32 * w) << 16);
-            const bool none = k0 == k1;                                     // no products: the tile is zero
+            const int c0 = n * kTileN + half * 128;                         // and its first of 128 columns
             if (kMode == kStats) {
-                const int t = row < rows ? p.target[row] : -1;
-                const int v0 = p.v_off + n * kTileN;
-                float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < kTileN; c += 32) {
-                    if (v0 + c >= p.vocab) break;
-                    uint32_t r[32];
-                    tmem_load32(acc + c, r);
-                    tmem_wait(r);
-                    float best = -INFINITY;
+                float x[128];
+                int k = k0;
+                do {
+                    ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float x = v0 + c + j < p.vocab ? __uint_as_float(r[j]) : -INFINITY;
-                        r[j] = __float_as_uint(x);
-                        best = fmaxf(best, x);
-                        if (t == v0 + c + j) p.target_logit[row] = x;
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t r[32];
+                        tmem_load32(tmem + buf * kTileN + lanes + half * 128 + c, r);
+                        tmem_wait(r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[c + j] = k == k0 ? __uint_as_float(r[j]) : x[c + j] + __uint_as_float(r[j]);
                     }
-                    const float up = fmaxf(top, best);
-                    const float base = up == -INFINITY ? 0.0f : up * kLog2e;
-                    sum *= exp2_approx(fmaf(top, kLog2e, -base));
+                    release();
+                    k = chunk_end(k, k1);
+                } while (k < k1);
+                if (!ok) break;
+                const int left = p.vocab - (p.v_off + c0);
+                const int t = row < rows ? p.target[row] - (p.v_off + c0) : -1;
+                float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) sum += exp2_approx(fmaf(__uint_as_float(r[j]), kLog2e, -base));
-                    top = up;
+                for (int j = 0; j < 128; ++j) {
+                    if (j >= left) x[j] = -INFINITY;
+                    top = fmaxf(top, x[j]);
                 }
-                if (row < rows) p.part[(int64_t)(v0 / kTileN) * p.rows_pad + row] = make_float2(top, sum);
-            } else if (kMode == kGrad) {
+                const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+                if (t >= 0 && t < 128) {
+                    float l = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 128; ++j) l = t == j ? x[j] : l;
+                    p.target_logit[row] = l;
+                }
+#pragma unroll
+                for (int j = 0; j < 128; ++j) sum += exp2_approx(fmaf(x[j], kLog2e, -base));
+                if (row < rows) p.part[(int64_t)((p.v_off + c0) / 128) * p.rows_pad + row] = make_float2(top, sum);
+                __syncwarp();
+                continue;
+            }
+            ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kTileN + lanes + half * 128;
+            const bool none = k0 == k1;                                     // no products: the tile is zero
+            if (kMode == kGrad) {
                 const bool live = row < rows;
-                const int t = live ? p.target[row] - p.v_off - n * kTileN : -1;   // the target's column of this tile
+                const int t = live ? p.target[row] - p.v_off - c0 : -1;     // the target's column of this half
                 const float g = live ? p.scale[row] : 0.0f;
                 const float base = live ? p.lse[row] * kLog2e : 0.0f;
-                uint16_t* const out = p.e + row * p.lde + n * kTileN;
+                uint16_t* const out = p.e + row * p.lde + c0;
 #pragma unroll 1
-                for (int c = 0; c < kTileN; c += 32) {
+                for (int c = 0; c < 128; c += 32) {
                     uint32_t r[32];
                     tmem_load32(acc + c, r);
                     tmem_wait(r);
-                    const int left = p.vocab - (p.v_off + n * kTileN + c);
+                    const int left = p.vocab - (p.v_off + c0 + c);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         float x = exp2_approx(fmaf(__uint_as_float(r[j]), kLog2e, -base));
                         if (t == c + j) x -= 1.0f;
-                        // a row without weight is zero whatever it holds; so are columns past the vocabulary
-                        r[j] = __float_as_uint(live && j < left && g != 0.0f ? x * g : 0.0f);
+                        // rows past the last and columns past the vocabulary are zero, whatever was multiplied
+                        r[j] = __float_as_uint(live && j < left ? x * g : 0.0f);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -280,10 +328,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     }
                 }
             } else if (kMode == kHidden) {
-                float* const out = p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + n * kTileN;
+                float* const out = p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + c0;
 #pragma unroll 1
-                for (int c = 0; c < kTileN; c += 32) {
-                    if (n * kTileN + c >= p.ldacc) break;
+                for (int c = 0; c < 128; c += 32) {
+                    if (c0 + c >= p.ldacc) break;
                     uint32_t r[32];
                     tmem_load32(acc + c, r);
                     tmem_wait(r);
@@ -304,37 +352,39 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 }
             } else {
                 const int v = p.v_off + row;
-                uint16_t* const out = p.dw + v * p.lddw + n * kTileN;
+                const float g = p.head->grad_scale;
+                uint16_t* const out = p.dw + v * p.lddw + c0;
 #pragma unroll 1
-                for (int c = 0; c < kTileN; c += 32) {
-                    const int left = p.dim - (n * kTileN + c);
+                for (int c = 0; c < 128; c += 32) {
+                    const int left = p.dim - (c0 + c);
                     if (left <= 0) break;
                     uint32_t r[32];
                     tmem_load32(acc + c, r);
                     tmem_wait(r);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
-                        r[j / 2] = none ? 0u : bf16_pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                    if (v >= p.vocab) {
-                    } else if (p.dw_aligned && left >= 32) {
+                        r[j / 2] = none ? 0u : bf16_pair(__uint_as_float(r[j]) * g, __uint_as_float(r[j + 1]) * g);
+                    if (p.dw_aligned && left >= 32) {
+                        if (v < p.vocab) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4*>(out + c + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-                    } else {
+                            for (int q = 0; q < 4; ++q)
+                                *reinterpret_cast<uint4*>(out + c + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                        }
+                    } else {   // through shared memory, so that a warp writes 32 neighbours of one row at a time
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < left) out[c + j] = (uint16_t)(r[j / 2] >> (16 * (j & 1)));
+                        for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(&stage[lane][2 * j]) = r[j];
+                        __syncwarp();
+                        uint16_t* const o = p.dw + (int64_t)(v - lane) * p.lddw + c0 + c + lane;
+                        const int have = min(32, p.vocab - (v - lane));
+                        if (lane < left)
+                            for (int i = 0; i < have; ++i) o[i * p.lddw] = stage[i][lane];
                     }
                     __syncwarp();
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
-            if (++buf == 2) buf = 0, buf_phase ^= 1u;
+            release();
         }
     }
-    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (kCta == 2) cluster_sync();
@@ -362,11 +412,28 @@ struct RowArgs {
 
 // Which rows have a target, in order: one CTA, eight rows a thread at a time (the prefix sum over all rows
 // is a few microseconds; the copy of the rows themselves follows on the whole GPU).
+// Backward: E is formed in units of the largest |grad_loss|, which the gradients are multiplied with in
+// fp32 at the end.  With equal grad_loss (a mean) E's largest entries are then near -1, where bf16
+// is at its finest, whatever the mean's divisor rounds to.
 __global__ void __launch_bounds__(1024) k_xent_rows(const RowArgs a) {
     __shared__ int sums[33];
+    __shared__ uint32_t largest;
     constexpr int kPer = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int base = 0;
+    float unit = 1.0f;
+    if (a.grad) {
+        if (threadIdx.x == 0) largest = 0u;
+        __syncthreads();
+        uint32_t top = 0u;   // of the finite ones: a NaN or an infinity stays in its row
+        for (int64_t n = threadIdx.x; n < a.rows; n += 1024) {
+            const uint32_t b = __float_as_uint(a.grad[n]) & 0x7FFFFFFFu;
+            if (a.target[n] != a.ignore && b < 0x7F800000u) top = max(top, b);
+        }
+        atomicMax(&largest, __reduce_max_sync(0xFFFFFFFFu, top));
+        __syncthreads();
+        if (largest != 0u) unit = __uint_as_float(largest);
+    }
     for (int64_t n0 = 0; n0 < a.rows; n0 += 1024 * kPer) {
         const int64_t first = n0 + (int64_t)threadIdx.x * kPer;
         int64_t t[kPer];
@@ -414,7 +481,7 @@ __global__ void __launch_bounds__(1024) k_xent_rows(const RowArgs a) {
             a.target_of[pos] = in ? (int32_t)t[i] : -1;
             if (a.grad) {
                 a.lse_of[pos] = a.lse_in[n];
-                a.scale_of[pos] = in ? a.grad[n] : __int_as_float(0x7FC00000);
+                a.scale_of[pos] = in ? a.grad[n] / unit : __int_as_float(0x7FC00000);
             }
             ++pos;
         }
@@ -423,6 +490,7 @@ __global__ void __launch_bounds__(1024) k_xent_rows(const RowArgs a) {
     if (threadIdx.x == 0) {
         a.head->rows = base;
         a.head->gave_up = 0;
+        a.head->grad_scale = unit;
     }
 }
 
@@ -496,7 +564,8 @@ __global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, 
                     x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                 }
             }
-            if (bad) x.x = x.y = x.z = x.w = __int_as_float(0x7FC00000);
+            const float g = bad ? __int_as_float(0x7FC00000) : head->grad_scale;
+            x = make_float4(x.x * g, x.y * g, x.z * g, x.w * g);
             uint16_t* const o = dh + n * lddh + i;
             const uint32_t lo = bf16_pair(x.x, x.y), hi = bf16_pair(x.z, x.w);
             if (vec && i + 4 <= dim) {
@@ -532,7 +601,7 @@ XentPlan plan_xent(int64_t rows, int64_t dim, int64_t vocab, const void* weight,
     p.dim = dim;
     p.vocab = vocab;
     p.pack_w = !is_aligned(weight, 16) || ldw % 8 != 0;
-    p.cta = 1;
+    p.cta = rows > 128 ? 2 : 1;
     p.rows_pad = up(std::max<int64_t>(rows, 1), 128 * p.cta);
     p.ldh = up(dim, 8);
     int64_t piece = up(vocab, kTileN);
@@ -561,7 +630,7 @@ XentPlan plan_xent(int64_t rows, int64_t dim, int64_t vocab, const void* weight,
         p.acc = take(4 * p.splits * p.rows_pad * p.ldacc);
     } else {
         p.target_logit = take(4 * p.rows_pad);
-        p.part = take(8 * (up(vocab, kTileN) / kTileN) * p.rows_pad);
+        p.part = take(8 * (up(vocab, kTileN) / 128) * p.rows_pad);
     }
     p.bytes = at;
     return p;
@@ -598,7 +667,7 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
 
 template <int kMode, int kCta>
 int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
-    constexpr int kSmem = 1024 + kStages * (128 + kTileN / kCta) * kTileK * 2;
+    constexpr int kSmem = 1024 + product_stages(kCta) * (128 + kTileN / kCta) * kTileK * 2 + kFinishBytes;
     auto kernel = k_product<kMode, kCta>;
     static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int rc = check_cuda(attr, "product kernel shared memory");
@@ -738,7 +807,7 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     if (rc) return rc;
     if (!c.backward) {
         k_xent_loss<<<(unsigned)std::min<int64_t>((c.rows + 31) / 32, sm_count() * 8), kThreads, 0, s>>>(
-            head, p.part, (int)((c.vocab + kTileN - 1) / kTileN), pl.rows_pad, p.target_logit, target_of, row_of, c.loss, c.lse);
+            head, p.part, (int)((c.vocab + 127) / 128), pl.rows_pad, p.target_logit, target_of, row_of, c.loss, c.lse);
         return check_cuda(cudaGetLastError(), "loss launch");
     }
     if (!c.d_hidden || c.rows == 0) return OPTIM_OK;
