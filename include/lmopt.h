@@ -469,7 +469,9 @@ int loss_xent_forward(const void* hidden, int64_t ldh, const void* weight, int64
  * not wanted.  lse is what forward gave.  The logits of a piece of the vocabulary at a time (256 MiB of
  * E, 8192 words at least) are formed again, E is rounded to bf16 for the products, d_hidden is
  * summed over the pieces in fp32.  Rows that are ignored or have grad_loss 0 are left out, whatever they hold; a target outside
- * the vocabulary makes what it reaches NaN.  Deterministic.  No rows: d_weight is zero. */
+ * the vocabulary makes what it reaches NaN.  Deterministic.  No rows: d_weight is zero.  The waits
+ * inside the product kernels of both calls are bounded (seconds); should one run out, the results
+ * it held up are NaN. */
 int loss_xent_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
                        const int64_t* target, const float* lse, const float* grad_loss, int64_t rows,
                        int64_t dim, int64_t vocab, int64_t ignore_index, void* d_hidden,

@@ -3,8 +3,7 @@
 // the vocabulary's worth of bf16 gradients.
 //   lse_n = log sum_v exp l_nv,  loss_n = lse_n - l_{n,t_n}
 //   E_nv = (exp(l_nv - lse_n) - [v = t_n]) c_n,  dH = E W,  dW = E^T H
-// Rows whose target is ignore_index are gathered away first (k_xent_rows, k_xent_gather): they
-// cost no products, and whatever they hold, NaN included, meets no product.  The number of rows
+// Rows whose target is ignore_index are gathered away first (k_xent_rows): they cost no products, and whatever they hold, NaN included, meets no product.  The number of rows
 // left stays on the device; the product kernels read it and skip what lies past it.
 //
 // One product kernel (k_product) in four roles, which differ in their operands' major axes and in
@@ -38,7 +37,7 @@ enum { kStats = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
 // First words of the workspace.
 struct XentHead {
     int32_t rows;      // rows with a target
-    int32_t gave_up;   // a wait of a product kernel ran out: results are NaN
+    int32_t pad;
     float grad_scale;  // backward: the largest |grad_loss|; E is in units of it (see k_xent_rows)
 };
 
@@ -60,12 +59,23 @@ struct ProductArgs {
     int64_t lde;
     float* acc;                 // kHidden: [splits][rows_pad][ldacc]
     int64_t ldacc;
-    int32_t first;              // kHidden: the first piece (store, not add)
+    int32_t first, last;        // kHidden: the first piece (nothing to add to), the last (dH itself; not if K is split)
+    uint16_t* dh;               // kHidden
+    int64_t lddh;
+    int32_t dh_aligned;         // rows of dH start on 16 bytes
+    const int32_t* row_of;      // kHidden: gathered row -> row of dH
     uint16_t* dw;               // kWeight: dW, row b_off + m
     int64_t lddw;
     int32_t dw_aligned;         // kWeight: rows of dW start on 16 bytes
-    int32_t* gave_up;
 };
+
+// Programmatic dependent launch: the kernels of a call start while their predecessor drains and wait
+// here before they read what it wrote; each lets its own successor start only after that wait, so
+// what lies further back is complete too.
+__device__ __forceinline__ void pdl_sync() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -96,9 +106,9 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 // long K that is a drift, ten times the error of rounded fp32 sums at K = 4096, which the loss
 // would show.  kStats therefore starts a new accumulator every kChunk blocks of K and adds them up
 // in registers, rounded to nearest; the other accumulator hides the extra reading of tensor memory.
-// Every wait is bounded (mbar_wait); one that runs out raises gave_up, each role stops at its next
-// wait, copies and products in flight are waited for (bounded too), and the kernel returns with
-// tensor memory freed.
+// Every wait is bounded (mbar_wait); one that runs out raises gave_up and each role stops at its next
+// wait: copies and products in flight are waited for (bounded too), the finishing warps write NaN
+// for what they did not get, and the kernel returns with tensor memory freed.
 template <int kMode, int kCta>
 __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ CUtensorMap map_a,
                                                                 const __grid_constant__ CUtensorMap map_b,
@@ -135,6 +145,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     if (kCta == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_sync();
 
     const int rows = p.head->rows;
     const int m_tiles = kMode == kWeight ? p.m_tiles : (rows + 128 * kCta - 1) / (128 * kCta);
@@ -240,14 +251,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
             smem_raw + (tiles - smem_u32(smem_raw)) + kStages * kStage + (warp - 4) * 32 * 34 * 2);
         int buf = 0;
         uint32_t buf_phase = 0;
+        bool ok = true;
+        auto wait_done = [&]() {
+            if (ok) ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+        };
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
+            if (lane == 0 && ok) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
             if (++buf == 2) buf = 0, buf_phase ^= 1u;
         };
-        bool ok = true;
-        for (int u = first_unit; ok && u < units; u += stride) {
+        constexpr float kNan = __builtin_nanf("");
+        for (int u = first_unit; u < units; u += stride) {
             int m, n, k0, k1, split;
             unit_tile(u, m, n, k0, k1, split);
             const int row = (m * kCta + (int)rank) * 128 + 32 * w + lane;   // this thread's row of the tile
@@ -256,9 +273,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 float x[128];
                 int k = k0;
                 do {
-                    ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
-                    if (!ok) break;
-                    tc_fence_after();
+                    wait_done();
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         uint32_t r[32];
@@ -271,7 +286,6 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     release();
                     k = chunk_end(k, k1);
                 } while (k < k1);
-                if (!ok) break;
                 const int left = p.vocab - (p.v_off + c0);
                 const int t = row < rows ? p.target[row] - (p.v_off + c0) : -1;
                 float top = -INFINITY, sum = 0.0f;
@@ -289,19 +303,17 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 }
 #pragma unroll
                 for (int j = 0; j < 128; ++j) sum += exp2_approx(fmaf(x[j], kLog2e, -base));
-                if (row < rows) p.part[(int64_t)((p.v_off + c0) / 128) * p.rows_pad + row] = make_float2(top, sum);
+                if (row < rows) p.part[(int64_t)((p.v_off + c0) / 128) * p.rows_pad + row] = make_float2(top, ok ? sum : kNan);
                 __syncwarp();
                 continue;
             }
-            ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
-            if (!ok) break;
-            tc_fence_after();
+            wait_done();
             const uint32_t acc = tmem + buf * kTileN + lanes + half * 128;
             const bool none = k0 == k1;                                     // no products: the tile is zero
             if (kMode == kGrad) {
                 const bool live = row < rows;
                 const int t = live ? p.target[row] - p.v_off - c0 : -1;     // the target's column of this half
-                const float g = live ? p.scale[row] : 0.0f;
+                const float g = live ? (ok ? p.scale[row] : kNan) : 0.0f;
                 const float base = live ? p.lse[row] * kLog2e : 0.0f;
                 uint16_t* const out = p.e + row * p.lde + c0;
 #pragma unroll 1
@@ -327,60 +339,69 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                         *reinterpret_cast<uint4*>(out + c + 8 * q) = o;
                     }
                 }
-            } else if (kMode == kHidden) {
-                float* const out = p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + c0;
+                release();
+                continue;
+            }
+            // the gradients: this thread's row of dH or dW (-1: none), or of the fp32 sums
+            const bool sums = kMode == kHidden && !p.last;
+            const int64_t out_row = kMode == kHidden ? (row < rows && p.last ? p.row_of[row] : -1)
+                                                     : (p.v_off + row < p.vocab ? p.v_off + row : -1);
+            uint16_t* const out_base = kMode == kHidden ? p.dh : p.dw;
+            const int64_t ld = kMode == kHidden ? p.lddh : p.lddw;
+            const bool aligned = kMode == kHidden ? p.dh_aligned : p.dw_aligned;
+            const float g = sums ? 1.0f : p.head->grad_scale;
+            float* const part = kMode == kHidden ? p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + c0 : nullptr;
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    if (c0 + c >= p.ldacc) break;
-                    uint32_t r[32];
-                    tmem_load32(acc + c, r);
-                    tmem_wait(r);
+            for (int c = 0; c < 128; c += 32) {
+                const int left = p.dim - (c0 + c);
+                if (left <= 0) break;
+                uint32_t r[32];
+                tmem_load32(acc + c, r);
+                tmem_wait(r);
+                if (none || !ok) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = ok ? 0u : 0x7FC00000u;
+                }
+                if (kMode == kHidden && row < rows) {   // one launch per piece, one thread per element: the order is the pieces'
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        if (row >= rows) break;
-                        float4 x = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                        : make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                                      __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-                        float4* const o = reinterpret_cast<float4*>(out + c) + q;
-                        if (!p.first) {   // one launch per piece, one thread per element: the order is the pieces'
+                        float4* const o = reinterpret_cast<float4*>(part + c) + q;
+                        float4 x = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                               __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+                        if (!p.first) {
                             const float4 y = *o;
                             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                         }
-                        *o = x;
-                    }
-                    __syncwarp();
-                }
-            } else {
-                const int v = p.v_off + row;
-                const float g = p.head->grad_scale;
-                uint16_t* const out = p.dw + v * p.lddw + c0;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    const int left = p.dim - (c0 + c);
-                    if (left <= 0) break;
-                    uint32_t r[32];
-                    tmem_load32(acc + c, r);
-                    tmem_wait(r);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        r[j / 2] = none ? 0u : bf16_pair(__uint_as_float(r[j]) * g, __uint_as_float(r[j + 1]) * g);
-                    if (p.dw_aligned && left >= 32) {
-                        if (v < p.vocab) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                *reinterpret_cast<uint4*>(out + c + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                        if (sums) {
+                            *o = x;
+                        } else {
+                            r[4 * q] = __float_as_uint(x.x), r[4 * q + 1] = __float_as_uint(x.y);
+                            r[4 * q + 2] = __float_as_uint(x.z), r[4 * q + 3] = __float_as_uint(x.w);
                         }
-                    } else {   // through shared memory, so that a warp writes 32 neighbours of one row at a time
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(&stage[lane][2 * j]) = r[j];
-                        __syncwarp();
-                        uint16_t* const o = p.dw + (int64_t)(v - lane) * p.lddw + c0 + c + lane;
-                        const int have = min(32, p.vocab - (v - lane));
-                        if (lane < left)
-                            for (int i = 0; i < have; ++i) o[i * p.lddw] = stage[i][lane];
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
+                if (sums) continue;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) r[j / 2] = bf16_pair(__uint_as_float(r[j]) * g, __uint_as_float(r[j + 1]) * g);
+                if (aligned && left >= 32) {
+                    if (out_row >= 0) {
+                        uint16_t* const o = out_base + out_row * ld + c0 + c;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4*>(o + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                    }
+                } else {   // through shared memory, so that a warp writes 32 neighbours of one row at a time
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(&stage[lane][2 * j]) = r[j];
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = 0; i < 32; ++i) {
+                        const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
+                        if (to >= 0 && lane < left) out_base[to * ld + c0 + c + lane] = stage[i][lane];
+                    }
+                }
+                __syncwarp();
             }
             release();
         }
@@ -389,18 +410,42 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     __syncthreads();
     if (kCta == 2) cluster_sync();
     tc_fence_after();
-    if (threadIdx.x == 0 && gave_up) *p.gave_up = 1;
     if (warp == 2) tmem_free<kCta>(tmem, kTmemColumns);
 }
 
 // ---- rows -------------------------------------------------------------------------------------
+// Eight consecutive elements from any address of 16-bit elements, in the widest loads it allows.
+__device__ __forceinline__ uint4 load8_any(const uint16_t* p) {
+    if (aligned16(p)) return *reinterpret_cast<const uint4*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) == 0u) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+        return make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p + 1);
+    const uint32_t a = p[0], b = q[0], c = q[1], d = q[2], e = p[7];
+    return make_uint4(a | (b << 16), __funnelshift_l(b, c, 16), __funnelshift_l(c, d, 16), (d >> 16) | (e << 16));
+}
+// Elements i..i+7 of a row of `dim`, zero past its end.
+__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int i, int dim) {
+    if (i + 8 <= dim) return load8_any(row + i);
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = i + j < dim ? row[i + j] : 0u;
+    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+}
+
 struct RowArgs {
     const int64_t* target;
-    int64_t rows, rows_pad, ignore;
-    int32_t vocab;
+    int64_t rows, ignore;
+    int32_t vocab, dim;
+    const uint16_t* hidden;
+    int64_t ldh;
+    int64_t per_cta;        // rows to a CTA, a multiple of kThreads or below it
     XentHead* head;
+    uint16_t* hc;           // gathered rows, ldhc elements apart
+    int64_t ldhc;
     int32_t* row_of;        // gathered row -> row
-    int32_t* pos_of;        // row -> gathered row, or -1
+    int32_t* pos_of;        // backward: row -> gathered row, or -1
     int32_t* target_of;     // per gathered row; -1 for a target outside the vocabulary
     float* loss;            // forward: outputs, zeroed for rows without a target
     float* lse;
@@ -408,138 +453,163 @@ struct RowArgs {
     const float* grad;
     float* lse_of;
     float* scale_of;
+    uint16_t* dh;           // backward: zeroed for rows left out (NULL: not written)
+    int64_t lddh;
 };
 
-// Which rows have a target, in order: one CTA, eight rows a thread at a time (the prefix sum over all rows
-// is a few microseconds; the copy of the rows themselves follows on the whole GPU).
-// Backward: E is formed in units of the largest |grad_loss|, which the gradients are multiplied with in
-// fp32 at the end.  With equal grad_loss (a mean) E's largest entries are then near -1, where bf16
-// is at its finest, whatever the mean's divisor rounds to.
-__global__ void __launch_bounds__(1024) k_xent_rows(const RowArgs a) {
-    __shared__ int sums[33];
-    __shared__ uint32_t largest;
-    constexpr int kPer = 8;
+// Gathers the rows that count, in their order: tables per gathered row, and the rows themselves side by
+// side.  Each CTA takes a run of rows and first counts, over all targets, how many rows before it
+// count (every CTA reads every target: 8 or 12 bytes a row out of L2, less than a launch between a
+// scan and a copy would take until the rows are hundreds of thousands).
+// Backward: rows whose grad_loss is zero are left out too.  E is formed in units of the largest
+// |grad_loss|, which the gradients are multiplied with in fp32 at the end: with equal grad_loss
+// (a mean) E's largest entries are then near -1, where bf16 is at its finest, whatever the mean's
+// divisor rounds to.
+__global__ void __launch_bounds__(kThreads) k_xent_rows(const RowArgs a) {
+    __shared__ int before_s, total_s;
+    __shared__ uint32_t top_s;
+    __shared__ int warp_count[kThreads / 32 + 1];
+    __shared__ int list_src[kThreads], list_pos[kThreads];
+    // launched without the early start itself: its successor may come as soon as there is room
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int base = 0;
-    float unit = 1.0f;
-    if (a.grad) {
-        if (threadIdx.x == 0) largest = 0u;
-        __syncthreads();
-        uint32_t top = 0u;   // of the finite ones: a NaN or an infinity stays in its row
-        for (int64_t n = threadIdx.x; n < a.rows; n += 1024) {
+    if (threadIdx.x == 0) before_s = total_s = 0, top_s = 0u;
+    __syncthreads();
+    const int64_t start = (int64_t)blockIdx.x * a.per_cta, end = min(a.rows, start + a.per_cta);
+    int before = 0, total = 0;
+    uint32_t top = 0u;   // of the finite ones: a NaN or an infinity stays in its row
+#pragma unroll 4
+    for (int64_t n = threadIdx.x; n < a.rows; n += kThreads) {
+        bool counts = a.target[n] != a.ignore;
+        if (a.grad) {
             const uint32_t b = __float_as_uint(a.grad[n]) & 0x7FFFFFFFu;
-            if (a.target[n] != a.ignore && b < 0x7F800000u) top = max(top, b);
+            counts = counts && b != 0u;
+            if (counts && b < 0x7F800000u) top = max(top, b);
         }
-        atomicMax(&largest, __reduce_max_sync(0xFFFFFFFFu, top));
-        __syncthreads();
-        if (largest != 0u) unit = __uint_as_float(largest);
+        total += counts;
+        before += counts && n < start;
     }
-    for (int64_t n0 = 0; n0 < a.rows; n0 += 1024 * kPer) {
-        const int64_t first = n0 + (int64_t)threadIdx.x * kPer;
-        int64_t t[kPer];
-        int count = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            t[i] = first + i < a.rows ? a.target[first + i] : a.ignore;
-            if (a.grad && first + i < a.rows && a.grad[first + i] == 0.0f) t[i] = a.ignore;   // nothing to add
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) count += t[i] != a.ignore;
-        int run = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xFFFFFFFFu, run, o);
-            if (lane >= o) run += up;
-        }
-        if (lane == 31) sums[warp] = run;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) {
+        atomicAdd(&before_s, before);
+        atomicAdd(&total_s, total);
+        atomicMax(&top_s, top);
+    }
+    __syncthreads();
+    total = total_s;
+    const float unit = top_s != 0u ? __uint_as_float(top_s) : 1.0f;
+    int base = before_s;
+    const int vecs = (int)(a.ldhc / 8);
+    for (int64_t n0 = start; n0 < end; n0 += kThreads) {
+        const int64_t n = n0 + threadIdx.x;
+        const int64_t t = n < end ? a.target[n] : a.ignore;
+        const float g = a.grad && n < end ? a.grad[n] : 1.0f;
+        const bool counts = t != a.ignore && g != 0.0f;
+        const unsigned votes = __ballot_sync(0xFFFFFFFFu, counts);
+        if (lane == 0) warp_count[warp] = __popc(votes);
         __syncthreads();
-        if (warp == 0) {
-            int s = sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xFFFFFFFFu, s, o);
-                if (lane >= o) s += up;
-            }
-            sums[lane] = s;
+        int pos = 0, here = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            pos += i < warp ? warp_count[i] : 0;
+            here += warp_count[i];
         }
-        __syncthreads();
-        int pos = base + run - count + (warp ? sums[warp - 1] : 0);
-        base += sums[31];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int64_t n = first + i;
-            if (n >= a.rows) break;
-            if (t[i] == a.ignore) {
-                a.pos_of[n] = -1;
-                if (a.loss) a.loss[n] = 0.0f;
-                if (a.lse) a.lse[n] = 0.0f;
-                continue;
-            }
-            const bool in = t[i] >= 0 && t[i] < a.vocab;
-            a.pos_of[n] = pos;
-            a.row_of[pos] = (int32_t)n;
-            a.target_of[pos] = in ? (int32_t)t[i] : -1;
+        pos += __popc(votes & ((1u << lane) - 1u));
+        if (counts) {
+            const bool in = t >= 0 && t < a.vocab;
+            const int to = base + pos;
+            list_src[pos] = (int)(n - n0);
+            list_pos[pos] = to;
+            a.row_of[to] = (int32_t)n;
+            a.target_of[to] = in ? (int32_t)t : -1;
             if (a.grad) {
-                a.lse_of[pos] = a.lse_in[n];
-                a.scale_of[pos] = in ? a.grad[n] / unit : __int_as_float(0x7FC00000);
+                a.pos_of[n] = to;
+                a.lse_of[to] = a.lse_in[n];
+                a.scale_of[to] = in ? g / unit : __int_as_float(0x7FC00000);
             }
-            ++pos;
+        } else if (n < end) {
+            if (a.grad) a.pos_of[n] = -1;
+            else a.loss[n] = a.lse[n] = 0.0f;
         }
         __syncthreads();
+        for (int64_t i = threadIdx.x; i < (int64_t)here * vecs; i += kThreads) {
+            const int k = (int)(i / vecs), c = (int)(i - (int64_t)k * vecs) * 8;
+            *reinterpret_cast<uint4*>(a.hc + (int64_t)list_pos[k] * a.ldhc + c) =
+                load_row8(a.hidden + (n0 + list_src[k]) * a.ldh, c, a.dim);
+        }
+        if (a.dh && here < (int)min((int64_t)kThreads, end - n0)) {
+            for (int64_t m = n0; m < min(end, n0 + kThreads); ++m) {
+                const bool out = a.target[m] == a.ignore || a.grad[m] == 0.0f;
+                if (out)
+                    for (int c = threadIdx.x; c < a.dim; c += kThreads) a.dh[m * a.lddh + c] = 0;
+            }
+        }
+        base += here;
+        __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        a.head->rows = base;
-        a.head->gave_up = 0;
+    // backward: the rows' last block of K is filled up with zeros (E is zero there, which NaN would not heed)
+    if (a.grad) {
+        const int fill = (total + kTileK - 1) / kTileK * kTileK;
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)(fill - total) * vecs;
+             i += (int64_t)gridDim.x * kThreads)
+            *reinterpret_cast<uint4*>(a.hc + (int64_t)total * a.ldhc + 8 * i) = make_uint4(0, 0, 0, 0);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.head->rows = total;
         a.head->grad_scale = unit;
     }
 }
 
-// Rows of a matrix copied side by side: dst row c = src row row_of[c] (NULL: src row c), zero from
-// dim to ldd and, past the head's row count, up to the next `round` rows (NULL head: `rows` rows).
-// kVec: both sides in 16-byte vectors.
-template <bool kVec>
-__global__ void __launch_bounds__(kThreads) k_xent_gather(const XentHead* head, const int32_t* __restrict__ row_of,
-                                                          const uint16_t* __restrict__ src, int64_t lds,
-                                                          uint16_t* __restrict__ dst, int64_t ldd, int64_t rows, int dim,
-                                                          int round) {
-    const int64_t have = head ? head->rows : rows;
-    const int64_t limit = head ? min(rows, (have + round - 1) / round * round) : rows;
-    for (int64_t c = blockIdx.x; c < limit; c += gridDim.x) {
-        const uint16_t* s = src + (c < have && row_of ? (int64_t)row_of[c] : c) * lds;
-        uint16_t* d = dst + c * ldd;
-        if (kVec) {
-            for (int i = threadIdx.x * 8; i < ldd; i += kThreads * 8)
-                *reinterpret_cast<uint4*>(d + i) = c < have ? *reinterpret_cast<const uint4*>(s + i) : make_uint4(0, 0, 0, 0);
-        } else {
-            for (int i = threadIdx.x; i < ldd; i += kThreads) d[i] = c < have && i < dim ? s[i] : (uint16_t)0;
-        }
+// Rows of the weight that TMA cannot address (16-byte steps) copied side by side.
+__global__ void __launch_bounds__(kThreads) k_xent_pack(const uint16_t* __restrict__ src, int64_t lds, uint16_t* __restrict__ dst,
+                                                        int64_t ldd, int64_t rows, int dim) {
+    pdl_sync();
+    const int vecs = (int)(ldd / 8);
+    const int64_t n = rows * vecs, step = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+        const int64_t row = i / vecs;
+        *reinterpret_cast<uint4*>(dst + 8 * i) = load_row8(src + row * lds, (int)(i - row * vecs) * 8, dim);
     }
 }
 
-// Joins a row's (maximum, sum) pairs of all vocabulary tiles: 32 rows a CTA, 8 threads a row, a fixed order.
+// Joins a row's (maximum, sum) pairs of all 128-word tiles: 8 rows a CTA, 32 threads a row, a fixed order.
 __global__ void __launch_bounds__(kThreads) k_xent_loss(const XentHead* head, const float2* __restrict__ part, int tiles,
                                                         int64_t rows_pad, const float* __restrict__ target_logit,
                                                         const int32_t* __restrict__ target, const int32_t* __restrict__ row_of,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
-    __shared__ float2 red[8][32];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    __shared__ float2 red[32][9];
+    pdl_sync();
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
     const int rows = head->rows;
     auto join = [](float2 a, float2 b) {
         const float m = fmaxf(a.x, b.x);
         if (m == -INFINITY) return make_float2(m, a.y + b.y);
         return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
     };
-    for (int64_t r0 = (int64_t)blockIdx.x * 32; r0 < rows; r0 += (int64_t)gridDim.x * 32) {
+    for (int64_t r0 = (int64_t)blockIdx.x * 8; r0 < rows; r0 += (int64_t)gridDim.x * 8) {
         const int64_t c = r0 + tx;
         float2 s = make_float2(-INFINITY, 0.0f);
-        if (c < rows)
-            for (int k = ty; k < tiles; k += 8) s = join(s, part[k * rows_pad + c]);
+        if (c < rows) {
+            for (int k = ty; k < tiles; k += 128) {   // four loads at a time
+                float2 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = k + 32 * i < tiles ? part[(k + 32 * i) * rows_pad + c] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s = join(s, q[i]);
+            }
+        }
         red[ty][tx] = s;
+        __syncthreads();
+        if (ty < 8) {
+            for (int k = ty + 8; k < 32; k += 8) s = join(s, red[k][tx]);
+        }
+        __syncthreads();
+        if (ty < 8) red[ty][tx] = s;
         __syncthreads();
         if (ty == 0 && c < rows) {
             for (int k = 1; k < 8; ++k) s = join(s, red[k][tx]);
-            const bool bad = head->gave_up != 0;
-            const float l = bad ? __int_as_float(0x7FC00000) : s.x + logf(s.y);
+            const float l = s.x + logf(s.y);
             const int64_t n = row_of[c];
             lse[n] = l;
             loss[n] = target[c] < 0 ? __int_as_float(0x7FC00000) : l - target_logit[c];
@@ -548,26 +618,26 @@ __global__ void __launch_bounds__(kThreads) k_xent_loss(const XentHead* head, co
     }
 }
 
-// dH rows from the fp32 sums of the gathered rows (the parts of a split K in order); zero where ignored.
+// dH rows from the fp32 parts of a split K, in their order; zero for rows left out.
 __global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, const int32_t* __restrict__ pos_of,
                                                           const float* __restrict__ acc, int splits, int64_t rows_pad,
                                                           int64_t ldacc, uint16_t* __restrict__ dh, int64_t lddh, int64_t rows,
                                                           int dim, bool vec) {
-    const bool bad = head->gave_up != 0;
+    pdl_sync();
+    const float g = head->grad_scale;
     for (int64_t n = blockIdx.x; n < rows; n += gridDim.x) {
         const int64_t c = pos_of[n];
         for (int i = threadIdx.x * 4; i < dim; i += kThreads * 4) {
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (c >= 0) {
+#pragma unroll 4
                 for (int s = 0; s < splits; ++s) {
                     const float4 y = *reinterpret_cast<const float4*>(acc + ((int64_t)s * rows_pad + c) * ldacc + i);
                     x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                 }
             }
-            const float g = bad ? __int_as_float(0x7FC00000) : head->grad_scale;
-            x = make_float4(x.x * g, x.y * g, x.z * g, x.w * g);
             uint16_t* const o = dh + n * lddh + i;
-            const uint32_t lo = bf16_pair(x.x, x.y), hi = bf16_pair(x.z, x.w);
+            const uint32_t lo = bf16_pair(x.x * g, x.y * g), hi = bf16_pair(x.z * g, x.w * g);
             if (vec && i + 4 <= dim) {
                 *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
             } else {
@@ -586,7 +656,7 @@ struct XentPlan {
     int64_t rows, dim, vocab;
     bool pack_w;                // the weight's rows cannot be addressed by TMA: copied piece by piece
     int cta;                    // CTAs on a tile
-    int64_t rows_pad, ldh, piece, ldacc;
+    int64_t rows_pad, ldh, piece, ldacc;   // ldh: of the gathered rows and a copied weight
     int splits;
     size_t row_of, pos_of, target_of, lse_of, scale_of, target_logit, hc, wc, part, e, acc, bytes;
 };
@@ -665,6 +735,25 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
     return OPTIM_OK;
 }
 
+// Launches a kernel behind its predecessor in the call (pdl_sync), as clusters of `cta`.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cta, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cta;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cta > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 template <int kMode, int kCta>
 int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
     constexpr int kSmem = 1024 + product_stages(kCta) * (128 + kTileN / kCta) * kTileK * 2 + kFinishBytes;
@@ -673,37 +762,13 @@ int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductAr
     int rc = check_cuda(attr, "product kernel shared memory");
     if (rc) return rc;
     const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / kCta)) * kCta;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kProductThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = kCta > 1 ? 1 : 0;
-    return check_cuda(cudaLaunchKernelEx(&cfg, kernel, a, b, p), "product launch");
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / kCta)) * kCta;
+    return check_cuda(launch_after(kernel, grid, kProductThreads, kSmem, kCta, s, a, b, p), "product launch");
 }
 
 template <int kMode>
 int launch_product(const XentPlan& pl, const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
     return pl.cta == 2 ? launch_product_t<kMode, 2>(a, b, p, s) : launch_product_t<kMode, 1>(a, b, p, s);
-}
-
-int gather(const XentHead* head, const int32_t* row_of, const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows,
-           int64_t dim, int round, cudaStream_t s) {
-    const bool vec = is_aligned(src, 16) && lds % 8 == 0 && dim % 8 == 0;
-    const unsigned grid = (unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * 16);
-    if (vec)
-        k_xent_gather<true><<<grid, kThreads, 0, s>>>(head, row_of, static_cast<const uint16_t*>(src), lds,
-                                                      static_cast<uint16_t*>(dst), ldd, rows, (int)dim, round);
-    else
-        k_xent_gather<false><<<grid, kThreads, 0, s>>>(head, row_of, static_cast<const uint16_t*>(src), lds,
-                                                       static_cast<uint16_t*>(dst), ldd, rows, (int)dim, round);
-    return check_cuda(cudaGetLastError(), "row copy launch");
 }
 
 }  // namespace
@@ -719,25 +784,39 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     int32_t* const row_of = reinterpret_cast<int32_t*>(ws + pl.row_of);
     int32_t* const pos_of = reinterpret_cast<int32_t*>(ws + pl.pos_of);
     int32_t* const target_of = reinterpret_cast<int32_t*>(ws + pl.target_of);
-    RowArgs ra{c.target, c.rows, pl.rows_pad, c.ignore_index, (int32_t)c.vocab, head, row_of, pos_of, target_of,
-               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    uint16_t* const hc = reinterpret_cast<uint16_t*>(ws + pl.hc);
+    RowArgs ra{};
+    ra.target = c.target;
+    ra.rows = c.rows;
+    ra.ignore = c.ignore_index;
+    ra.vocab = (int32_t)c.vocab;
+    ra.dim = (int32_t)c.dim;
+    ra.hidden = static_cast<const uint16_t*>(c.hidden);
+    ra.ldh = c.ldh;
+    ra.head = head;
+    ra.hc = hc;
+    ra.ldhc = pl.ldh;
+    ra.row_of = row_of;
+    ra.target_of = target_of;
     if (c.backward) {
+        ra.pos_of = pos_of;
         ra.lse_in = c.lse;
         ra.grad = c.grad_loss;
         ra.lse_of = reinterpret_cast<float*>(ws + pl.lse_of);
         ra.scale_of = reinterpret_cast<float*>(ws + pl.scale_of);
+        if (pl.splits == 1) ra.dh = static_cast<uint16_t*>(c.d_hidden);   // else k_xent_hidden writes every row
+        ra.lddh = c.lddh;
     } else {
         ra.loss = c.loss;
         ra.lse = c.lse;
     }
-    k_xent_rows<<<1, 1024, 0, s>>>(ra);
-    int rc = check_cuda(cudaGetLastError(), "row scan launch");
-    uint16_t* const hc = reinterpret_cast<uint16_t*>(ws + pl.hc);
-    if (!rc) rc = gather(head, row_of, c.hidden, c.ldh, hc, pl.ldh, pl.rows_pad, c.dim, 128 * pl.cta, s);
+    // four rows to a CTA while there are few, two CTAs on an SM at most
+    ra.per_cta = std::max<int64_t>(4, (c.rows + 2 * sm_count() - 1) / (2 * sm_count()));
+    k_xent_rows<<<(unsigned)std::max<int64_t>(1, (c.rows + ra.per_cta - 1) / ra.per_cta), kThreads, 0, s>>>(ra);
+    int rc = check_cuda(cudaGetLastError(), "row gathering launch");
 
     ProductArgs p{};
     p.head = head;
-    p.gave_up = &head->gave_up;
     p.vocab = (int32_t)c.vocab;
     p.dim = (int32_t)c.dim;
     p.rows_pad = pl.rows_pad;
@@ -750,6 +829,10 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     p.lde = pl.piece;
     p.acc = reinterpret_cast<float*>(ws + pl.acc);
     p.ldacc = pl.ldacc;
+    p.row_of = row_of;
+    p.dh = static_cast<uint16_t*>(c.d_hidden);
+    p.lddh = c.lddh;
+    p.dh_aligned = is_aligned(c.d_hidden, 16) && c.lddh % 8 == 0;
     p.dw = static_cast<uint16_t*>(c.d_weight);
     p.lddw = c.lddw;
     p.dw_aligned = is_aligned(c.d_weight, 16) && c.lddw % 8 == 0;
@@ -768,7 +851,8 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
         const uint16_t* w = static_cast<const uint16_t*>(c.weight);
         if (pl.pack_w) {   // the piece's rows, side by side; the maps then start at the piece
             uint16_t* const wc = reinterpret_cast<uint16_t*>(ws + pl.wc);
-            rc = gather(nullptr, nullptr, w + v0 * c.ldw, c.ldw, wc, pl.ldh, width, c.dim, 1, s);
+            rc = check_cuda(launch_after(k_xent_pack, std::min<int64_t>(width, (int64_t)sm_count() * 8), kThreads, 0, 1, s,
+                                         w + v0 * c.ldw, c.ldw, wc, pl.ldh, width, (int)c.dim), "weight copy launch");
             w = wc;
         }
         if (!rc && (pl.pack_w || v0 == 0)) {
@@ -795,6 +879,7 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
             h.k_blocks = (int)((width + kTileK - 1) / kTileK);
             h.splits = pl.splits;
             h.first = v0 == 0;
+            h.last = pl.splits == 1 && v0 + width == c.vocab;
             rc = launch_product<kHidden>(pl, e_k, w_mn, h, s);
         }
         if (!rc && c.d_weight) {
@@ -805,16 +890,15 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
         }
     }
     if (rc) return rc;
-    if (!c.backward) {
-        k_xent_loss<<<(unsigned)std::min<int64_t>((c.rows + 31) / 32, sm_count() * 8), kThreads, 0, s>>>(
-            head, p.part, (int)((c.vocab + 127) / 128), pl.rows_pad, p.target_logit, target_of, row_of, c.loss, c.lse);
-        return check_cuda(cudaGetLastError(), "loss launch");
-    }
-    if (!c.d_hidden || c.rows == 0) return OPTIM_OK;
+    if (!c.backward)
+        return check_cuda(launch_after(k_xent_loss, std::min<int64_t>((c.rows + 7) / 8, (int64_t)sm_count() * 8), kThreads, 0, 1, s,
+                                       head, p.part, (int)((c.vocab + 127) / 128), pl.rows_pad, p.target_logit, target_of,
+                                       row_of, c.loss, c.lse), "loss launch");
+    if (!c.d_hidden || c.rows == 0 || pl.splits == 1) return OPTIM_OK;
     const bool vec = is_aligned(c.d_hidden, 8) && c.lddh % 4 == 0;
-    k_xent_hidden<<<(unsigned)std::min<int64_t>(c.rows, sm_count() * 16), kThreads, 0, s>>>(
-        head, pos_of, p.acc, pl.splits, pl.rows_pad, pl.ldacc, static_cast<uint16_t*>(c.d_hidden), c.lddh, c.rows, (int)c.dim, vec);
-    return check_cuda(cudaGetLastError(), "hidden gradient launch");
+    return check_cuda(launch_after(k_xent_hidden, std::min<int64_t>(c.rows, (int64_t)sm_count() * 16), kThreads, 0, 1, s, head,
+                                   pos_of, p.acc, pl.splits, pl.rows_pad, pl.ldacc, p.dh, c.lddh, c.rows, (int)c.dim, vec),
+                      "hidden gradient launch");
 }
 
 }  // namespace lmo

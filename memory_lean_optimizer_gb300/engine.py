@@ -19,8 +19,8 @@ SMALL = lmopt.SMALL_NUMEL
 
 
 def _stream_ptr(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without making a Stream object (3 us) for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -504,6 +504,7 @@ class AdamWGroup(_Group):
         self.flat_m, self.flat_v = (x.view(torch.float32) if states == "fp32" else x for x in flat)
         descs = [_desc(w, r, m, v, w.shape) for w, r, m, v in zip(self.weights, self.res, self.m, self.v)]
         self.handle = lmopt.optim_group_create(descs, self.kind)
+        self._unpacked = sum((w.numel() + 63) // 64 * 64 for w in self.weights)
         self.offload = offload
         if offload is not None:
             lmopt.optim_group_attach_offload(self.handle, offload.handle)
@@ -540,14 +541,14 @@ class AdamWGroup(_Group):
 
     def unpacked_numel(self) -> int:
         """Elements of each flat buffer of unpack_states: every tensor on a multiple of 64."""
-        return sum((w.numel() + 63) // 64 * 64 for w in self.weights)
+        return self._unpacked
 
     def unpack_states(self, m: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
         """The moments as fp32, in two flat buffers (allocated zeroed if not given)."""
-        dev = self.weights[0].device
-        m, v = (torch.zeros(self.unpacked_numel(), dtype=torch.float32, device=dev) if x is None else x for x in (m, v))
+        m, v = (torch.zeros(self._unpacked, dtype=torch.float32, device=self.weights[0].device) if x is None else x
+                for x in (m, v))
         for x in (m, v):
-            assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.numel() >= self.unpacked_numel()
+            assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.numel() >= self._unpacked
         lmopt.optim_group_unpack_state(self.handle, m.data_ptr(), v.data_ptr(), _stream_ptr(stream))
         return m, v
 

@@ -39,22 +39,24 @@ def _on_stream(fn):
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
     """t as a matrix of its last dimension's rows, whose elements lie next to each other: a view where the
     strides allow one (rows may be apart), else a copy."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current GPU")
-    if t.dim() < 1:
-        raise ValueError(f"{name} needs at least one dimension")
     if t.dim() != 2:
+        if t.dim() < 1:
+            raise ValueError(f"{name} needs at least one dimension")
         t = t.reshape(-1, t.shape[-1])
     # a broadcast row (stride 0) is laid out too: the calls want rows at least their length apart
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    rows, dim = t.shape
+    ld, step = t.stride()
+    if dim > 1 and step != 1 or rows > 1 and ld < dim:
         t = t.contiguous()
     return t
 
 
 def _vector(t: torch.Tensor, n: int, like: torch.Tensor, dtype, name: str) -> torch.Tensor:
-    if t.shape != (n,) or t.dtype != dtype or t.device != like.device:
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be {n} values of {dtype} on {like.device}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 @_on_stream
@@ -66,8 +68,8 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     weight = _vector(weight, dim, x, weight.dtype, "weight")
     if bias is not None:
         bias = _vector(bias, dim, x, weight.dtype, "bias")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+    y = x.new_empty(x.shape)
+    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
     lmopt.norm_layer_forward(m.data_ptr(), m.stride(0), weight.data_ptr(), None if bias is None else bias.data_ptr(),
                              y.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim, eps, xt, wt,
                              _stream_ptr(None))
@@ -84,11 +86,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     m, g = _rows(x, "x"), _rows(dy, "dy")
     rows, dim = m.shape
     weight = _vector(weight, dim, x, weight.dtype, "weight")
-    mean, rstd = (_vector(t, rows, x, torch.float32, n) for t, n in ((mean, "mean"), (rstd, "rstd")))
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dweight, dbias = torch.empty_like(weight), torch.empty_like(weight)
+    mean, rstd = _vector(mean, rows, x, torch.float32, "mean"), _vector(rstd, rows, x, torch.float32, "rstd")
+    dx = x.new_empty(x.shape)
+    dweight, dbias = weight.new_empty(dim), weight.new_empty(dim)
     nbytes = lmopt.norm_layer_workspace(rows, dim)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    work = x.new_empty(nbytes, dtype=torch.uint8)
     lmopt.norm_layer_backward(g.data_ptr(), g.stride(0), m.data_ptr(), m.stride(0), weight.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), dx.data_ptr(), dim, dweight.data_ptr(), dbias.data_ptr(), rows, dim,
                               xt, wt, work.data_ptr(), nbytes, _stream_ptr(None))
@@ -122,9 +124,9 @@ def _xent_args(hidden, weight, target):
     if w.dim() != 2 or w.shape[1] != h.shape[1]:
         raise ValueError(f"weight must be [vocabulary, {h.shape[1]}], not {list(weight.shape)}")
     w = _rows(w, "weight")
-    if target.dtype != torch.int64 or target.shape != hidden.shape[:-1] or target.device != hidden.device:
+    if target.dtype != torch.int64 or target.shape != hidden.shape[:-1] or target.get_device() != hidden.get_device():
         raise ValueError(f"target must be int64 {list(hidden.shape[:-1])} on {hidden.device}")
-    return h, w, target.reshape(-1).contiguous()
+    return h, w, target if target.dim() == 1 and target.is_contiguous() else target.reshape(-1).contiguous()
 
 
 @_on_stream
@@ -133,9 +135,9 @@ def xent_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tenso
     and the log of the softmax's denominator.  Rows with ignore_index have 0 for both."""
     h, w, t = _xent_args(hidden, weight, target)
     (rows, dim), vocab = h.shape, w.shape[0]
-    loss, lse = (torch.empty(target.shape, dtype=torch.float32, device=h.device) for _ in range(2))
+    loss, lse = h.new_empty(target.shape, dtype=torch.float32), h.new_empty(target.shape, dtype=torch.float32)
     nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), False)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
+    work = h.new_empty(nbytes, dtype=torch.uint8)
     lmopt.loss_xent_forward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), rows, dim, vocab,
                             ignore_index, loss.data_ptr(), lse.data_ptr(), work.data_ptr(), nbytes, _stream_ptr(None))
     return loss, lse
@@ -147,11 +149,12 @@ def xent_backward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tens
     """(d_hidden, d_weight) of sum(grad_loss * loss), bf16; None for one that is not needed."""
     h, w, t = _xent_args(hidden, weight, target)
     (rows, dim), vocab = h.shape, w.shape[0]
-    lse, g = (_vector(x.reshape(-1), rows, h, torch.float32, n) for x, n in ((lse, "lse"), (grad_loss, "grad_loss")))
-    dh = torch.empty(hidden.shape, dtype=torch.bfloat16, device=h.device) if need_hidden else None
-    dw = torch.empty(weight.shape, dtype=torch.bfloat16, device=h.device) if need_weight else None
+    lse, g = (_vector(x if x.dim() == 1 else x.reshape(-1), rows, h, torch.float32, n)
+              for x, n in ((lse, "lse"), (grad_loss, "grad_loss")))
+    dh = h.new_empty(hidden.shape) if need_hidden else None
+    dw = w.new_empty(weight.shape) if need_weight else None
     nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), True)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
+    work = h.new_empty(nbytes, dtype=torch.uint8)
     lmopt.loss_xent_backward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), lse.data_ptr(),
                              g.data_ptr(), rows, dim, vocab, ignore_index, None if dh is None else dh.data_ptr(), dim,
                              None if dw is None else dw.data_ptr(), dim, work.data_ptr(), nbytes, _stream_ptr(None))
