@@ -80,8 +80,9 @@ __device__ __forceinline__ uint32_t enc8_m(float m, float r) {
     const float y = fminf(sqrt_rn_z(__fmul_rn(fabsf(m), r)), 127.0f);
     return __float_as_uint(__fadd_rn(12583040.0f, copysignf(y, m)));
 }
-__device__ __forceinline__ uint32_t enc8_v(float v, float r) {
-    const float y = fminf(sqrt_rn_z(__fmul_rn(sqrt_rn_z(v), r)), 255.0f);
+// sv = sqrt(v), shared with the update's denominator.
+__device__ __forceinline__ uint32_t enc8_v(float v, float sv, float r) {
+    const float y = fminf(sqrt_rn_z(__fmul_rn(sv, r)), 255.0f);
     return __float_as_uint(__fadd_rn(12582912.0f, v == 0.0f ? 0.0f : fmaxf(y, 1.0f)));
 }
 __device__ __forceinline__ uint32_t pack_byte0(const uint32_t* b) {
@@ -159,85 +160,294 @@ __device__ __forceinline__ void store8f(float* __restrict__ p, int64_t i, int cn
         if (e < cnt) p[i + e] = x[e];
 }
 
-// Each warp takes blocks of 256 elements of its CTA's chunk; a lane holds 8 consecutive ones.
-// Elements past the tensor's end load as zero weight, gradient and state and are not stored (they
-// cannot raise a block's maximum).
+// What a warp needs to know about its CTA's tensor.
+struct Tensor {
+    uint16_t* w;
+    uint16_t* res;
+    const uint16_t* g;
+    void* m;
+    void* v;
+    float* mq;   // 8-bit states: the blocks' constants
+    float* vq;
+    int64_t numel;
+    uint32_t index;
+    bool has_res, u8;
+};
+
+// One block of 256 elements from b0, any alignment, any length: lane l holds elements b0 + 8l .. + 7.
+// Elements past `end` load as zero weight, gradient and state and are not stored (they cannot raise
+// a block's maximum).  Returns the largest exponent field stored.
 template <bool kSR, bool kU8>
-__global__ void __launch_bounds__(kThreads) k_adamw_step(NadamLaunch L, AdamWPrm k) {
-    __shared__ uint32_t red[32];
-    const Chunk c = L.chunks[blockIdx.x];
-    const TensorRec t = L.tensors[c.tensor];
-    const uint16_t* __restrict__ g = L.grads[c.tensor];
-    const bool has_res = (t.flags & kFlagRes) != 0;
-    const bool u8 = kU8 && (t.flags & kFlagSmall) == 0;
-    const int64_t n = t.numel;
-    const int64_t start = (int64_t)c.index * L.chunk;
-    const int64_t end = min(n, start + L.chunk);
-    const float gs = k.grad_scale ? __ldg(k.grad_scale) : 1.0f;
-    const bool aligned = aligned16(t.w) && (!has_res || aligned16(t.res)) && aligned16(g) && aligned16(t.m) &&
-                         aligned16(t.v);
+__device__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, int64_t end, bool aligned) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i = b0 + 8 * lane;
+    const int cnt = (int)max((int64_t)0, min((int64_t)8, end - i));
+    const bool vec = aligned && cnt == 8;
+    uint4 W = load8h(t.w, i, cnt, vec), G = load8h(t.g, i, cnt, vec);
+    uint4 R = t.has_res ? load8h(t.res, i, cnt, vec) : make_uint4(0, 0, 0, 0);
     uint8_t* const mc = static_cast<uint8_t*>(t.m);
     uint8_t* const vc = static_cast<uint8_t*>(t.v);
-    float* const mq = u8 ? reinterpret_cast<float*>(mc + u8_scale_offset(n)) : nullptr;
-    float* const vq = u8 ? reinterpret_cast<float*>(vc + u8_scale_offset(n)) : nullptr;
+    const bool u8 = kU8 && t.u8;
+    float m[8], v[8];
+    if (u8) {
+        dec8<true>(load8b(mc, i, cnt, vec), t.mq[b0 / kBlk], m);
+        dec8<false>(load8b(vc, i, cnt, vec), t.vq[b0 / kBlk], v);
+    } else {
+        load8f(static_cast<const float*>(t.m), i, cnt, vec, m);
+        load8f(static_cast<const float*>(t.v), i, cnt, vec, v);
+    }
+    uint32_t rnd[4] = {0u, 0u, 0u, 0u};
+    if (kSR && !t.has_res) sr_block8(k.key, (uint64_t)k.step, t.index, i, rnd);
+    uint32_t* w32 = reinterpret_cast<uint32_t*>(&W);
+    uint32_t* r32 = reinterpret_cast<uint32_t*>(&R);
+    const uint32_t g32[4] = {G.x, G.y, G.z, G.w};
     uint32_t nf = 0u;
-    const int lane = threadIdx.x & 31;
-    for (int64_t b0 = start + (threadIdx.x >> 5) * kBlk; b0 < end; b0 += (kThreads / 32) * kBlk) {
-        const int64_t i = b0 + 8 * lane;
-        const int cnt = (int)max((int64_t)0, min((int64_t)8, end - i));
-        const bool vec = aligned && cnt == 8;
-        uint4 W = load8h(t.w, i, cnt, vec), G = load8h(g, i, cnt, vec);
-        uint4 R = has_res ? load8h(t.res, i, cnt, vec) : make_uint4(0, 0, 0, 0);
-        float m[8], v[8];
-        if (u8) {
-            dec8<true>(load8b(mc, i, cnt, vec), mq[b0 / kBlk], m);
-            dec8<false>(load8b(vc, i, cnt, vec), vq[b0 / kBlk], v);
-        } else {
-            load8f(static_cast<const float*>(t.m), i, cnt, vec, m);
-            load8f(static_cast<const float*>(t.v), i, cnt, vec, v);
-        }
-        uint32_t rnd[4] = {0u, 0u, 0u, 0u};
-        if (kSR && !has_res) sr_block8(k.key, (uint64_t)k.step, c.tensor, i, rnd);
-        uint32_t* w32 = reinterpret_cast<uint32_t*>(&W);
-        uint32_t* r32 = reinterpret_cast<uint32_t*>(&R);
-        const uint32_t g32[4] = {G.x, G.y, G.z, G.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int q = e >> 1, sh = 16 * (e & 1);
+        float w = __uint_as_float(__byte_perm(r32[q], w32[q], e & 1 ? 0x7632 : 0x5410));
+        // past the end the codes' zero point is not zero: keep those lanes' states at zero
+        if (kU8 && e >= cnt) m[e] = v[e] = 0.0f;
+        adamw_elem(k, gs, w, bf16_to_f32((g32[q] >> sh) & 0xFFFFu), m[e], v[e]);
+        uint32_t lo;
+        const uint32_t hi = store_bits<kSR>(w, t.has_res, (rnd[q] >> sh) & 0xFFFFu, lo);
+        w32[q] = (w32[q] & ~(0xFFFFu << sh)) | (hi << sh);
+        r32[q] = (r32[q] & ~(0xFFFFu << sh)) | (lo << sh);
+        if (e < cnt) nf = max(nf, hi & 0x7FFFu);
+    }
+    store8h(t.w, i, cnt, vec, W);
+    if (t.has_res) store8h(t.res, i, cnt, vec, R);
+    if (u8) {
+        const float qm = __fmul_rn(__fsqrt_rn(block_top(m)), 1.0f / 127.0f);
+        const float qv = __fmul_rn(__fsqrt_rn(__fsqrt_rn(block_top(v))), 1.0f / 255.0f);
+        const float rm = code_factor(qm), rv = code_factor(qv);
+        uint32_t cm[8], cv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int q = e >> 1, sh = 16 * (e & 1);
-            const uint32_t hw = (w32[q] >> sh) & 0xFFFFu, lw = (r32[q] >> sh) & 0xFFFFu;
-            float w = __uint_as_float((hw << 16) | lw);
-            // past the end the codes' zero point is not zero: keep those lanes' states at zero
-            if (kU8 && e >= cnt) m[e] = v[e] = 0.0f;
-            adamw_elem(k, gs, w, bf16_to_f32((g32[q] >> sh) & 0xFFFFu), m[e], v[e]);
-            uint32_t lo;
-            const uint32_t hi = store_bits<kSR>(w, has_res, (rnd[q] >> sh) & 0xFFFFu, lo);
-            w32[q] = (w32[q] & ~(0xFFFFu << sh)) | (hi << sh);
-            r32[q] = (r32[q] & ~(0xFFFFu << sh)) | (lo << sh);
-            if (e < cnt) nf = max(nf, hi & 0x7FFFu);
+            cm[e] = enc8_m(m[e], rm);
+            cv[e] = enc8_v(v[e], __fsqrt_rn(v[e]), rv);
         }
-        store8h(t.w, i, cnt, vec, W);
-        if (has_res) store8h(t.res, i, cnt, vec, R);
-        if (u8) {
-            const float qm = __fmul_rn(__fsqrt_rn(block_top(m)), 1.0f / 127.0f);
-            const float qv = __fmul_rn(__fsqrt_rn(__fsqrt_rn(block_top(v))), 1.0f / 255.0f);
-            const float rm = code_factor(qm), rv = code_factor(qv);
-            uint32_t cm[8], cv[8];
+        store8b(mc, i, cnt, vec, make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
+        store8b(vc, i, cnt, vec, make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
+        if (lane == 0) {
+            t.mq[b0 / kBlk] = qm;
+            t.vq[b0 / kBlk] = qv;
+        }
+    } else {
+        store8f(static_cast<float*>(t.m), i, cnt, vec, m);
+        store8f(static_cast<float*>(t.v), i, cnt, vec, v);
+    }
+    return nf;
+}
+
+// Two fp32 values to an instruction (each rounded as by itself).
+struct F2 {
+    uint64_t x;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.x) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v.x)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
+    return r;
+}
+// a - b as b times -1 plus a: the product is exact, so the one rounding is the difference's.  Sums are
+// written as differences from a negated operand, with a product only as b: a packed sum of products
+// was seen to come out as one multiply-add in spite of .rn (a sixth of a million random cases of
+// b1 m + omb1 g; none of them in this form).
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    F2 r;
+    const F2 minus = f2(-1.0f, -1.0f);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.x) : "l"(b.x), "l"(minus.x), "l"(a.x));
+    return r;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What one lane holds of a block between its loads and its arithmetic.
+struct Raw {
+    uint4 w, r, g;
+    uint2 m, v;
+    float qm, qv;
+};
+__device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
+    const int64_t i = b0 + 8 * (threadIdx.x & 31);
+    x.w = ld_stream(reinterpret_cast<const uint4*>(t.w + i));
+    x.g = ld_stream(reinterpret_cast<const uint4*>(t.g + i));
+    x.r = t.has_res ? ld_stream(reinterpret_cast<const uint4*>(t.res + i)) : make_uint4(0, 0, 0, 0);
+    x.m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
+    x.v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
+    x.qm = t.mq[b0 / kBlk];
+    x.qv = t.vq[b0 / kBlk];
+}
+
+// A whole aligned block with 8-bit states: the arithmetic of adamw_block, two elements to an instruction
+// where one exists.  The step moves 12 bytes an element, which leaves some 60 instructions an
+// element before it is bound by their issue and not by memory, so three things are cut:
+//  - the codes' roots.  A code is the nearest integer to a root; an approximate root (relative error
+//    2^-23 by the instruction's specification, so below 1e-4 at 255) gives the same integer unless
+//    it lies within 1e-4 of the middle between two, and only a lane that has such a one
+//    (1 in 300) forms its eight codes from the exact roots.
+//  - the block's constants.  Lanes 0-15 compute those of m, lanes 16-31 those of v, in one pass.
+//  - infinities and NaN.  A block that holds any takes the exact path as a whole.
+// Returns 0 times the stored weights: NaN if one of them is not finite.
+template <bool kSR>
+__device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, const Raw& x) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i = b0 + 8 * lane;
+    const uint32_t wr[4] = {x.w.x, x.w.y, x.w.z, x.w.w}, rr[4] = {x.r.x, x.r.y, x.r.z, x.r.w};
+    const uint32_t gr[4] = {x.g.x, x.g.y, x.g.z, x.g.w}, mr[2] = {x.m.x, x.m.y}, vr[2] = {x.v.x, x.v.y};
+    const F2 qm2 = f2(x.qm, x.qm), qv2 = f2(x.qv, x.qv), gs2 = f2(gs, gs);
+    const F2 b1 = f2(k.b1, k.b1), n_omb1 = f2(-k.omb1, -k.omb1), b2 = f2(k.b2, k.b2), n_omb2 = f2(-k.omb2, -k.omb2);
+    const F2 wd = f2(k.lr_wd, k.lr_wd), k1 = f2(k.k1, k.k1), n_k2 = f2(-k.k2, -k.k2), eps = f2(k.eps, k.eps);
+    uint32_t rnd[4] = {0u, 0u, 0u, 0u};
+    if (kSR && !t.has_res) sr_block8(k.key, (uint64_t)k.step, t.index, i, rnd);
+    float m[8], v[8], sv[8], top_m = 0.0f, top_v = 0.0f, bad = 0.0f;
+    uint32_t wo[4], ro[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cm[e] = enc8_m(m[e], rm);
-                cv[e] = enc8_v(v[e], rv);
-            }
-            store8b(mc, i, cnt, vec, make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
-            store8b(vc, i, cnt, vec, make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
-            if (lane == 0) {
-                mq[b0 / kBlk] = qm;
-                vq[b0 / kBlk] = qv;
-            }
+    for (int q = 0; q < 4; ++q) {
+        // the pair's codes: byte 2 (q mod 2) and the next of word q / 2
+        const uint32_t mw = mr[q >> 1], vw = vr[q >> 1];
+        const F2 cm = q & 1 ? f2(byte_to_f32<2>(mw, 8388736.0f), byte_to_f32<3>(mw, 8388736.0f))
+                            : f2(byte_to_f32<0>(mw, 8388736.0f), byte_to_f32<1>(mw, 8388736.0f));
+        const F2 cv = q & 1 ? f2(byte_to_f32<2>(vw, 8388608.0f), byte_to_f32<3>(vw, 8388608.0f))
+                            : f2(byte_to_f32<0>(vw, 8388608.0f), byte_to_f32<1>(vw, 8388608.0f));
+        const F2 tm = mul2(cm, qm2), tv = mul2(cv, qv2), tv2 = mul2(tv, tv);
+        float ta, tb, ma, mb;
+        split2(tm, ta, tb);
+        split2(mul2(tm, tm), ma, mb);
+        const F2 m0 = f2(copysignf(ma, ta), copysignf(mb, tb)), v0 = mul2(tv2, tv2);   // t |t|, (z z)(z z)
+        const F2 g = mul2(f2(__uint_as_float(gr[q] << 16), __uint_as_float(gr[q] & 0xFFFF0000u)), gs2);
+        const F2 m1 = sub2(mul2(b1, m0), mul2(n_omb1, g));
+        const F2 v1 = sub2(mul2(b2, v0), mul2(n_omb2, mul2(g, g)));
+        F2 w = f2(__uint_as_float(__byte_perm(rr[q], wr[q], 0x5410)), __uint_as_float(__byte_perm(rr[q], wr[q], 0x7632)));
+        w = sub2(w, mul2(wd, w));
+        split2(m1, m[2 * q], m[2 * q + 1]);
+        split2(v1, v[2 * q], v[2 * q + 1]);
+        sv[2 * q] = sqrt_rn_z(v[2 * q]);
+        sv[2 * q + 1] = sqrt_rn_z(v[2 * q + 1]);
+        float da, db, na, nb;
+        split2(sub2(eps, mul2(f2(sv[2 * q], sv[2 * q + 1]), n_k2)), da, db);
+        split2(mul2(k1, m1), na, nb);
+        w = sub2(w, f2(div_rn_z(na, da), div_rn_z(nb, db)));
+        float wa, wb;
+        split2(w, wa, wb);
+        bad = fmaf(wa, 0.0f, fmaf(wb, 0.0f, bad));
+        if (t.has_res) {
+            wo[q] = pack_hi16(__float_as_uint(wa), __float_as_uint(wb));
+            ro[q] = pack_lo16(__float_as_uint(wa), __float_as_uint(wb));
         } else {
-            store8f(static_cast<float*>(t.m), i, cnt, vec, m);
-            store8f(static_cast<float*>(t.v), i, cnt, vec, v);
+            uint32_t lo;
+            wo[q] = pack_lo16(store_bits<kSR>(wa, false, rnd[q] & 0xFFFFu, lo), store_bits<kSR>(wb, false, rnd[q] >> 16, lo));
+            // rounding to bf16 can carry a finite weight to infinity
+            if ((wo[q] & 0x7F80u) == 0x7F80u || (wo[q] & 0x7F800000u) == 0x7F800000u) bad = __int_as_float(0x7FC00000);
+        }
+        top_m = fmaxf(top_m, fmaxf(fabsf(m[2 * q]), fabsf(m[2 * q + 1])));
+        top_v = fmaxf(top_v, fmaxf(v[2 * q], v[2 * q + 1]));
+    }
+    st_stream(reinterpret_cast<uint4*>(t.w + i), make_uint4(wo[0], wo[1], wo[2], wo[3]));
+    if (t.has_res) st_stream(reinterpret_cast<uint4*>(t.res + i), make_uint4(ro[0], ro[1], ro[2], ro[3]));
+
+    top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_m)));
+    top_v = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_v)));
+    const bool finite = __all_sync(0xFFFFFFFFu, bad == 0.0f) && fmaxf(top_m, top_v) < __int_as_float(0x7F800000);
+    if (!finite) {   // whole warp: the maxima of the finite values
+        top_m = block_top(m);
+        top_v = block_top(v);
+    }
+    const bool second = lane >= 16;
+    const float root = __fsqrt_rn(second ? top_v : top_m);
+    const float q0 = second ? __fmul_rn(__fsqrt_rn(root), 1.0f / 255.0f) : __fmul_rn(root, 1.0f / 127.0f);
+    const float r0 = code_factor(q0);
+    const float rm = __shfl_sync(0xFFFFFFFFu, r0, 0), rv = __shfl_sync(0xFFFFFFFFu, r0, 16);
+    uint32_t cm[8], cv[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float xa, xb, ya, yb;
+        split2(mul2(f2(m[e], m[e + 1]), f2(rm, rm)), xa, xb);
+        const F2 y = f2(copysignf(sqrt_approx(fabsf(xa)), xa), copysignf(sqrt_approx(fabsf(xb)), xb));
+        const F2 zero_m = f2(12583040.0f, 12583040.0f), zero_v = f2(12582912.0f, 12582912.0f);   // 1.5 * 2^23, + 128
+        F2 c = sub2(y, f2(-12583040.0f, -12583040.0f));
+        split2(c, xa, xb);
+        cm[e] = __float_as_uint(xa);
+        cm[e + 1] = __float_as_uint(xb);
+        split2(sub2(y, sub2(c, zero_m)), ya, yb);
+        off = fmaxf(off, fmaxf(fabsf(ya), fabsf(yb)));
+        split2(mul2(f2(sv[e], sv[e + 1]), f2(rv, rv)), xa, xb);
+        // at least 1 for a positive v: sv times 1e38, saturated, is 1 for every positive root and 0 for none
+        const F2 z = f2(fmaxf(sqrt_approx(xa), __saturatef(sv[e] * 1e38f)), fmaxf(sqrt_approx(xb), __saturatef(sv[e + 1] * 1e38f)));
+        c = sub2(z, f2(-12582912.0f, -12582912.0f));
+        split2(c, xa, xb);
+        cv[e] = __float_as_uint(xa);
+        cv[e + 1] = __float_as_uint(xb);
+        split2(sub2(z, sub2(c, zero_v)), ya, yb);
+        off = fmaxf(off, fmaxf(fabsf(ya), fabsf(yb)));
+    }
+    if (!finite || off > 0.4999f) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+            const float me = m[0], ve = v[0], se = sv[0];   // rotated through the first place: no indexed registers
+#pragma unroll
+            for (int j = 0; j < 7; ++j) m[j] = m[j + 1], v[j] = v[j + 1], sv[j] = sv[j + 1], cm[j] = cm[j + 1], cv[j] = cv[j + 1];
+            cm[7] = enc8_m(me, rm);
+            cv[7] = enc8_v(ve, se, rv);
         }
     }
+    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
+    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
+    if (lane == 0) t.mq[b0 / kBlk] = q0;
+    if (lane == 16) t.vq[b0 / kBlk] = q0;
+    return bad;
+}
+
+// Each warp takes blocks of 256 elements of its CTA's chunk.  With 8-bit states the whole aligned ones go
+// through adamw_block_fast, the next block's loads under way while one is computed.
+template <bool kSR, bool kU8>
+__global__ void __launch_bounds__(kThreads, kU8 ? 2 : 3) k_adamw_step(NadamLaunch L, AdamWPrm k) {
+    __shared__ uint32_t red[32];
+    const Chunk c = L.chunks[blockIdx.x];
+    const TensorRec rec = L.tensors[c.tensor];
+    Tensor t;
+    t.w = rec.w;
+    t.res = rec.res;
+    t.g = L.grads[c.tensor];
+    t.m = rec.m;
+    t.v = rec.v;
+    t.numel = rec.numel;
+    t.index = c.tensor;
+    t.has_res = (rec.flags & kFlagRes) != 0;
+    t.u8 = kU8 && (rec.flags & kFlagSmall) == 0;
+    t.mq = t.u8 ? reinterpret_cast<float*>(static_cast<uint8_t*>(t.m) + u8_scale_offset(t.numel)) : nullptr;
+    t.vq = t.u8 ? reinterpret_cast<float*>(static_cast<uint8_t*>(t.v) + u8_scale_offset(t.numel)) : nullptr;
+    const int64_t start = (int64_t)c.index * L.chunk, end = min(t.numel, start + L.chunk);
+    const float gs = k.grad_scale ? __ldg(k.grad_scale) : 1.0f;
+    const bool aligned = aligned16(t.w) && (!t.has_res || aligned16(t.res)) && aligned16(t.g) && aligned16(t.m) &&
+                         aligned16(t.v);
+    constexpr int64_t kStep = (kThreads / 32) * kBlk;
+    int64_t b0 = start + (threadIdx.x >> 5) * kBlk;
+    uint32_t nf = 0u;
+    if (kU8 && t.u8 && aligned) {
+        const int64_t whole = start + (end - start) / kBlk * kBlk;
+        float bad = 0.0f;
+        Raw x;
+        if (b0 < whole) load_raw(x, t, b0);
+        for (; b0 < whole; b0 += kStep) {
+            Raw next;
+            if (b0 + kStep < whole) load_raw(next, t, b0 + kStep);
+            bad += adamw_block_fast<kSR>(k, t, gs, b0, x);
+            x = next;
+        }
+        if (bad != 0.0f) nf = 0x7F80u;
+    }
+    for (; b0 < end; b0 += kStep) nf = max(nf, adamw_block<kSR, kU8>(k, t, gs, b0, end, aligned));
     uint32_t r[1] = {nf >= 0x7F80u ? 1u : 0u};
     block_max_u32<1>(r, red);
     if (threadIdx.x == 0 && r[0]) atomicAdd(L.nonfinite, 1ull);
@@ -250,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_unpack(NadamLaunch L, float*
     const TensorRec t = L.tensors[c.tensor];
     const bool u8 = kU8 && (t.flags & kFlagSmall) == 0;
     const int64_t n = t.numel;
-    const int64_t start = (int64_t)c.index * L.chunk;
+    int64_t start = (int64_t)c.index * L.chunk;
     const int64_t end = min(n, start + L.chunk);
     float* const om = fm + 64 * (int64_t)t.slot64;
     float* const ov = fv + 64 * (int64_t)t.slot64;
@@ -259,18 +469,30 @@ __global__ void __launch_bounds__(kThreads) k_adamw_unpack(NadamLaunch L, float*
     const uint8_t* vc = static_cast<const uint8_t*>(t.v);
     const float* mq = u8 ? reinterpret_cast<const float*>(mc + u8_scale_offset(n)) : nullptr;
     const float* vq = u8 ? reinterpret_cast<const float*>(vc + u8_scale_offset(n)) : nullptr;
-    for (int64_t i = start + 8 * (int64_t)threadIdx.x; i < end; i += 8 * kThreads) {
-        const int cnt = (int)min((int64_t)8, end - i);
+    // four elements a lane: a word of codes in, one 16-byte store of each moment, neighbours side by side
+    if (u8 && in16 && out16) {
+        const int64_t whole = start + (end - start) / 4 * 4;
+#pragma unroll 4
+        for (int64_t i = start + 4 * (int64_t)threadIdx.x; i < whole; i += 4 * kThreads) {
+            float m[8], v[8];
+            dec8<true>(make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(mc + i)), 0u), mq[i / kBlk], m);
+            dec8<false>(make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(vc + i)), 0u), vq[i / kBlk], v);
+            st_stream(reinterpret_cast<float4*>(om + i), make_float4(m[0], m[1], m[2], m[3]));
+            st_stream(reinterpret_cast<float4*>(ov + i), make_float4(v[0], v[1], v[2], v[3]));
+        }
+        start = whole;
+    }
+    for (int64_t i = start + threadIdx.x; i < end; i += kThreads) {
         float m[8], v[8];
         if (u8) {
-            dec8<true>(load8b(mc, i, cnt, in16 && cnt == 8), mq[i / kBlk], m);
-            dec8<false>(load8b(vc, i, cnt, in16 && cnt == 8), vq[i / kBlk], v);
+            dec8<true>(make_uint2(mc[i], 0u), mq[i / kBlk], m);
+            dec8<false>(make_uint2(vc[i], 0u), vq[i / kBlk], v);
         } else {
-            load8f(static_cast<const float*>(t.m), i, cnt, in16 && cnt == 8, m);
-            load8f(static_cast<const float*>(t.v), i, cnt, in16 && cnt == 8, v);
+            m[0] = __ldcs(static_cast<const float*>(t.m) + i);
+            v[0] = __ldcs(static_cast<const float*>(t.v) + i);
         }
-        store8f(om, i, cnt, out16 && cnt == 8, m);
-        store8f(ov, i, cnt, out16 && cnt == 8, v);
+        om[i] = m[0];
+        ov[i] = v[0];
     }
 }
 
