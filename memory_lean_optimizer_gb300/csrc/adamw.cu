@@ -25,6 +25,7 @@ struct AdamWPrm {
     float b1, omb1, b2, omb2, eps, lr_wd, k1, k2;
     const float* grad_scale;   // device scalar s, or NULL: 1
     int64_t step;
+    int32_t plain_range;       // k1, k2 and eps lie where the branch-free quotient holds (see Range)
     PhiloxKey key;
 };
 
@@ -80,10 +81,10 @@ __device__ __forceinline__ uint32_t enc8_m(float m, float r) {
     const float y = fminf(sqrt_rn_z(__fmul_rn(fabsf(m), r)), 127.0f);
     return __float_as_uint(__fadd_rn(12583040.0f, copysignf(y, m)));
 }
-// sv = sqrt(v), shared with the update's denominator.
-__device__ __forceinline__ uint32_t enc8_v(float v, float sv, float r) {
+// sv = sqrt(v), shared with the update's denominator (zero for v = 0 alone).
+__device__ __forceinline__ uint32_t enc8_v(float sv, float r) {
     const float y = fminf(sqrt_rn_z(__fmul_rn(sv, r)), 255.0f);
-    return __float_as_uint(__fadd_rn(12582912.0f, v == 0.0f ? 0.0f : fmaxf(y, 1.0f)));
+    return __float_as_uint(__fadd_rn(12582912.0f, sv == 0.0f ? 0.0f : fmaxf(y, 1.0f)));
 }
 __device__ __forceinline__ uint32_t pack_byte0(const uint32_t* b) {
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
@@ -167,18 +168,17 @@ struct Tensor {
     const uint16_t* g;
     void* m;
     void* v;
-    float* mq;   // 8-bit states: the blocks' constants
-    float* vq;
-    int64_t numel;
     uint32_t index;
     bool has_res, u8;
 };
 
 // One block of 256 elements from b0, any alignment, any length: lane l holds elements b0 + 8l .. + 7.
 // Elements past `end` load as zero weight, gradient and state and are not stored (they cannot raise
-// a block's maximum).  Returns the largest exponent field stored.
+// a block's maximum).  8-bit states: qmv holds the block's constants, old in, new out.  Returns the largest
+// exponent field stored.
 template <bool kSR, bool kU8>
-__device__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, int64_t end, bool aligned) {
+__device__ __noinline__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, int64_t end, bool aligned,
+                                             float2& qmv) {
     const int lane = threadIdx.x & 31;
     const int64_t i = b0 + 8 * lane;
     const int cnt = (int)max((int64_t)0, min((int64_t)8, end - i));
@@ -190,8 +190,8 @@ __device__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, in
     const bool u8 = kU8 && t.u8;
     float m[8], v[8];
     if (u8) {
-        dec8<true>(load8b(mc, i, cnt, vec), t.mq[b0 / kBlk], m);
-        dec8<false>(load8b(vc, i, cnt, vec), t.vq[b0 / kBlk], v);
+        dec8<true>(load8b(mc, i, cnt, vec), qmv.x, m);
+        dec8<false>(load8b(vc, i, cnt, vec), qmv.y, v);
     } else {
         load8f(static_cast<const float*>(t.m), i, cnt, vec, m);
         load8f(static_cast<const float*>(t.v), i, cnt, vec, v);
@@ -225,14 +225,11 @@ __device__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, in
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             cm[e] = enc8_m(m[e], rm);
-            cv[e] = enc8_v(v[e], __fsqrt_rn(v[e]), rv);
+            cv[e] = enc8_v(sqrt_rn_z(v[e]), rv);
         }
         store8b(mc, i, cnt, vec, make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
         store8b(vc, i, cnt, vec, make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
-        if (lane == 0) {
-            t.mq[b0 / kBlk] = qm;
-            t.vq[b0 / kBlk] = qv;
-        }
+        qmv = make_float2(qm, qv);
     } else {
         store8f(static_cast<float*>(t.m), i, cnt, vec, m);
         store8f(static_cast<float*>(t.v), i, cnt, vec, v);
@@ -271,11 +268,58 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return y;
 }
 
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.x) : "l"(a.x), "l"(b.x), "l"(c.x));
+    return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Root and quotient rounded to nearest without a branch, two at a time, by the multiply-add sequences of
+// Markstein ("IA-64 and Elementary Functions", 2000): an approximate 1/sqrt(x) or 1/b refined once,
+// then the exact remainder x - g^2 or a - b q added back.  Compared with __fsqrt_rn over every
+// significand and both parities of the exponent, with the correctly rounded reciprocal over every
+// significand, and with __fdiv_rn on 2e10 random pairs and the 1.7e7 pairs whose quotient is
+// closest to the middle of two numbers: no difference.  The intermediate results must not leave the
+// normal range, which Range states; CUDA's own have no such limit, but a branch each, and
+// sixteen branches in a lane's block of eight keep its elements from overlapping.
+struct Range {   // of v and |m|, given plain_range: 2^-30 <= k1 <= 2^20, 1 <= k2 <= 2^13, eps <= 1
+    static constexpr float v_min = 0x1p-96f, v_max = 0x1p40f, m_min = 0x1p-60f, m_max = 0x1p20f;
+};
+// -sqrt(x) from nx = -x.
+__device__ __forceinline__ F2 neg_sqrt2(F2 nx) {
+    float a, b;
+    split2(nx, a, b);
+    const F2 y = f2(rsqrt_approx(-a), rsqrt_approx(-b)), half = f2(0.5f, 0.5f);
+    F2 ng = mul2(nx, y), h = mul2(y, half);
+    const F2 e = fma2(ng, h, half);
+    ng = fma2(ng, e, ng);
+    h = fma2(h, e, h);
+    return fma2(fma2(ng, ng, nx), h, ng);
+}
+// a / b from nb = -b.
+__device__ __forceinline__ F2 div2(F2 a, F2 nb) {
+    float x, y;
+    split2(nb, x, y);
+    F2 r = f2(rcp_approx(-x), rcp_approx(-y));
+    r = fma2(fma2(nb, r, f2(1.0f, 1.0f)), r, r);
+    const F2 q = mul2(a, r);
+    return fma2(fma2(nb, q, a), r, q);
+}
+
 // What one lane holds of a block between its loads and its arithmetic.
 struct Raw {
     uint4 w, r, g;
     uint2 m, v;
-    float qm, qv;
 };
 __device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
     const int64_t i = b0 + 8 * (threadIdx.x & 31);
@@ -284,32 +328,33 @@ __device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
     x.r = t.has_res ? ld_stream(reinterpret_cast<const uint4*>(t.res + i)) : make_uint4(0, 0, 0, 0);
     x.m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
     x.v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
-    x.qm = t.mq[b0 / kBlk];
-    x.qv = t.vq[b0 / kBlk];
 }
 
-// A whole aligned block with 8-bit states: the arithmetic of adamw_block, two elements to an instruction
+// A whole aligned block with 8-bit states: the results of adamw_block, two elements to an instruction
 // where one exists.  The step moves 12 bytes an element, which leaves some 60 instructions an
 // element before it is bound by their issue and not by memory, so three things are cut:
+//  - the update's root and quotient have no branch (above).
 //  - the codes' roots.  A code is the nearest integer to a root; an approximate root (relative error
 //    2^-23 by the instruction's specification, so below 1e-4 at 255) gives the same integer unless
 //    it lies within 1e-4 of the middle between two, and only a lane that has such a one
 //    (1 in 300) forms its eight codes from the exact roots.
 //  - the block's constants.  Lanes 0-15 compute those of m, lanes 16-31 those of v, in one pass.
-//  - infinities and NaN.  A block that holds any takes the exact path as a whole.
+// A block with a moment outside Range (an exact zero, an infinity or a NaN among them) is left to
+// adamw_block as a whole, before anything of it is stored.
 // Returns 0 times the stored weights: NaN if one of them is not finite.
 template <bool kSR>
-__device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, const Raw& x) {
+__device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, const Raw& x, float2& qmv) {
     const int lane = threadIdx.x & 31;
     const int64_t i = b0 + 8 * lane;
     const uint32_t wr[4] = {x.w.x, x.w.y, x.w.z, x.w.w}, rr[4] = {x.r.x, x.r.y, x.r.z, x.r.w};
     const uint32_t gr[4] = {x.g.x, x.g.y, x.g.z, x.g.w}, mr[2] = {x.m.x, x.m.y}, vr[2] = {x.v.x, x.v.y};
-    const F2 qm2 = f2(x.qm, x.qm), qv2 = f2(x.qv, x.qv), gs2 = f2(gs, gs);
-    const F2 b1 = f2(k.b1, k.b1), n_omb1 = f2(-k.omb1, -k.omb1), b2 = f2(k.b2, k.b2), n_omb2 = f2(-k.omb2, -k.omb2);
-    const F2 wd = f2(k.lr_wd, k.lr_wd), k1 = f2(k.k1, k.k1), n_k2 = f2(-k.k2, -k.k2), eps = f2(k.eps, k.eps);
+    const F2 qm2 = f2(qmv.x, qmv.x), qv2 = f2(qmv.y, qmv.y), gs2 = f2(gs, gs);
+    const F2 b1 = f2(k.b1, k.b1), n_omb1 = f2(-k.omb1, -k.omb1), n_b2 = f2(-k.b2, -k.b2), omb2 = f2(k.omb2, k.omb2);
+    const F2 wd = f2(k.lr_wd, k.lr_wd), k1 = f2(k.k1, k.k1), n_k2 = f2(-k.k2, -k.k2), n_eps = f2(-k.eps, -k.eps);
     uint32_t rnd[4] = {0u, 0u, 0u, 0u};
     if (kSR && !t.has_res) sr_block8(k.key, (uint64_t)k.step, t.index, i, rnd);
-    float m[8], v[8], sv[8], top_m = 0.0f, top_v = 0.0f, bad = 0.0f;
+    float m[8], nsv[8];          // the new first moments, and minus the roots of the second
+    float top_m = 0.0f, top_v = 0.0f, low_m = FLT_MAX, low_v = FLT_MAX, bad = 0.0f;
     uint32_t wo[4], ro[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -320,23 +365,24 @@ __device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tenso
         const F2 cv = q & 1 ? f2(byte_to_f32<2>(vw, 8388608.0f), byte_to_f32<3>(vw, 8388608.0f))
                             : f2(byte_to_f32<0>(vw, 8388608.0f), byte_to_f32<1>(vw, 8388608.0f));
         const F2 tm = mul2(cm, qm2), tv = mul2(cv, qv2), tv2 = mul2(tv, tv);
-        float ta, tb, ma, mb;
+        float ta, tb, ma, mb, na, nb;
         split2(tm, ta, tb);
         split2(mul2(tm, tm), ma, mb);
         const F2 m0 = f2(copysignf(ma, ta), copysignf(mb, tb)), v0 = mul2(tv2, tv2);   // t |t|, (z z)(z z)
         const F2 g = mul2(f2(__uint_as_float(gr[q] << 16), __uint_as_float(gr[q] & 0xFFFF0000u)), gs2);
         const F2 m1 = sub2(mul2(b1, m0), mul2(n_omb1, g));
-        const F2 v1 = sub2(mul2(b2, v0), mul2(n_omb2, mul2(g, g)));
+        const F2 nv = sub2(mul2(n_b2, v0), mul2(omb2, mul2(g, g)));                    // -v
+        const F2 root = neg_sqrt2(nv);
+        const F2 upd = div2(mul2(k1, m1), sub2(n_eps, mul2(root, n_k2)));
         F2 w = f2(__uint_as_float(__byte_perm(rr[q], wr[q], 0x5410)), __uint_as_float(__byte_perm(rr[q], wr[q], 0x7632)));
-        w = sub2(w, mul2(wd, w));
+        w = sub2(sub2(w, mul2(wd, w)), upd);
         split2(m1, m[2 * q], m[2 * q + 1]);
-        split2(v1, v[2 * q], v[2 * q + 1]);
-        sv[2 * q] = sqrt_rn_z(v[2 * q]);
-        sv[2 * q + 1] = sqrt_rn_z(v[2 * q + 1]);
-        float da, db, na, nb;
-        split2(sub2(eps, mul2(f2(sv[2 * q], sv[2 * q + 1]), n_k2)), da, db);
-        split2(mul2(k1, m1), na, nb);
-        w = sub2(w, f2(div_rn_z(na, da), div_rn_z(nb, db)));
+        split2(root, nsv[2 * q], nsv[2 * q + 1]);
+        split2(nv, na, nb);
+        top_m = fmaxf(top_m, fmaxf(fabsf(m[2 * q]), fabsf(m[2 * q + 1])));
+        low_m = fminf(low_m, fminf(fabsf(m[2 * q]), fabsf(m[2 * q + 1])));
+        top_v = fmaxf(top_v, fmaxf(-na, -nb));
+        low_v = fminf(low_v, fminf(-na, -nb));
         float wa, wb;
         split2(w, wa, wb);
         bad = fmaf(wa, 0.0f, fmaf(wb, 0.0f, bad));
@@ -346,22 +392,21 @@ __device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tenso
         } else {
             uint32_t lo;
             wo[q] = pack_lo16(store_bits<kSR>(wa, false, rnd[q] & 0xFFFFu, lo), store_bits<kSR>(wb, false, rnd[q] >> 16, lo));
+            ro[q] = 0u;
             // rounding to bf16 can carry a finite weight to infinity
             if ((wo[q] & 0x7F80u) == 0x7F80u || (wo[q] & 0x7F800000u) == 0x7F800000u) bad = __int_as_float(0x7FC00000);
         }
-        top_m = fmaxf(top_m, fmaxf(fabsf(m[2 * q]), fabsf(m[2 * q + 1])));
-        top_v = fmaxf(top_v, fmaxf(v[2 * q], v[2 * q + 1]));
     }
+    // minima and maxima pass over a NaN, but it reaches the weight
+    const bool plain = k.plain_range && low_v >= Range::v_min && top_v <= Range::v_max && low_m >= Range::m_min &&
+                       top_m <= Range::m_max && bad == 0.0f;
+    if (!__all_sync(0xFFFFFFFFu, plain))
+        return adamw_block<kSR, true>(k, t, gs, b0, b0 + kBlk, true, qmv) >= 0x7F80u ? __int_as_float(0x7FC00000) : 0.0f;
     st_stream(reinterpret_cast<uint4*>(t.w + i), make_uint4(wo[0], wo[1], wo[2], wo[3]));
     if (t.has_res) st_stream(reinterpret_cast<uint4*>(t.res + i), make_uint4(ro[0], ro[1], ro[2], ro[3]));
 
     top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_m)));
     top_v = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_v)));
-    const bool finite = __all_sync(0xFFFFFFFFu, bad == 0.0f) && fmaxf(top_m, top_v) < __int_as_float(0x7F800000);
-    if (!finite) {   // whole warp: the maxima of the finite values
-        top_m = block_top(m);
-        top_v = block_top(v);
-    }
     const bool second = lane >= 16;
     const float root = __fsqrt_rn(second ? top_v : top_m);
     const float q0 = second ? __fmul_rn(__fsqrt_rn(root), 1.0f / 255.0f) : __fmul_rn(root, 1.0f / 127.0f);
@@ -369,50 +414,54 @@ __device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tenso
     const float rm = __shfl_sync(0xFFFFFFFFu, r0, 0), rv = __shfl_sync(0xFFFFFFFFu, r0, 16);
     uint32_t cm[8], cv[8];
     float off = 0.0f;
+    const F2 zero_m = f2(12583040.0f, 12583040.0f), zero_v = f2(12582912.0f, 12582912.0f);   // 1.5 * 2^23 (+ 128)
+    const F2 n_zero_m = f2(-12583040.0f, -12583040.0f), n_zero_v = f2(-12582912.0f, -12582912.0f);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         float xa, xb, ya, yb;
         split2(mul2(f2(m[e], m[e + 1]), f2(rm, rm)), xa, xb);
         const F2 y = f2(copysignf(sqrt_approx(fabsf(xa)), xa), copysignf(sqrt_approx(fabsf(xb)), xb));
-        const F2 zero_m = f2(12583040.0f, 12583040.0f), zero_v = f2(12582912.0f, 12582912.0f);   // 1.5 * 2^23, + 128
-        F2 c = sub2(y, f2(-12583040.0f, -12583040.0f));
+        F2 c = sub2(y, n_zero_m);
         split2(c, xa, xb);
         cm[e] = __float_as_uint(xa);
         cm[e + 1] = __float_as_uint(xb);
         split2(sub2(y, sub2(c, zero_m)), ya, yb);
         off = fmaxf(off, fmaxf(fabsf(ya), fabsf(yb)));
-        split2(mul2(f2(sv[e], sv[e + 1]), f2(rv, rv)), xa, xb);
-        // at least 1 for a positive v: sv times 1e38, saturated, is 1 for every positive root and 0 for none
-        const F2 z = f2(fmaxf(sqrt_approx(xa), __saturatef(sv[e] * 1e38f)), fmaxf(sqrt_approx(xb), __saturatef(sv[e + 1] * 1e38f)));
-        c = sub2(z, f2(-12582912.0f, -12582912.0f));
+        split2(mul2(f2(nsv[e], nsv[e + 1]), f2(rv, rv)), xa, xb);
+        const F2 z = f2(fmaxf(sqrt_approx(fabsf(xa)), 1.0f), fmaxf(sqrt_approx(fabsf(xb)), 1.0f));   // v > 0 here
+        c = sub2(z, n_zero_v);
         split2(c, xa, xb);
         cv[e] = __float_as_uint(xa);
         cv[e + 1] = __float_as_uint(xb);
         split2(sub2(z, sub2(c, zero_v)), ya, yb);
         off = fmaxf(off, fmaxf(fabsf(ya), fabsf(yb)));
     }
-    if (!finite || off > 0.4999f) {
+    if (off > 0.4999f) {
 #pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-            const float me = m[0], ve = v[0], se = sv[0];   // rotated through the first place: no indexed registers
+        for (int e = 0; e < 8; ++e) {   // rotated through the first place: no indexed registers
+            const float me = m[0], se = -nsv[0];
 #pragma unroll
-            for (int j = 0; j < 7; ++j) m[j] = m[j + 1], v[j] = v[j + 1], sv[j] = sv[j + 1], cm[j] = cm[j + 1], cv[j] = cv[j + 1];
+            for (int j = 0; j < 7; ++j) m[j] = m[j + 1], nsv[j] = nsv[j + 1], cm[j] = cm[j + 1], cv[j] = cv[j + 1];
             cm[7] = enc8_m(me, rm);
-            cv[7] = enc8_v(ve, se, rv);
+            cv[7] = enc8_v(se, rv);
         }
     }
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
-    if (lane == 0) t.mq[b0 / kBlk] = q0;
-    if (lane == 16) t.vq[b0 / kBlk] = q0;
+    qmv = make_float2(__shfl_sync(0xFFFFFFFFu, q0, 0), __shfl_sync(0xFFFFFFFFu, q0, 16));
     return bad;
 }
 
-// Each warp takes blocks of 256 elements of its CTA's chunk.  With 8-bit states the whole aligned ones go
-// through adamw_block_fast, the next block's loads under way while one is computed.
+// Each warp takes a run of blocks of its CTA's chunk.  With 8-bit states lane j holds the constants of the run's
+// j-th block from before the first to after the last -- one load and one store of neighbours (read
+// and written block by block, 4 bytes in a sector that other warps write too, they cost more than
+// all the other traffic: 1494 against 595 us at 278M parameters) -- and the whole aligned
+// blocks go through adamw_block_fast, the next one's loads under way while one is computed.
 template <bool kSR, bool kU8>
-__global__ void __launch_bounds__(kThreads, kU8 ? 2 : 3) k_adamw_step(NadamLaunch L, AdamWPrm k) {
-    __shared__ uint32_t red[32];
+__global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamWPrm k) {
+    __shared__ int counted;
+    if (threadIdx.x == 0) counted = 0;
+    __syncthreads();
     const Chunk c = L.chunks[blockIdx.x];
     const TensorRec rec = L.tensors[c.tensor];
     Tensor t;
@@ -421,36 +470,49 @@ __global__ void __launch_bounds__(kThreads, kU8 ? 2 : 3) k_adamw_step(NadamLaunc
     t.g = L.grads[c.tensor];
     t.m = rec.m;
     t.v = rec.v;
-    t.numel = rec.numel;
     t.index = c.tensor;
     t.has_res = (rec.flags & kFlagRes) != 0;
     t.u8 = kU8 && (rec.flags & kFlagSmall) == 0;
-    t.mq = t.u8 ? reinterpret_cast<float*>(static_cast<uint8_t*>(t.m) + u8_scale_offset(t.numel)) : nullptr;
-    t.vq = t.u8 ? reinterpret_cast<float*>(static_cast<uint8_t*>(t.v) + u8_scale_offset(t.numel)) : nullptr;
-    const int64_t start = (int64_t)c.index * L.chunk, end = min(t.numel, start + L.chunk);
+    const int64_t start = (int64_t)c.index * L.chunk, end = min(rec.numel, start + L.chunk);
     const float gs = k.grad_scale ? __ldg(k.grad_scale) : 1.0f;
     const bool aligned = aligned16(t.w) && (!t.has_res || aligned16(t.res)) && aligned16(t.g) && aligned16(t.m) &&
                          aligned16(t.v);
-    constexpr int64_t kStep = (kThreads / 32) * kBlk;
-    int64_t b0 = start + (threadIdx.x >> 5) * kBlk;
+    const int lane = threadIdx.x & 31;
+    const int run = (int)(L.chunk / kThreads * 32 / kBlk);           // blocks to a warp: 1 to 16
+    const int64_t first = start + (int64_t)(threadIdx.x >> 5) * run * kBlk;
+    const int blocks = (int)max((int64_t)0, min((int64_t)run, (end - first + kBlk - 1) / kBlk));
+    float* const mq = reinterpret_cast<float*>(static_cast<uint8_t*>(t.m) + u8_scale_offset(rec.numel)) + first / kBlk + lane;
+    float* const vq = reinterpret_cast<float*>(static_cast<uint8_t*>(t.v) + u8_scale_offset(rec.numel)) + first / kBlk + lane;
+    float2 q = make_float2(0.0f, 0.0f);
+    if (kU8 && t.u8 && lane < blocks) q = make_float2(*mq, *vq);
     uint32_t nf = 0u;
+    int j = 0;
     if (kU8 && t.u8 && aligned) {
-        const int64_t whole = start + (end - start) / kBlk * kBlk;
+        const int whole = (int)((min(end, first + (int64_t)blocks * kBlk) - first) / kBlk);
         float bad = 0.0f;
         Raw x;
-        if (b0 < whole) load_raw(x, t, b0);
-        for (; b0 < whole; b0 += kStep) {
+        if (whole > 0) load_raw(x, t, first);
+        for (; j < whole; ++j) {
             Raw next;
-            if (b0 + kStep < whole) load_raw(next, t, b0 + kStep);
-            bad += adamw_block_fast<kSR>(k, t, gs, b0, x);
+            if (j + 1 < whole) load_raw(next, t, first + (int64_t)(j + 1) * kBlk);
+            float2 qj = make_float2(__shfl_sync(0xFFFFFFFFu, q.x, j), __shfl_sync(0xFFFFFFFFu, q.y, j));
+            bad += adamw_block_fast<kSR>(k, t, gs, first + (int64_t)j * kBlk, x, qj);
+            if (lane == j) q = qj;
             x = next;
         }
         if (bad != 0.0f) nf = 0x7F80u;
     }
-    for (; b0 < end; b0 += kStep) nf = max(nf, adamw_block<kSR, kU8>(k, t, gs, b0, end, aligned));
-    uint32_t r[1] = {nf >= 0x7F80u ? 1u : 0u};
-    block_max_u32<1>(r, red);
-    if (threadIdx.x == 0 && r[0]) atomicAdd(L.nonfinite, 1ull);
+    for (; j < blocks; ++j) {
+        float2 qj = make_float2(__shfl_sync(0xFFFFFFFFu, q.x, j), __shfl_sync(0xFFFFFFFFu, q.y, j));
+        nf = max(nf, adamw_block<kSR, kU8>(k, t, gs, first + (int64_t)j * kBlk, end, aligned, qj));
+        if (lane == j) q = qj;
+    }
+    if (kU8 && t.u8 && lane < blocks) {
+        *mq = q.x;
+        *vq = q.y;
+    }
+    // once per chunk, without a barrier that would hold the CTA's warps for its slowest
+    if (nf >= 0x7F80u && atomicExch(&counted, 1) == 0) atomicAdd(L.nonfinite, 1ull);
 }
 
 // Moments of every tensor as fp32 values, into flat buffers (tensor i at 64 * slot64 elements).
@@ -500,7 +562,9 @@ __global__ void __launch_bounds__(kThreads) k_adamw_unpack(NadamLaunch L, float*
 
 int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& s, bool u8, cudaStream_t stream) {
     if (L.n_chunks_total == 0) return OPTIM_OK;
-    const AdamWPrm k{s.b1, s.omb1, s.b2, s.omb2, s.eps, s.lr_wd, s.k1, s.k2, s.grad_scale, s.step, philox_key(s.seed)};
+    const bool plain_range = s.k1 >= 0x1p-30f && s.k1 <= 0x1p20f && s.k2 >= 1.0f && s.k2 <= 0x1p13f && s.eps <= 1.0f;
+    const AdamWPrm k{s.b1, s.omb1, s.b2, s.omb2, s.eps, s.lr_wd, s.k1, s.k2, s.grad_scale, s.step, plain_range,
+                     philox_key(s.seed)};
     const unsigned grid = (unsigned)L.n_chunks_total;
     if (u8) {
         if (s.sr) k_adamw_step<true, true><<<grid, kThreads, 0, stream>>>(L, k);
