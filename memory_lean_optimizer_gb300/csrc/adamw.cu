@@ -177,7 +177,7 @@ struct Tensor {
 // a block's maximum).  8-bit states: qmv holds the block's constants, old in, new out.  Returns the largest
 // exponent field stored.
 template <bool kSR, bool kU8>
-__device__ __noinline__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, int64_t end, bool aligned,
+__device__ __forceinline__ uint32_t adamw_block(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, int64_t end, bool aligned,
                                              float2& qmv) {
     const int lane = threadIdx.x & 31;
     const int64_t i = b0 + 8 * lane;
@@ -339,11 +339,10 @@ __device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
 //    it lies within 1e-4 of the middle between two, and only a lane that has such a one
 //    (1 in 300) forms its eight codes from the exact roots.
 //  - the block's constants.  Lanes 0-15 compute those of m, lanes 16-31 those of v, in one pass.
-// A block with a moment outside Range (an exact zero, an infinity or a NaN among them) is left to
-// adamw_block as a whole, before anything of it is stored.
-// Returns 0 times the stored weights: NaN if one of them is not finite.
+// A block with a moment outside Range (an exact zero, an infinity or a NaN among them) or a weight that comes
+// out infinite or NaN is left to adamw_block as a whole: false, and nothing of it is stored.
 template <bool kSR>
-__device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, const Raw& x, float2& qmv) {
+__device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor& t, float gs, int64_t b0, const Raw& x, float2& qmv) {
     const int lane = threadIdx.x & 31;
     const int64_t i = b0 + 8 * lane;
     const uint32_t wr[4] = {x.w.x, x.w.y, x.w.z, x.w.w}, rr[4] = {x.r.x, x.r.y, x.r.z, x.r.w};
@@ -400,8 +399,7 @@ __device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tenso
     // minima and maxima pass over a NaN, but it reaches the weight
     const bool plain = k.plain_range && low_v >= Range::v_min && top_v <= Range::v_max && low_m >= Range::m_min &&
                        top_m <= Range::m_max && bad == 0.0f;
-    if (!__all_sync(0xFFFFFFFFu, plain))
-        return adamw_block<kSR, true>(k, t, gs, b0, b0 + kBlk, true, qmv) >= 0x7F80u ? __int_as_float(0x7FC00000) : 0.0f;
+    if (!__all_sync(0xFFFFFFFFu, plain)) return false;
     st_stream(reinterpret_cast<uint4*>(t.w + i), make_uint4(wo[0], wo[1], wo[2], wo[3]));
     if (t.has_res) st_stream(reinterpret_cast<uint4*>(t.res + i), make_uint4(ro[0], ro[1], ro[2], ro[3]));
 
@@ -449,7 +447,7 @@ __device__ __forceinline__ float adamw_block_fast(const AdamWPrm& k, const Tenso
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
     qmv = make_float2(__shfl_sync(0xFFFFFFFFu, q0, 0), __shfl_sync(0xFFFFFFFFu, q0, 16));
-    return bad;
+    return true;
 }
 
 // Each warp takes a run of blocks of its CTA's chunk.  With 8-bit states lane j holds the constants of the run's
@@ -485,24 +483,23 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamW
     float* const vq = reinterpret_cast<float*>(static_cast<uint8_t*>(t.v) + u8_scale_offset(rec.numel)) + first / kBlk + lane;
     float2 q = make_float2(0.0f, 0.0f);
     if (kU8 && t.u8 && lane < blocks) q = make_float2(*mq, *vq);
-    uint32_t nf = 0u;
-    int j = 0;
+    uint32_t done = 0u;   // bit j: block j is finished
     if (kU8 && t.u8 && aligned) {
         const int whole = (int)((min(end, first + (int64_t)blocks * kBlk) - first) / kBlk);
-        float bad = 0.0f;
         Raw x;
         if (whole > 0) load_raw(x, t, first);
-        for (; j < whole; ++j) {
+        for (int j = 0; j < whole; ++j) {
             Raw next;
             if (j + 1 < whole) load_raw(next, t, first + (int64_t)(j + 1) * kBlk);
             float2 qj = make_float2(__shfl_sync(0xFFFFFFFFu, q.x, j), __shfl_sync(0xFFFFFFFFu, q.y, j));
-            bad += adamw_block_fast<kSR>(k, t, gs, first + (int64_t)j * kBlk, x, qj);
+            if (adamw_block_fast<kSR>(k, t, gs, first + (int64_t)j * kBlk, x, qj)) done |= 1u << j;
             if (lane == j) q = qj;
             x = next;
         }
-        if (bad != 0.0f) nf = 0x7F80u;
     }
-    for (; j < blocks; ++j) {
+    uint32_t nf = 0u;
+    for (int j = 0; j < blocks; ++j) {
+        if (done >> j & 1u) continue;
         float2 qj = make_float2(__shfl_sync(0xFFFFFFFFu, q.x, j), __shfl_sync(0xFFFFFFFFu, q.y, j));
         nf = max(nf, adamw_block<kSR, kU8>(k, t, gs, first + (int64_t)j * kBlk, end, aligned, qj));
         if (lane == j) q = qj;
