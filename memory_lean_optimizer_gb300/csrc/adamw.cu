@@ -14,6 +14,7 @@
 // A positive v keeps a code of at least 1: decoded to zero, it would leave a kept m divided by eps
 // alone in a later step whose gradient is zero.
 #include "internal.h"
+#include "packed.cuh"
 
 namespace lmo {
 namespace {
@@ -237,21 +238,6 @@ __device__ __forceinline__ uint32_t adamw_block(const AdamWPrm& k, const Tensor&
     return nf;
 }
 
-// Two fp32 values to an instruction (each rounded as by itself).
-struct F2 {
-    uint64_t x;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.x) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split2(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v.x)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
-    return r;
-}
 // a - b as b times -1 plus a: the product is exact, so the one rounding is the difference's.  Sums are
 // written as differences from a negated operand, with a product only as b: a packed sum of products
 // was seen to come out as one multiply-add in spite of .rn (a sixth of a million random cases of
@@ -268,11 +254,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return y;
 }
 
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.x) : "l"(a.x), "l"(b.x), "l"(c.x));
-    return r;
-}
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "packed.cuh"
 
 namespace lmo {
 namespace {
@@ -87,91 +88,153 @@ struct Vec<float, 8> {
     }
 };
 
-// Sums of N values over the blockDim.x threads that share a row, in every one of them.  One warp: by
-// shuffles alone.  More: each warp leaves its sums in shared memory and, after one barrier, every
-// warp adds them all in the same order; `turn` alternates between two areas, so the next call's
-// writes cannot meet this call's reads (a third call is a barrier away).
+// Sums of N values over the blockDim.x threads that share a row, in every one of them, in a fixed order.
+// One warp: by shuffles alone.  More: each warp leaves its sums in shared memory and, after one
+// barrier, every thread adds them all; `turn` alternates between two areas, so the next call's writes
+// cannot meet this call's reads (a third call is a barrier away).
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*smem)[2][32], int& turn) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*smem)[2][32], int& turn) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = warp_sum_f32(v[i]);
     if (blockDim.x == 32) return;
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) {
+    const int nw = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) smem[turn][i][threadIdx.x >> 5] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum_f32(lane < nw ? smem[turn][i][lane] : 0.0f);
+    for (int i = 0; i < N; ++i) {
+        float s = 0.0f;
+        for (int k = 0; k < nw; k += 4) {   // the areas are zero past the last warp
+            const float4 q = *reinterpret_cast<const float4*>(&smem[turn][i][k]);
+            s += (q.x + q.y) + (q.z + q.w);
+        }
+        v[i] = s;
+    }
     turn ^= 1;
 }
+__device__ __forceinline__ void clear_sums(float (*smem)[2][32]) {
+    if (threadIdx.y == 0)
+        for (int i = threadIdx.x; i < 128; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
+    __syncthreads();
+}
 
-// Forward, the row in registers: blockDim.x threads hold a row as K vectors of V elements each (element
-// (k * blockDim.x + threadIdx.x) * V of it), blockDim.y rows at a time.  x is read once, y written
-// once; the next row is on its way while this one is reduced.
-template <class TX, class TW, int V, int K>
-__global__ void __launch_bounds__(1024) k_norm_forward(const TX* x, int64_t ldx, const TW* __restrict__ w,
-                                                       const TW* __restrict__ b, TX* y, int64_t ldy,
-                                                       float* __restrict__ mean, float* __restrict__ rstd, int64_t rows,
-                                                       int dim, float eps) {
-    __shared__ float red[2][2][32];
+__device__ __forceinline__ float total(F2 p) {
+    float a, b;
+    split2(p, a, b);
+    return a + b;
+}
+
+// What a thread holds of a row is K slices of kWide values.  Rows that can be read in 16-byte vectors (kWide = V
+// values next to each other, element (k * blockDim.x + threadIdx.x) * V on), or not (V = 1): single
+// elements (2k * kT + threadIdx.x) and kT further, kT threads to a row, two to a slice so that the
+// packed instructions serve them as well; the second of the last slice may lie past the row's end.
+template <class T, int V, int kT>
+struct Slice {
+    static constexpr int kWide = V > 1 ? V : 2, n = kWide / 2;
+    static __device__ __forceinline__ int column(int k) {
+        return V > 1 ? (k * (int)blockDim.x + (int)threadIdx.x) * V : 2 * k * kT + (int)threadIdx.x;
+    }
+    Vec<T, V> raw[V > 1 ? 1 : 2];
+    // c: column(k), below dim
+    __device__ __forceinline__ void load(const T* row, int c, int dim) {
+        raw[0].load(row + c);
+        if (V == 1) {
+            raw[V > 1 ? 0 : 1] = Vec<T, V>{};
+            if (c + kT < dim) raw[V > 1 ? 0 : 1].load(row + c + kT);
+        }
+    }
+    __device__ __forceinline__ void get(F2 (&p)[n]) const {
+        float f[V], g[V];
+        raw[0].get(f);
+        raw[V > 1 ? 0 : 1].get(g);
+#pragma unroll
+        for (int i = 0; i < n; ++i) p[i] = V > 1 ? f2(f[2 * i % V], f[(2 * i + 1) % V]) : f2(f[0], g[0]);
+    }
+    static __device__ __forceinline__ void store(T* row, int c, int dim, const F2 (&p)[n]) {
+        float f[V], g[V];
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            if (V > 1) split2(p[i], f[2 * i % V], f[(2 * i + 1) % V]);
+            else split2(p[i], f[0], g[0]);
+        }
+        Vec<T, V>::store(row + c, f);
+        if (V == 1 && c + kT < dim) Vec<T, V>::store(row + c + kT, g);
+    }
+};
+
+// Forward, the row in registers: blockDim.x threads hold a row, blockDim.y rows at a time.  x is read once, y
+// written once; the next row is on its way while this one is reduced.
+template <class TX, class TW, int V, int K, int kT, int kMaxThreads, int kMinCtas>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) k_norm_forward(const TX* x, int64_t ldx, const TW* __restrict__ w,
+                                                                        const TW* __restrict__ b, TX* y, int64_t ldy,
+                                                                        float* __restrict__ mean, float* __restrict__ rstd,
+                                                                        int64_t rows, int dim, float eps) {
+    using S = Slice<TX, V, kT>;
+    __shared__ __align__(16) float red[2][2][32];
+    clear_sums(red);
     const float inv = 1.0f / (float)dim;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int turn = 0;
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    Vec<TX, V> raw[K];
+    const TX* px = x + r * ldx;
+    S raw[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (r < rows && c < dim) raw[k].load(x + r * ldx + c);
+        const int c = S::column(k);
+        if (r < rows && c < dim) raw[k].load(px, c, dim);
     }
     for (; r < rows; r += step) {
-        float f[K][V];
-        float s[1] = {0.0f};
+        F2 f[K][S::n];
+        F2 acc = f2(0.0f, 0.0f);
+        px += step * ldx;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+            const int c = S::column(k);
             if (c < dim) {
                 raw[k].get(f[k]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s[0] += f[k][e];
-                if (r + step < rows) raw[k].load(x + (r + step) * ldx + c);
+                for (int i = 0; i < S::n; ++i) acc = add2(acc, f[k][i]);
+                if (r + step < rows) raw[k].load(px, c, dim);
             }
         }
-        row_sum(s, red, turn);
+        float s[1] = {total(acc)};
+        row_sums(s, red, turn);
         const float mu = s[0] * inv;
-        s[0] = 0.0f;
+        const F2 n_mu = f2(-mu, -mu);
+        acc = f2(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+            const int c = S::column(k);
             if (c < dim) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    f[k][e] -= mu;
-                    s[0] = fmaf(f[k][e], f[k][e], s[0]);
+                for (int i = 0; i < S::n; ++i) {
+                    f[k][i] = add2(f[k][i], V > 1 || c + kT < dim ? n_mu : f2(-mu, 0.0f));   // past the end: stays 0
+                    acc = fma2(f[k][i], f[k][i], acc);
                 }
             }
         }
-        row_sum(s, red, turn);
+        s[0] = total(acc);
+        row_sums(s, red, turn);
         const float rs = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+        const F2 rs2 = f2(rs, rs);
+        TX* const py = y + r * ldy;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+            const int c = S::column(k);
             if (c < dim) {
-                Vec<TW, V> wv, bv;
-                float wf[V], bf[V];
-                wv.load(w + c);
-                wv.get(wf);
-#pragma unroll
-                for (int e = 0; e < V; ++e) bf[e] = 0.0f;
+                Slice<TW, V, kT> raw_w, raw_b;
+                F2 wv[S::n], bv[S::n];
+                raw_w.load(w, c, dim);
+                raw_w.get(wv);
                 if (b) {
-                    bv.load(b + c);
-                    bv.get(bf);
+                    raw_b.load(b, c, dim);
+                    raw_b.get(bv);
                 }
 #pragma unroll
-                for (int e = 0; e < V; ++e) f[k][e] = fmaf(f[k][e] * rs, wf[e], bf[e]);
-                Vec<TX, V>::store(y + r * ldy + c, f[k]);
+                for (int i = 0; i < S::n; ++i) f[k][i] = fma2(mul2(f[k][i], rs2), wv[i], b ? bv[i] : f2(0.0f, 0.0f));
+                S::store(py, c, dim, f[k]);
             }
         }
         if (threadIdx.x == 0) {
@@ -184,111 +247,112 @@ __global__ void __launch_bounds__(1024) k_norm_forward(const TX* x, int64_t ldx,
 // Backward with everything in one pass: x and dy are read once, dx written once, and each thread
 // keeps the sums of dy xh and dy of its own columns over all of its CTA's rows, so that the weight's
 // gradient costs no second reading -- one fp32 row of each per CTA at the end (partial[CTA][2][dim],
-// joined by k_norm_join in CTA order).
-template <class TX, class TW, int V, int K, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_backward(const TX* dy, int64_t lddy, const TX* x, int64_t ldx,
-                                                               const TW* __restrict__ w, const float* __restrict__ mean,
-                                                               const float* __restrict__ rstd, TX* dx, int64_t lddx,
-                                                               float* __restrict__ partial, int64_t rows, int dim) {
-    __shared__ float red[2][2][32];
+// joined by k_norm_join in CTA order).  kAhead: the next row is on its way while this one is reduced
+// (where the registers allow it).
+template <class TX, class TW, int V, int K, int kT, int kMaxThreads, bool kAhead>
+__global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward(const TX* dy, int64_t lddy, const TX* x, int64_t ldx,
+                                                                  const TW* __restrict__ w, const float* __restrict__ mean,
+                                                                  const float* __restrict__ rstd, TX* dx, int64_t lddx,
+                                                                  float* __restrict__ partial, int64_t rows, int dim) {
+    using S = Slice<TX, V, kT>;
+    __shared__ __align__(16) float red[2][2][32];
     extern __shared__ float cols[];   // [2][dim], only when blockDim.y > 1
-    constexpr bool kPre = K * V <= 16;   // the next row on its way: more would not fit in registers
+    clear_sums(red);
     const float inv = 1.0f / (float)dim;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int turn = 0;
-    float aw[K][V], ab[K][V], wf[K][V];
-    Vec<TX, V> rx[K], rg[K];
+    F2 aw[K][S::n], ab[K][S::n], wv[K][S::n];
+    S rx[K], rg[K];
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const TX* px = x + r * ldx;
+    const TX* pg = dy + r * lddy;
     float mu = 0.0f, rs = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+        const int c = S::column(k);
 #pragma unroll
-        for (int e = 0; e < V; ++e) aw[k][e] = ab[k][e] = 0.0f;
+        for (int i = 0; i < S::n; ++i) aw[k][i] = ab[k][i] = wv[k][i] = f2(0.0f, 0.0f);
         if (c < dim) {
-            Vec<TW, V> wv;
-            wv.load(w + c);
-            wv.get(wf[k]);
-            if (kPre && r < rows) {
-                rx[k].load(x + r * ldx + c);
-                rg[k].load(dy + r * lddy + c);
+            Slice<TW, V, kT> raw_w;
+            raw_w.load(w, c, dim);
+            raw_w.get(wv[k]);
+            if (kAhead && r < rows) {
+                rx[k].load(px, c, dim);
+                rg[k].load(pg, c, dim);
             }
         }
     }
-    if (kPre && r < rows) {
-        mu = mean[r];
-        rs = rstd[r];
-    }
+    if (kAhead && r < rows) mu = mean[r], rs = rstd[r];
     for (; r < rows; r += step) {
-        if (!kPre) {
-            mu = mean[r];
-            rs = rstd[r];
+        if (!kAhead) {
+            mu = mean[r], rs = rstd[r];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+                const int c = S::column(k);
                 if (c < dim) {
-                    rx[k].load(x + r * ldx + c);
-                    rg[k].load(dy + r * lddy + c);
+                    rx[k].load(px, c, dim);
+                    rg[k].load(pg, c, dim);
                 }
             }
         }
-        Vec<TX, V> nx[K], ng[K];
+        px += step * ldx;
+        pg += step * lddy;
+        S nx[K], ng[K];
         float nmu = 0.0f, nrs = 0.0f;
-        if (kPre && r + step < rows) {
-            nmu = mean[r + step];
-            nrs = rstd[r + step];
+        if (kAhead && r + step < rows) {
+            nmu = mean[r + step], nrs = rstd[r + step];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+                const int c = S::column(k);
                 if (c < dim) {
-                    nx[k].load(x + (r + step) * ldx + c);
-                    ng[k].load(dy + (r + step) * lddy + c);
+                    nx[k].load(px, c, dim);
+                    ng[k].load(pg, c, dim);
                 }
             }
         }
-        float s[2] = {0.0f, 0.0f};
+        const F2 n_mu = f2(-mu, -mu), rs2 = f2(rs, rs);
+        F2 sa = f2(0.0f, 0.0f), sx = sa;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
-            if (c < dim) {
-                float fx[V], fg[V];
-                rx[k].get(fx);
-                rg[k].get(fg);
+            if (S::column(k) < dim) {
+                F2 vx[S::n], vg[S::n];   // past the end dy is 0 and adds nothing
+                rx[k].get(vx);
+                rg[k].get(vg);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (fx[e] - mu) * rs, a = fg[e] * wf[k][e];
-                    aw[k][e] = fmaf(fg[e], xh, aw[k][e]);
-                    ab[k][e] += fg[e];
-                    s[0] += a;
-                    s[1] = fmaf(a, xh, s[1]);
+                for (int i = 0; i < S::n; ++i) {
+                    const F2 xh = mul2(add2(vx[i], n_mu), rs2), a = mul2(vg[i], wv[k][i]);
+                    aw[k][i] = fma2(vg[i], xh, aw[k][i]);
+                    ab[k][i] = add2(ab[k][i], vg[i]);
+                    sa = add2(sa, a);
+                    sx = fma2(a, xh, sx);
                 }
             }
         }
         if (dx) {   // uniform: the barrier inside is reached by all threads or none
-            row_sum(s, red, turn);
-            const float m1 = s[0] * inv, m2 = s[1] * inv;
+            float s[2] = {total(sa), total(sx)};
+            row_sums(s, red, turn);
+            const F2 m1 = f2(-s[0] * inv, -s[0] * inv), m2 = f2(-s[1] * inv, -s[1] * inv);
+            TX* const pd = dx + r * lddx;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V;
+                const int c = S::column(k);
                 if (c < dim) {
-                    float fx[V], fg[V];
-                    rx[k].get(fx);
-                    rg[k].get(fg);
+                    F2 vx[S::n], vg[S::n];
+                    rx[k].get(vx);
+                    rg[k].get(vg);
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        fg[e] = rs * (fmaf(-((fx[e] - mu) * rs), m2, fg[e] * wf[k][e]) - m1);
-                    Vec<TX, V>::store(dx + r * lddx + c, fg);
+                    for (int i = 0; i < S::n; ++i) {
+                        const F2 xh = mul2(add2(vx[i], n_mu), rs2), a = mul2(vg[i], wv[k][i]);
+                        vg[i] = mul2(add2(fma2(xh, m2, a), m1), rs2);
+                    }
+                    S::store(pd, c, dim, vg);
                 }
             }
         }
-        if (kPre) {
-            mu = nmu;
-            rs = nrs;
+        if (kAhead) {
+            mu = nmu, rs = nrs;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                rx[k] = nx[k];
-                rg[k] = ng[k];
-            }
+            for (int k = 0; k < K; ++k) rx[k] = nx[k], rg[k] = ng[k];
         }
     }
     if (!partial) return;
@@ -298,14 +362,19 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(const TX* dy, int
             const bool last = turn_y + 1 == (int)blockDim.y;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
+                const int c = S::column(k);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int c = (k * (int)blockDim.x + (int)threadIdx.x) * V + e;
-                    if (c < dim) {
-                        const float pw = turn_y ? cols[c] + aw[k][e] : aw[k][e];
-                        const float pb = turn_y ? cols[dim + c] + ab[k][e] : ab[k][e];
-                        (last ? out : cols)[c] = pw;
-                        (last ? out : cols)[dim + c] = pb;
+                for (int i = 0; i < S::n; ++i) {
+                    float w2[2], b2[2];
+                    split2(aw[k][i], w2[0], w2[1]);
+                    split2(ab[k][i], b2[0], b2[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at = V > 1 ? c + 2 * i + e : c + e * kT;
+                        if (at < dim) {
+                            (last ? out : cols)[at] = turn_y ? cols[at] + w2[e] : w2[e];
+                            (last ? out : cols)[dim + at] = turn_y ? cols[dim + at] + b2[e] : b2[e];
+                        }
                     }
                 }
             }
@@ -324,6 +393,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_join(const float* __restrict_
     const int64_t j = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.0f;
     if (j < 2 * dim)
+#pragma unroll 8
         for (int k = ty; k < slices; k += 8) s += partial[(int64_t)k * 2 * dim + j];
     red[ty][tx] = s;
     __syncthreads();
@@ -439,34 +509,26 @@ unsigned row_grid(int64_t rows) { return (unsigned)std::min<int64_t>(rows, (int6
 
 bool rows_aligned(const void* p, int64_t ld, size_t elem) { return is_aligned(p, 16) && (size_t)ld * elem % 16 == 0; }
 
-// How a row is laid over threads: V elements a vector, K vectors a thread, tx threads, ty rows a CTA.
+// How a row is laid over threads: K slices a thread (Slice), tx threads a row, ty rows a CTA.
 struct RowShape {
     int V = 0, K = 0, tx = 0, ty = 1;   // K = 0: too long
 };
-// Few threads with several vectors each keep a row inside one warp where it fits (no barrier);
-// above that two vectors each -- enough loads in flight, and room in the registers for the next
-// row -- up to `max_threads`, then four.  Rows that cannot be read in 16-byte vectors (odd width,
-// stride or start) take single elements, eight or sixteen a thread.
-RowShape row_shape(int64_t dim, int vec, bool aligned, int max_threads) {
-    RowShape s;
-    s.V = aligned && dim % vec == 0 ? vec : 1;
-    const int64_t units = dim / s.V;
-    const int k_warp = s.V > 1 ? 4 : 8, k_few = s.V > 1 ? 2 : 8, k_many = s.V > 1 ? 4 : 16;
-    if (units <= 32 * k_warp) {
-        s.K = k_warp;
-        s.tx = 32;
-        s.ty = 4;
-        return s;
+// Two 16-byte vectors a thread up to 512 threads, then four.  One vector shares what a thread does for a row besides
+// its values (the trees, the addresses, the root) among too few of them, and with four the
+// registers leave too few threads on an SM: 16384 x 4096 bf16, forward / backward, one 78 / 109,
+// two 64 / 86, four 73 / 115 us; 8192 x 4096 fp32, two 63 / 80, four 68 / 124 us.  A row inside one
+// warp, where it fits, needs no barrier.
+RowShape row_shape(int64_t dim, int vec, bool aligned) {
+    if (aligned && dim % vec == 0) {
+        const int64_t units = dim / vec;
+        if (units <= 128) return {vec, 4, 32, 4};
+        for (int k : {2, 4})
+            if (units <= 512 * k) return {vec, k, (int)((units + 32 * k - 1) / (32 * k) * 32), 1};
+        return {};
     }
-    for (int k : {k_few, k_many}) {
-        const int64_t t = (units + k - 1) / k;
-        if (t <= max_threads) {
-            s.K = k;
-            s.tx = (int)((t + 31) / 32 * 32);
-            return s;
-        }
-    }
-    return s;
+    for (int t : {32, 64, 128, 256, 512})
+        if (dim <= 16 * t) return {1, 8, t, t == 32 ? 4 : 1};
+    return {};
 }
 
 // CTAs of one kernel that fit on the GPU at once.
@@ -477,9 +539,9 @@ int64_t resident(F kernel, int threads, size_t smem) {
     return (int64_t)per_sm * sm_count();
 }
 
-template <class TX, class TW, int V, int K>
+template <class TX, class TW, int V, int K, int kT, int kMax, int kMin>
 int forward_rows(const NormForward& a, const RowShape& sh, cudaStream_t s) {
-    auto kernel = k_norm_forward<TX, TW, V, K>;
+    auto kernel = k_norm_forward<TX, TW, V, K, kT, kMax, kMin>;
     const int64_t grid = std::min((a.rows + sh.ty - 1) / sh.ty, resident(kernel, sh.tx * sh.ty, 0));
     kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), 0, s>>>(
         static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias),
@@ -492,11 +554,15 @@ int forward_t(const NormForward& a, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(TX);
     const bool aligned = rows_aligned(a.x, a.ldx, sizeof(TX)) && rows_aligned(a.y, a.ldy, sizeof(TX)) &&
                          is_aligned(a.weight, 16) && is_aligned(a.bias, 16);
-    const RowShape sh = row_shape(a.dim, kVec, aligned, 1024);
-    if (sh.V > 1 && sh.K == 2) return forward_rows<TX, TW, kVec, 2>(a, sh, s);
-    if (sh.V > 1 && sh.K == 4) return forward_rows<TX, TW, kVec, 4>(a, sh, s);
-    if (sh.V == 1 && sh.K == 8) return forward_rows<TX, TW, 1, 8>(a, sh, s);
-    if (sh.V == 1 && sh.K == 16) return forward_rows<TX, TW, 1, 16>(a, sh, s);
+    const RowShape sh = row_shape(a.dim, kVec, aligned);
+    if (sh.V > 1 && sh.tx == 32) return forward_rows<TX, TW, kVec, 4, 0, 128, 4>(a, sh, s);
+    if (sh.V > 1 && sh.K == 2) return forward_rows<TX, TW, kVec, 2, 0, 512, 2>(a, sh, s);
+    if (sh.V > 1 && sh.K == 4) return forward_rows<TX, TW, kVec, 4, 0, 512, 1>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 32) return forward_rows<TX, TW, 1, 8, 32, 128, 4>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 64) return forward_rows<TX, TW, 1, 8, 64, 64, 8>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 128) return forward_rows<TX, TW, 1, 8, 128, 128, 5>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 256) return forward_rows<TX, TW, 1, 8, 256, 256, 2>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 512) return forward_rows<TX, TW, 1, 8, 512, 512, 1>(a, sh, s);
     k_norm_forward_long<TX, TW><<<row_grid(a.rows), kThreads, 0, s>>>(
         static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias),
         static_cast<TX*>(a.y), a.ldy, a.mean, a.rstd, a.rows, a.dim, a.eps);
@@ -510,9 +576,9 @@ int join_slices(const NormBackward& a, int slices, cudaStream_t s) {
     return check_cuda(cudaGetLastError(), "layer norm weight gradient launch");
 }
 
-template <class TX, class TW, int V, int K>
+template <class TX, class TW, int V, int K, int kT, int kMax, bool kAhead>
 int backward_rows(const NormBackward& a, const RowShape& sh, cudaStream_t s) {
-    auto kernel = k_norm_backward<TX, TW, V, K, 512>;
+    auto kernel = k_norm_backward<TX, TW, V, K, kT, kMax, kAhead>;
     const bool sums = a.dweight || a.dbias;
     const size_t smem = sh.ty > 1 ? 2 * sizeof(float) * (size_t)a.dim : 0;
     const int64_t grid = std::max<int64_t>(1, std::min({(a.rows + sh.ty - 1) / sh.ty, (int64_t)kMaxSlices,
@@ -529,11 +595,15 @@ int backward_t(const NormBackward& a, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(TX);
     const bool aligned = rows_aligned(a.x, a.ldx, sizeof(TX)) && rows_aligned(a.dy, a.lddy, sizeof(TX)) &&
                          (!a.dx || rows_aligned(a.dx, a.lddx, sizeof(TX))) && is_aligned(a.weight, 16);
-    const RowShape sh = row_shape(a.dim, kVec, aligned, 512);
-    if (sh.V > 1 && sh.K == 2) return backward_rows<TX, TW, kVec, 2>(a, sh, s);
-    if (sh.V > 1 && sh.K == 4) return backward_rows<TX, TW, kVec, 4>(a, sh, s);
-    if (sh.V == 1 && sh.K == 8) return backward_rows<TX, TW, 1, 8>(a, sh, s);
-    if (sh.V == 1 && sh.K == 16) return backward_rows<TX, TW, 1, 16>(a, sh, s);
+    const RowShape sh = row_shape(a.dim, kVec, aligned);
+    if (sh.V > 1 && sh.tx == 32) return backward_rows<TX, TW, kVec, 4, 0, 128, true>(a, sh, s);
+    if (sh.V > 1 && sh.K == 2) return backward_rows<TX, TW, kVec, 2, 0, 512, true>(a, sh, s);
+    if (sh.V > 1 && sh.K == 4) return backward_rows<TX, TW, kVec, 4, 0, 512, false>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 32) return backward_rows<TX, TW, 1, 8, 32, 128, true>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 64) return backward_rows<TX, TW, 1, 8, 64, 64, true>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 128) return backward_rows<TX, TW, 1, 8, 128, 128, true>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 256) return backward_rows<TX, TW, 1, 8, 256, 256, true>(a, sh, s);
+    if (sh.V == 1 && sh.tx == 512) return backward_rows<TX, TW, 1, 8, 512, 512, false>(a, sh, s);
     const TX* dy = static_cast<const TX*>(a.dy);
     const TX* x = static_cast<const TX*>(a.x);
     if (a.dweight || a.dbias) {   // before dx, which may lie over dy
