@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "packed.cuh"
@@ -531,18 +532,27 @@ RowShape row_shape(int64_t dim, int vec, bool aligned) {
     return {};
 }
 
-// CTAs of one kernel that fit on the GPU at once.
+// CTAs of one kernel that fit on the GPU at once, `wanted` at most.  `last` (one per kernel) remembers the answer for
+// the last shape, threads << 48 | smem << 16 | CTAs an SM: the query costs as much as a launch.
 template <class F>
-int64_t resident(F kernel, int threads, size_t smem) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
-    return (int64_t)per_sm * sm_count();
+int64_t resident(F kernel, int threads, size_t smem, int64_t wanted, std::atomic<uint64_t>& last) {
+    if (wanted <= sm_count()) return wanted;
+    const uint64_t shape = (uint64_t)threads << 48 | (uint64_t)smem << 16;
+    uint64_t known = last.load(std::memory_order_relaxed);
+    if ((known & ~(uint64_t)0xFFFF) != shape || (known & 0xFFFF) == 0) {
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1) per_sm = 1;
+        known = shape | (uint64_t)per_sm;
+        last.store(known, std::memory_order_relaxed);
+    }
+    return std::min<int64_t>(wanted, (int64_t)(known & 0xFFFF) * sm_count());
 }
 
 template <class TX, class TW, int V, int K, int kT, int kMax, int kMin>
 int forward_rows(const NormForward& a, const RowShape& sh, cudaStream_t s) {
     auto kernel = k_norm_forward<TX, TW, V, K, kT, kMax, kMin>;
-    const int64_t grid = std::min((a.rows + sh.ty - 1) / sh.ty, resident(kernel, sh.tx * sh.ty, 0));
+    static std::atomic<uint64_t> last{0};
+    const int64_t grid = resident(kernel, sh.tx * sh.ty, 0, (a.rows + sh.ty - 1) / sh.ty, last);
     kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), 0, s>>>(
         static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias),
         static_cast<TX*>(a.y), a.ldy, a.mean, a.rstd, a.rows, (int)a.dim, a.eps);
@@ -581,8 +591,9 @@ int backward_rows(const NormBackward& a, const RowShape& sh, cudaStream_t s) {
     auto kernel = k_norm_backward<TX, TW, V, K, kT, kMax, kAhead>;
     const bool sums = a.dweight || a.dbias;
     const size_t smem = sh.ty > 1 ? 2 * sizeof(float) * (size_t)a.dim : 0;
-    const int64_t grid = std::max<int64_t>(1, std::min({(a.rows + sh.ty - 1) / sh.ty, (int64_t)kMaxSlices,
-                                                        resident(kernel, sh.tx * sh.ty, smem)}));
+    static std::atomic<uint64_t> last{0};
+    const int64_t wanted = std::min<int64_t>((a.rows + sh.ty - 1) / sh.ty, kMaxSlices);
+    const int64_t grid = std::max<int64_t>(1, resident(kernel, sh.tx * sh.ty, smem, wanted, last));
     kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), smem, s>>>(
         static_cast<const TX*>(a.dy), a.lddy, static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), a.mean,
         a.rstd, static_cast<TX*>(a.dx), a.lddx, sums ? a.partial : nullptr, a.rows, (int)a.dim);

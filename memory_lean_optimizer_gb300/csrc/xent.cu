@@ -62,11 +62,11 @@ struct ProductArgs {
     int32_t first, last;        // kHidden: the first piece (nothing to add to), the last (dH itself; not if K is split)
     uint16_t* dh;               // kHidden
     int64_t lddh;
-    int32_t dh_aligned;         // rows of dH start on 16 bytes
+    int32_t dh_aligned;         // bytes that every row of dH starts on a multiple of: 32, 4 or 2
     const int32_t* row_of;      // kHidden: gathered row -> row of dH
     uint16_t* dw;               // kWeight: dW, row b_off + m
     int64_t lddw;
-    int32_t dw_aligned;         // kWeight: rows of dW start on 16 bytes
+    int32_t dw_aligned;         // kWeight: the same of dW
 };
 
 // Programmatic dependent launch: the kernels of a call start while their predecessor drains and wait
@@ -86,6 +86,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// 16 bf16 values (8 words) to 32 bytes: a whole sector in one store.
+__device__ __forceinline__ void store_32b(uint16_t* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Loads one K block of an operand: `rows` rows of M or N from `mn`, 64 of K from `k`.
@@ -330,14 +337,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                         r[j] = __float_as_uint(live && j < left ? x * g : 0.0f);
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 o;
-                        o.x = bf16_pair(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]));
-                        o.y = bf16_pair(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
-                        o.z = bf16_pair(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
-                        o.w = bf16_pair(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
-                        *reinterpret_cast<uint4*>(out + c + 8 * q) = o;
-                    }
+                    for (int j = 0; j < 32; j += 2) r[j / 2] = bf16_pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                    store_32b(out + c, r);
+                    store_32b(out + c + 16, r + 8);
                 }
                 release();
                 continue;
@@ -348,7 +350,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                                                      : (p.v_off + row < p.vocab ? p.v_off + row : -1);
             uint16_t* const out_base = kMode == kHidden ? p.dh : p.dw;
             const int64_t ld = kMode == kHidden ? p.lddh : p.lddw;
-            const bool aligned = kMode == kHidden ? p.dh_aligned : p.dw_aligned;
+            const bool aligned = (kMode == kHidden ? p.dh_aligned : p.dw_aligned) == 32;
+            const bool words = (kMode == kHidden ? p.dh_aligned : p.dw_aligned) >= 4;
             const float g = sums ? 1.0f : p.head->grad_scale;
             float* const part = kMode == kHidden ? p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + c0 : nullptr;
 #pragma unroll 1
@@ -387,18 +390,29 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 if (aligned && left >= 32) {
                     if (out_row >= 0) {
                         uint16_t* const o = out_base + out_row * ld + c0 + c;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4*>(o + 8 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                        store_32b(o, r);
+                        store_32b(o + 16, r + 8);
                     }
                 } else {   // through shared memory, so that a warp writes 32 neighbours of one row at a time
 #pragma unroll
                     for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(&stage[lane][2 * j]) = r[j];
                     __syncwarp();
-#pragma unroll 1
-                    for (int i = 0; i < 32; ++i) {
-                        const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
-                        if (to >= 0 && lane < left) out_base[to * ld + c0 + c + lane] = stage[i][lane];
+                    if (words) {           // rows start on 4 bytes: half a warp to a row, two elements a lane
+                        const int l = 2 * (lane & 15);
+#pragma unroll 4
+                        for (int i = lane >> 4; i < 32; i += 2) {
+                            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
+                            const uint32_t x = *reinterpret_cast<const uint32_t*>(&stage[i][l]);
+                            uint16_t* const o = out_base + to * ld + c0 + c + l;
+                            if (to >= 0 && l + 1 < left) *reinterpret_cast<uint32_t*>(o) = x;
+                            else if (to >= 0 && l < left) *o = (uint16_t)x;
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int i = 0; i < 32; ++i) {
+                            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
+                            if (to >= 0 && lane < left) out_base[to * ld + c0 + c + lane] = stage[i][lane];
+                        }
                     }
                 }
                 __syncwarp();
@@ -561,16 +575,19 @@ __global__ void __launch_bounds__(kThreads) k_xent_rows(const RowArgs a) {
     }
 }
 
-// Rows of the weight that TMA cannot address (16-byte steps) copied side by side.
+// Rows of the weight that TMA cannot address (16-byte steps) copied side by side.  The first piece is copied
+// beside the gathering of the rows, which has nothing to do with it; later ones wait for the
+// products that read the piece before.
 __global__ void __launch_bounds__(kThreads) k_xent_pack(const uint16_t* __restrict__ src, int64_t lds, uint16_t* __restrict__ dst,
-                                                        int64_t ldd, int64_t rows, int dim) {
-    pdl_sync();
+                                                        int64_t ldd, int64_t rows, int dim, bool first) {
+    if (!first) pdl_sync();
     const int vecs = (int)(ldd / 8);
     const int64_t n = rows * vecs, step = (int64_t)gridDim.x * kThreads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
         const int64_t row = i / vecs;
         *reinterpret_cast<uint4*>(dst + 8 * i) = load_row8(src + row * lds, (int)(i - row * vecs) * 8, dim);
     }
+    if (first) pdl_sync();
 }
 
 // Joins a row's (maximum, sum) pairs of all 128-word tiles: 8 rows a CTA, 32 threads a row, a fixed order.
@@ -650,6 +667,11 @@ __global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, 
 
 // ---- host -------------------------------------------------------------------------------------
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+int row_alignment(const void* p, int64_t ld) {
+    if (is_aligned(p, 32) && ld % 16 == 0) return 32;
+    return is_aligned(p, 4) && ld % 2 == 0 ? 4 : 2;
+}
 
 // Sizes and workspace layout of a call.
 struct XentPlan {
@@ -832,10 +854,10 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     p.row_of = row_of;
     p.dh = static_cast<uint16_t*>(c.d_hidden);
     p.lddh = c.lddh;
-    p.dh_aligned = is_aligned(c.d_hidden, 16) && c.lddh % 8 == 0;
+    p.dh_aligned = row_alignment(c.d_hidden, c.lddh);
     p.dw = static_cast<uint16_t*>(c.d_weight);
     p.lddw = c.lddw;
-    p.dw_aligned = is_aligned(c.d_weight, 16) && c.lddw % 8 == 0;
+    p.dw_aligned = row_alignment(c.d_weight, c.lddw);
     const int row_tiles = (int)(pl.rows_pad / (128 * pl.cta)), dim_tiles = (int)((c.dim + kTileN - 1) / kTileN);
     const int dim_blocks = (int)((c.dim + kTileK - 1) / kTileK);
     const int box_b = kTileN / pl.cta;
@@ -852,7 +874,7 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
         if (pl.pack_w) {   // the piece's rows, side by side; the maps then start at the piece
             uint16_t* const wc = reinterpret_cast<uint16_t*>(ws + pl.wc);
             rc = check_cuda(launch_after(k_xent_pack, std::min<int64_t>(width, (int64_t)sm_count() * 8), kThreads, 0, 1, s,
-                                         w + v0 * c.ldw, c.ldw, wc, pl.ldh, width, (int)c.dim), "weight copy launch");
+                                         w + v0 * c.ldw, c.ldw, wc, pl.ldh, width, (int)c.dim, v0 == 0), "weight copy launch");
             w = wc;
         }
         if (!rc && (pl.pack_w || v0 == 0)) {

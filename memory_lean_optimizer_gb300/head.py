@@ -59,6 +59,11 @@ def _vector(t: torch.Tensor, n: int, like: torch.Tensor, dtype, name: str) -> to
     return t if t.is_contiguous() else t.contiguous()
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(rows: int, dim: int) -> int:
+    return lmopt.norm_layer_workspace(rows, dim)
+
+
 @_on_stream
 def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
     """(y, mean, rstd) of the layer norm over x's last dimension; mean and rstd are fp32, one per row."""
@@ -69,7 +74,7 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     if bias is not None:
         bias = _vector(bias, dim, x, weight.dtype, "bias")
     y = x.new_empty(x.shape)
-    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
+    mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind(0)
     lmopt.norm_layer_forward(m.data_ptr(), m.stride(0), weight.data_ptr(), None if bias is None else bias.data_ptr(),
                              y.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim, eps, xt, wt,
                              _stream_ptr(None))
@@ -89,7 +94,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     mean, rstd = _vector(mean, rows, x, torch.float32, "mean"), _vector(rstd, rows, x, torch.float32, "rstd")
     dx = x.new_empty(x.shape)
     dweight, dbias = weight.new_empty(dim), weight.new_empty(dim)
-    nbytes = lmopt.norm_layer_workspace(rows, dim)
+    nbytes = _norm_bytes(rows, dim)
     work = x.new_empty(nbytes, dtype=torch.uint8)
     lmopt.norm_layer_backward(g.data_ptr(), g.stride(0), m.data_ptr(), m.stride(0), weight.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), dx.data_ptr(), dim, dweight.data_ptr(), dbias.data_ptr(), rows, dim,
@@ -129,14 +134,20 @@ def _xent_args(hidden, weight, target):
     return h, w, target if target.dim() == 1 and target.is_contiguous() else target.reshape(-1).contiguous()
 
 
+@functools.lru_cache(maxsize=256)
+def _xent_bytes(rows: int, dim: int, vocab: int, off16: int, ldw: int, backward: bool) -> int:
+    """Scratch bytes; of the weight's address only its place within 16 bytes counts."""
+    return lmopt.loss_xent_workspace(rows, dim, vocab, 256 + off16, ldw, backward)
+
+
 @_on_stream
 def xent_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, ignore_index: int = -100):
     """(loss, lse), fp32, one per row of hidden: the softmax cross entropy of hidden @ weight.T against target,
     and the log of the softmax's denominator.  Rows with ignore_index have 0 for both."""
     h, w, t = _xent_args(hidden, weight, target)
     (rows, dim), vocab = h.shape, w.shape[0]
-    loss, lse = h.new_empty(target.shape, dtype=torch.float32), h.new_empty(target.shape, dtype=torch.float32)
-    nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), False)
+    loss, lse = h.new_empty((2, *target.shape), dtype=torch.float32).unbind(0)
+    nbytes = _xent_bytes(rows, dim, vocab, w.data_ptr() % 16, w.stride(0), False)
     work = h.new_empty(nbytes, dtype=torch.uint8)
     lmopt.loss_xent_forward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), rows, dim, vocab,
                             ignore_index, loss.data_ptr(), lse.data_ptr(), work.data_ptr(), nbytes, _stream_ptr(None))
@@ -153,7 +164,7 @@ def xent_backward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tens
               for x, n in ((lse, "lse"), (grad_loss, "grad_loss")))
     dh = h.new_empty(hidden.shape) if need_hidden else None
     dw = w.new_empty(weight.shape) if need_weight else None
-    nbytes = lmopt.loss_xent_workspace(rows, dim, vocab, w.data_ptr(), w.stride(0), True)
+    nbytes = _xent_bytes(rows, dim, vocab, w.data_ptr() % 16, w.stride(0), True)
     work = h.new_empty(nbytes, dtype=torch.uint8)
     lmopt.loss_xent_backward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), lse.data_ptr(),
                              g.data_ptr(), rows, dim, vocab, ignore_index, None if dh is None else dh.data_ptr(), dim,
