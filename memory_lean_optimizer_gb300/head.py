@@ -199,3 +199,20 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, target: tor
         return loss
     total = loss.sum()
     return total if reduction == "sum" else total / (target != ignore_index).sum().clamp(min=1)
+
+
+class LMTail(torch.nn.Module):
+    """The last layers of a language model: layer norm, output matrix, cross entropy.  forward gives the loss of
+    hidden states [..., dim] against targets [...]; neither it nor its backward pass holds logits."""
+
+    def __init__(self, dim: int, vocab: int, eps: float = 1e-5, ignore_index: int = -100, device="cuda"):
+        super().__init__()
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        self.norm_weight = torch.nn.Parameter(torch.ones(dim, **bf16))
+        self.norm_bias = torch.nn.Parameter(torch.zeros(dim, **bf16))
+        self.weight = torch.nn.Parameter(torch.randn(vocab, dim, **bf16) * dim ** -0.5)
+        self.eps, self.ignore_index = eps, ignore_index
+
+    def forward(self, hidden: torch.Tensor, target: torch.Tensor, reduction: str = "mean") -> torch.Tensor:
+        y = layer_norm(hidden, self.norm_weight, self.norm_bias, self.eps)
+        return linear_cross_entropy(y, self.weight, target, self.ignore_index, reduction)
