@@ -50,10 +50,14 @@ __device__ __forceinline__ uint32_t store_bits(float w1, bool has_res, uint32_t 
 
 __device__ __forceinline__ int64_t u8_scale_offset(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
-// Byte k of a word as a float, minus `bias` (2^23 plus the code's zero point).
+// Byte k of a word in the mantissa of 2^23, and as a float, minus `bias` (2^23 plus the code's zero point).
+template <int kB>
+__device__ __forceinline__ float byte_in_2p23(uint32_t word) {
+    return __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440 | kB));
+}
 template <int kB>
 __device__ __forceinline__ float byte_to_f32(uint32_t word, float bias) {
-    return __fsub_rn(__uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440 | kB)), bias);
+    return __fsub_rn(byte_in_2p23<kB>(word), bias);
 }
 __device__ __forceinline__ float dec8_m(float c, float q) {
     const float t = __fmul_rn(c, q);
@@ -287,6 +291,12 @@ __device__ __forceinline__ F2 neg_sqrt2(F2 nx) {
     h = fma2(h, e, h);
     return fma2(fma2(ng, ng, nx), h, ng);
 }
+// (-a, sqrt(-b)): the first moment's constant takes one root, the second's two.
+__device__ __forceinline__ F2 neg_sqrt2_second(float a, float b) {
+    float drop, second;
+    split2(neg_sqrt2(f2(b, b)), drop, second);
+    return f2(-a, -second);
+}
 // a / b from nb = -b.
 __device__ __forceinline__ F2 div2(F2 a, F2 nb) {
     float x, y;
@@ -319,7 +329,7 @@ __device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
 //    2^-23 by the instruction's specification, so below 1e-4 at 255) gives the same integer unless
 //    it lies within 1e-4 of the middle between two, and only a lane that has such a one
 //    (1 in 300) forms its eight codes from the exact roots.
-//  - the block's constants.  Lanes 0-15 compute those of m, lanes 16-31 those of v, in one pass.
+//  - the block's constants.  Those of m and of v are the halves of one pair.
 // A block with a moment outside Range (an exact zero, an infinity or a NaN among them) or a weight that comes
 // out infinite or NaN is left to adamw_block as a whole: false, and nothing of it is stored.
 template <bool kSR>
@@ -334,17 +344,17 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
     uint32_t rnd[4] = {0u, 0u, 0u, 0u};
     if (kSR && !t.has_res) sr_block8(k.key, (uint64_t)k.step, t.index, i, rnd);
     float m[8], nsv[8];          // the new first moments, and minus the roots of the second
-    float top_m = 0.0f, top_v = 0.0f, low_m = FLT_MAX, low_v = FLT_MAX, bad = 0.0f;
+    float top_m = 0.0f, top_v = 0.0f, low_m = FLT_MAX, low_v = FLT_MAX, spill = 0.0f;
+    F2 bad = f2(0.0f, 0.0f);     // 0 times the weights
     uint32_t wo[4], ro[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         // the pair's codes: byte 2 (q mod 2) and the next of word q / 2
         const uint32_t mw = mr[q >> 1], vw = vr[q >> 1];
-        const F2 cm = q & 1 ? f2(byte_to_f32<2>(mw, 8388736.0f), byte_to_f32<3>(mw, 8388736.0f))
-                            : f2(byte_to_f32<0>(mw, 8388736.0f), byte_to_f32<1>(mw, 8388736.0f));
-        const F2 cv = q & 1 ? f2(byte_to_f32<2>(vw, 8388608.0f), byte_to_f32<3>(vw, 8388608.0f))
-                            : f2(byte_to_f32<0>(vw, 8388608.0f), byte_to_f32<1>(vw, 8388608.0f));
-        const F2 tm = mul2(cm, qm2), tv = mul2(cv, qv2), tv2 = mul2(tv, tv);
+        const F2 cm = q & 1 ? f2(byte_in_2p23<2>(mw), byte_in_2p23<3>(mw)) : f2(byte_in_2p23<0>(mw), byte_in_2p23<1>(mw));
+        const F2 cv = q & 1 ? f2(byte_in_2p23<2>(vw), byte_in_2p23<3>(vw)) : f2(byte_in_2p23<0>(vw), byte_in_2p23<1>(vw));
+        const F2 tm = mul2(sub2(cm, f2(8388736.0f, 8388736.0f)), qm2), tv = mul2(sub2(cv, f2(8388608.0f, 8388608.0f)), qv2);
+        const F2 tv2 = mul2(tv, tv);
         float ta, tb, ma, mb, na, nb;
         split2(tm, ta, tb);
         split2(mul2(tm, tm), ma, mb);
@@ -365,7 +375,7 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
         low_v = fminf(low_v, fminf(-na, -nb));
         float wa, wb;
         split2(w, wa, wb);
-        bad = fmaf(wa, 0.0f, fmaf(wb, 0.0f, bad));
+        bad = fma2(w, f2(0.0f, 0.0f), bad);
         if (t.has_res) {
             wo[q] = pack_hi16(__float_as_uint(wa), __float_as_uint(wb));
             ro[q] = pack_lo16(__float_as_uint(wa), __float_as_uint(wb));
@@ -374,23 +384,25 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
             wo[q] = pack_lo16(store_bits<kSR>(wa, false, rnd[q] & 0xFFFFu, lo), store_bits<kSR>(wb, false, rnd[q] >> 16, lo));
             ro[q] = 0u;
             // rounding to bf16 can carry a finite weight to infinity
-            if ((wo[q] & 0x7F80u) == 0x7F80u || (wo[q] & 0x7F800000u) == 0x7F800000u) bad = __int_as_float(0x7FC00000);
+            if ((wo[q] & 0x7F80u) == 0x7F80u || (wo[q] & 0x7F800000u) == 0x7F800000u) spill = 1.0f;
         }
     }
     // minima and maxima pass over a NaN, but it reaches the weight
+    float bad_a, bad_b;
+    split2(bad, bad_a, bad_b);
     const bool plain = k.plain_range && low_v >= Range::v_min && top_v <= Range::v_max && low_m >= Range::m_min &&
-                       top_m <= Range::m_max && bad == 0.0f;
+                       top_m <= Range::m_max && bad_a + bad_b == 0.0f && spill == 0.0f;
     if (!__all_sync(0xFFFFFFFFu, plain)) return false;
     st_stream(reinterpret_cast<uint4*>(t.w + i), make_uint4(wo[0], wo[1], wo[2], wo[3]));
     if (t.has_res) st_stream(reinterpret_cast<uint4*>(t.res + i), make_uint4(ro[0], ro[1], ro[2], ro[3]));
 
     top_m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_m)));
     top_v = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top_v)));
-    const bool second = lane >= 16;
-    const float root = __fsqrt_rn(second ? top_v : top_m);
-    const float q0 = second ? __fmul_rn(__fsqrt_rn(root), 1.0f / 255.0f) : __fmul_rn(root, 1.0f / 127.0f);
-    const float r0 = code_factor(q0);
-    const float rm = __shfl_sync(0xFFFFFFFFu, r0, 0), rv = __shfl_sync(0xFFFFFFFFu, r0, 16);
+    // the constants of both moments side by side, by the same branch-free root and quotient (their range holds)
+    float root_m, root_v, rm, rv;
+    split2(neg_sqrt2(f2(-top_m, -top_v)), root_m, root_v);
+    const F2 q0 = mul2(neg_sqrt2_second(root_m, root_v), f2(1.0f / 127.0f, 1.0f / 255.0f));
+    split2(div2(f2(1.0f, 1.0f), mul2(mul2(q0, q0), f2(-1.0f, -1.0f))), rm, rv);
     uint32_t cm[8], cv[8];
     float off = 0.0f;
     const F2 zero_m = f2(12583040.0f, 12583040.0f), zero_v = f2(12582912.0f, 12582912.0f);   // 1.5 * 2^23 (+ 128)
@@ -427,7 +439,7 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
     }
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack_byte0(cm), pack_byte0(cm + 4)));
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack_byte0(cv), pack_byte0(cv + 4)));
-    qmv = make_float2(__shfl_sync(0xFFFFFFFFu, q0, 0), __shfl_sync(0xFFFFFFFFu, q0, 16));
+    split2(q0, qmv.x, qmv.y);
     return true;
 }
 
