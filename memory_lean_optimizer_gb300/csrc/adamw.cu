@@ -312,13 +312,33 @@ struct Raw {
     uint4 w, r, g;
     uint2 m, v;
 };
-__device__ __forceinline__ void load_raw(Raw& x, const Tensor& t, int64_t b0) {
-    const int64_t i = b0 + 8 * (threadIdx.x & 31);
-    x.w = ld_stream(reinterpret_cast<const uint4*>(t.w + i));
-    x.g = ld_stream(reinterpret_cast<const uint4*>(t.g + i));
-    x.r = t.has_res ? ld_stream(reinterpret_cast<const uint4*>(t.res + i)) : make_uint4(0, 0, 0, 0);
-    x.m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
-    x.v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
+// A ring of blocks for each warp in shared memory, kAhead of them on their way at a time without a register: a lane
+// copies (cp.async) what it will read itself, so that waiting for its own copies is all the order there is.
+constexpr int kRing = 3, kAhead = kRing - 1;
+constexpr int kStageBytes = 8 * kBlk;   // w, residual, g: 512 bytes each; codes: 256 each
+constexpr int kRingBytes = kThreads / 32 * kRing * kStageBytes;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch_block(uint32_t stage, const Tensor& t, int64_t b0) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i = b0 + 8 * lane;
+    copy16(stage + 16 * lane, t.w + i);
+    copy16(stage + 512 + 16 * lane, t.g + i);
+    if (t.has_res) copy16(stage + 1024 + 16 * lane, t.res + i);
+    copy8(stage + 1536 + 8 * lane, static_cast<const uint8_t*>(t.m) + i);
+    copy8(stage + 1792 + 8 * lane, static_cast<const uint8_t*>(t.v) + i);
+}
+__device__ __forceinline__ void read_block(Raw& x, const char* stage, const Tensor& t) {
+    const int lane = threadIdx.x & 31;
+    x.w = *reinterpret_cast<const uint4*>(stage + 16 * lane);
+    x.g = *reinterpret_cast<const uint4*>(stage + 512 + 16 * lane);
+    x.r = t.has_res ? *reinterpret_cast<const uint4*>(stage + 1024 + 16 * lane) : make_uint4(0, 0, 0, 0);
+    x.m = *reinterpret_cast<const uint2*>(stage + 1536 + 8 * lane);
+    x.v = *reinterpret_cast<const uint2*>(stage + 1792 + 8 * lane);
 }
 
 // A whole aligned block with 8-bit states: the results of adamw_block, two elements to an instruction
@@ -447,9 +467,10 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
 // j-th block from before the first to after the last -- one load and one store of neighbours (read
 // and written block by block, 4 bytes in a sector that other warps write too, they cost more than
 // all the other traffic: 1494 against 595 us at 278M parameters) -- and the whole aligned
-// blocks go through adamw_block_fast, the next one's loads under way while one is computed.
+// blocks go through adamw_block_fast, the next two on their way while one is computed.
 template <bool kSR, bool kU8>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamWPrm k) {
+    extern __shared__ __align__(16) char ring[];   // kU8: kRingBytes
     __shared__ int counted;
     if (threadIdx.x == 0) counted = 0;
     __syncthreads();
@@ -479,15 +500,25 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamW
     uint32_t done = 0u;   // bit j: block j is finished
     if (kU8 && t.u8 && aligned) {
         const int whole = (int)((min(end, first + (int64_t)blocks * kBlk) - first) / kBlk);
-        Raw x;
-        if (whole > 0) load_raw(x, t, first);
+        char* const stages = ring + (threadIdx.x >> 5) * kRing * kStageBytes;
+        const uint32_t stages0 = (uint32_t)__cvta_generic_to_shared(stages);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (j < whole) fetch_block(stages0 + j * kStageBytes, t, first + (int64_t)j * kBlk);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int at = 0;
         for (int j = 0; j < whole; ++j) {
-            Raw next;
-            if (j + 1 < whole) load_raw(next, t, first + (int64_t)(j + 1) * kBlk);
+            const int to = at + kAhead < kRing ? at + kAhead : at + kAhead - kRing;
+            if (j + kAhead < whole) fetch_block(stages0 + to * kStageBytes, t, first + (int64_t)(j + kAhead) * kBlk);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            Raw x;
+            read_block(x, stages + at * kStageBytes, t);
+            if (++at == kRing) at = 0;
             float2 qj = make_float2(__shfl_sync(0xFFFFFFFFu, q.x, j), __shfl_sync(0xFFFFFFFFu, q.y, j));
             if (adamw_block_fast<kSR>(k, t, gs, first + (int64_t)j * kBlk, x, qj)) done |= 1u << j;
             if (lane == j) q = qj;
-            x = next;
         }
     }
     uint32_t nf = 0u;
@@ -557,8 +588,13 @@ int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& s, bool u8, cuda
                      philox_key(s.seed)};
     const unsigned grid = (unsigned)L.n_chunks_total;
     if (u8) {
-        if (s.sr) k_adamw_step<true, true><<<grid, kThreads, 0, stream>>>(L, k);
-        else k_adamw_step<false, true><<<grid, kThreads, 0, stream>>>(L, k);
+        auto kernel = s.sr ? k_adamw_step<true, true> : k_adamw_step<false, true>;
+        static const cudaError_t attr[2] = {
+            cudaFuncSetAttribute(k_adamw_step<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes),
+            cudaFuncSetAttribute(k_adamw_step<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)};
+        const int rc = check_cuda(attr[s.sr ? 1 : 0], "adamw step shared memory");
+        if (rc) return rc;
+        kernel<<<grid, kThreads, kRingBytes, stream>>>(L, k);
     } else {
         if (s.sr) k_adamw_step<true, false><<<grid, kThreads, 0, stream>>>(L, k);
         else k_adamw_step<false, false><<<grid, kThreads, 0, stream>>>(L, k);
