@@ -74,7 +74,7 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
     if bias is not None:
         bias = _vector(bias, dim, x, weight.dtype, "bias")
     y = x.new_empty(x.shape)
-    mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind(0)
+    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
     lmopt.norm_layer_forward(m.data_ptr(), m.stride(0), weight.data_ptr(), None if bias is None else bias.data_ptr(),
                              y.data_ptr(), dim, mean.data_ptr(), rstd.data_ptr(), rows, dim, eps, xt, wt,
                              _stream_ptr(None))
@@ -146,7 +146,7 @@ def xent_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tenso
     and the log of the softmax's denominator.  Rows with ignore_index have 0 for both."""
     h, w, t = _xent_args(hidden, weight, target)
     (rows, dim), vocab = h.shape, w.shape[0]
-    loss, lse = h.new_empty((2, *target.shape), dtype=torch.float32).unbind(0)
+    loss, lse = h.new_empty(target.shape, dtype=torch.float32), h.new_empty(target.shape, dtype=torch.float32)
     nbytes = _xent_bytes(rows, dim, vocab, w.data_ptr() % 16, w.stride(0), False)
     work = h.new_empty(nbytes, dtype=torch.uint8)
     lmopt.loss_xent_forward(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), t.data_ptr(), rows, dim, vocab,
