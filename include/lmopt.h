@@ -429,7 +429,9 @@ int optim_group_set_profile_event(optim_group_t* group, void* event);
  * them, as memory-lean as the step (nothing of the size of the logits is ever kept).  These calls
  * take plain buffers, no handle; scratch comes from the caller (the workspace calls say how much; it
  * carries nothing from one call to the next and may be shared by calls ordered on one stream).
- * Row strides (ld*) are in elements. */
+ * Row strides (ld*) are in elements.  Sums and softmax statistics are fp32, in an order fixed by the sizes
+ * and alignments (the tensor cores' included): two runs agree bit for bit, another alignment may
+ * differ by roundings of fp32. */
 enum { OPTIM_BF16 = 0, OPTIM_F32 = 1 };
 
 /* Layer norm of `rows` rows of `dim` elements: y = (x - mu) r w + b with mu the row's mean and

@@ -589,10 +589,8 @@ int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& s, bool u8, cuda
     const unsigned grid = (unsigned)L.n_chunks_total;
     if (u8) {
         auto kernel = s.sr ? k_adamw_step<true, true> : k_adamw_step<false, true>;
-        static const cudaError_t attr[2] = {
-            cudaFuncSetAttribute(k_adamw_step<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes),
-            cudaFuncSetAttribute(k_adamw_step<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)};
-        const int rc = check_cuda(attr[s.sr ? 1 : 0], "adamw step shared memory");
+        static std::atomic<uint64_t> allowed[2];
+        const int rc = allow_smem(kernel, kRingBytes, allowed[s.sr ? 1 : 0]);
         if (rc) return rc;
         kernel<<<grid, kThreads, kRingBytes, stream>>>(L, k);
     } else {

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 #include "common.cuh"
@@ -21,6 +22,20 @@ int check_cuda(cudaError_t e, const char* what);
 int sm_count();
 // Grid for a grid-stride elementwise kernel over `units` work units of kThreads each.
 unsigned grid_for(int64_t units);
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device, once for each device (`done`: a bit
+// each, one word per kernel).
+template <class F>
+int allow_smem(F kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    int rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
+    if (rc) return rc;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return OPTIM_OK;
+    rc = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), "kernel shared memory");
+    if (!rc) done.fetch_or(bit, std::memory_order_relaxed);
+    return rc;
+}
 
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

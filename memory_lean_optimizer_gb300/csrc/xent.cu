@@ -780,8 +780,8 @@ template <int kMode, int kCta>
 int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
     constexpr int kSmem = 1024 + product_stages(kCta) * (128 + kTileN / kCta) * kTileK * 2 + kFinishBytes;
     auto kernel = k_product<kMode, kCta>;
-    static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    int rc = check_cuda(attr, "product kernel shared memory");
+    static std::atomic<uint64_t> allowed{0};
+    const int rc = allow_smem(kernel, kSmem, allowed);
     if (rc) return rc;
     const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / kCta)) * kCta;
@@ -940,12 +940,19 @@ static int check_array(const void* p, size_t align, const char* name) {
     return OPTIM_OK;
 }
 
+// Tile and row numbers are 32-bit in the kernels.
+static int check_sizes(int64_t rows, int64_t dim, int64_t vocab) {
+    if (rows < 0 || dim < 1 || vocab < 1) return set_error(OPTIM_EINVAL, "need rows >= 0, dim >= 1 and vocab >= 1");
+    const int64_t most = (int64_t)1 << 28, tiles = (int64_t)1 << 30;
+    if (rows > most || dim > most || vocab > most || (rows / 128 + 2) * (vocab / 128 + 2) > tiles ||
+        (vocab / 128 + 2) * (dim / 128 + 2) > tiles || (rows / 128 + 2) * (dim / 128 + 2) * 64 > tiles)
+        return set_error(OPTIM_EINVAL, "%lld rows, dim %lld, vocab %lld: too large", (long long)rows, (long long)dim, (long long)vocab);
+    return OPTIM_OK;
+}
+
 static int check_xent(XentCall& c) {
-    if (c.rows < 0 || c.dim < 1 || c.vocab < 1) return set_error(OPTIM_EINVAL, "need rows >= 0, dim >= 1 and vocab >= 1");
-    // tile counts and row numbers are 32-bit in the kernels
-    if (c.rows > (1 << 28) || c.dim > (1 << 24) || c.vocab > (1 << 28))
-        return set_error(OPTIM_EINVAL, "rows and vocab must be at most 2^28, dim at most 2^24");
-    int rc = check_matrix(c.hidden, c.ldh, c.rows, c.dim, "hidden");
+    int rc = check_sizes(c.rows, c.dim, c.vocab);
+    if (!rc) rc = check_matrix(c.hidden, c.ldh, c.rows, c.dim, "hidden");
     if (!rc) rc = check_matrix(c.weight, c.ldw, c.vocab, c.dim, "weight");
     if (!rc && c.rows > 0) rc = check_array(c.target, 8, "target");
     if (!rc && c.rows > 0) rc = check_array(c.lse, 4, "lse");
@@ -963,8 +970,8 @@ extern "C" {
 int loss_xent_workspace(int64_t rows, int64_t dim, int64_t vocab, const void* weight, int64_t ldw, int32_t backward,
                         size_t* bytes) {
     if (!bytes) return set_error(OPTIM_EINVAL, "bytes is NULL");
-    if (rows < 0 || dim < 1 || vocab < 1 || rows > (1 << 28) || dim > (1 << 24) || vocab > (1 << 28))
-        return set_error(OPTIM_EINVAL, "need 0 <= rows <= 2^28, 1 <= dim <= 2^24 and 1 <= vocab <= 2^28");
+    const int rc = check_sizes(rows, dim, vocab);
+    if (rc) return rc;
     *bytes = xent_workspace_bytes(rows, dim, vocab, weight, vocab == 1 ? std::max(ldw, dim) : ldw, backward != 0);
     return OPTIM_OK;
 }

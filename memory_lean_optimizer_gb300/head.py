@@ -12,6 +12,7 @@ from __future__ import annotations
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import lmopt
 from .engine import _stream_ptr
@@ -32,7 +33,11 @@ def _on_stream(fn):
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):
-            return fn(*args, **kw)
+            out = fn(*args, **kw)
+        for t in (*args, *kw.values()):        # their memory is not given away before the stream is done with it
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return out
     return call
 
 
@@ -83,8 +88,9 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor
 
 @_on_stream
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
-                        rstd: torch.Tensor):
-    """(dx, dweight, dbias) from the gradient of y and what the forward call returned."""
+                        rstd: torch.Tensor, need_x: bool = True, need_weight: bool = True):
+    """(dx, dweight, dbias) from the gradient of y and what the forward call returned; None for those that are not
+    needed (dweight and dbias go together)."""
     xt, wt = _type(x, "x"), _type(weight, "weight")
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must have x's shape and type")
@@ -92,13 +98,15 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     rows, dim = m.shape
     weight = _vector(weight, dim, x, weight.dtype, "weight")
     mean, rstd = _vector(mean, rows, x, torch.float32, "mean"), _vector(rstd, rows, x, torch.float32, "rstd")
-    dx = x.new_empty(x.shape)
-    dweight, dbias = weight.new_empty(dim), weight.new_empty(dim)
+    dx = x.new_empty(x.shape) if need_x else None
+    dweight, dbias = (weight.new_empty(dim), weight.new_empty(dim)) if need_weight else (None, None)
     nbytes = _norm_bytes(rows, dim)
     work = x.new_empty(nbytes, dtype=torch.uint8)
     lmopt.norm_layer_backward(g.data_ptr(), g.stride(0), m.data_ptr(), m.stride(0), weight.data_ptr(), mean.data_ptr(),
-                              rstd.data_ptr(), dx.data_ptr(), dim, dweight.data_ptr(), dbias.data_ptr(), rows, dim,
-                              xt, wt, work.data_ptr(), nbytes, _stream_ptr(None))
+                              rstd.data_ptr(), dx.data_ptr() if need_x else None, dim,
+                              dweight.data_ptr() if need_weight else None,
+                              dbias.data_ptr() if need_weight else None, rows, dim, xt, wt, work.data_ptr(), nbytes,
+                              _stream_ptr(None))
     return dx, dweight, dbias
 
 
@@ -111,10 +119,12 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd)
-        return dx, dweight, dbias if ctx.has_bias else None, None
+        need = ctx.needs_input_grad
+        dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd, need[0], need[1] or need[2])
+        return dx, dweight if need[1] else None, dbias if ctx.has_bias and need[2] else None, None
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
@@ -181,6 +191,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         hidden, weight, target, lse = ctx.saved_tensors
         dh, dw = xent_backward(hidden, weight, target, lse, grad, ctx.ignore_index, ctx.needs_input_grad[0],

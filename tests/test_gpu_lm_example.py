@@ -52,3 +52,33 @@ def test_tail_equals_torch():
     assert abs(float(loss.detach()) - float(ref.detach())) < 2.0 ** -8
     for got, want in zip((h, tail.norm_weight, tail.norm_bias, tail.weight), p):
         assert float((got.grad.float() - want.grad).abs().max()) <= 2.0 ** -5 * float(want.grad.abs().max())
+
+
+def test_frozen_parts_cost_no_gradient():
+    """Autograd asks for what is needed: a frozen output matrix, frozen norm weights, a leaf hidden state without grad."""
+    from memory_lean_optimizer_gb300 import head
+    torch.manual_seed(2)
+    h = torch.randn(50, 96, device="cuda").to(torch.bfloat16)
+    t = torch.randint(700, (50,), device="cuda")
+    tail = head.LMTail(96, 700)
+    h.requires_grad_()
+    tail(h, t).backward()
+    full = [h.grad] + [p.grad for p in tail.parameters()]
+    for keep in range(4):
+        ps = [h] + list(tail.parameters())
+        for i, p in enumerate(ps):
+            p.grad = None
+            p.requires_grad_(i == keep)
+        tail(h, t).backward()
+        for i, p in enumerate(ps):
+            assert (p.grad is None) == (i != keep)
+        assert torch.equal(ps[keep].grad, full[keep])
+
+
+def test_no_second_derivatives():
+    from memory_lean_optimizer_gb300 import head
+    x = torch.randn(4, 64, device="cuda", requires_grad=True)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(head.layer_norm(x, w).pow(2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()

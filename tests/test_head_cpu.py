@@ -57,3 +57,9 @@ def test_workspaces(lib):
     n = ctypes.c_size_t()
     assert lib.load().loss_xent_workspace(4, 64, 10, P, 64, 1, None) == lib.OPTIM_EINVAL
     assert lib.load().loss_xent_workspace(4, 64, 10, P, 64, 1, ctypes.byref(n)) == lib.OPTIM_OK
+
+
+def test_sizes_past_the_kernels_numbers(lib):
+    for rows, dim, vocab in (((1 << 28) + 1, 8, 8), (1 << 26, 8, 1 << 26), (8, 1 << 26, 1 << 26), (1 << 27, 1 << 20, 8)):
+        with pytest.raises(lib.LmoptError):
+            lib.loss_xent_workspace(rows, dim, vocab, P, dim, True)
