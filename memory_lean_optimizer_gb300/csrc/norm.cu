@@ -165,41 +165,101 @@ struct Slice {
     }
 };
 
+// Rows on their way: a thread copies (cp.async) its own slices of the rows it will take next into its own places
+// of shared memory, kRowsAhead rows before it reads them, so that the copies cost no registers -- loads
+// into registers a row ahead were moved down to their use by the compiler -- and waiting for its
+// own copies is all the order there is.  Single bf16 elements are too small for these copies (4
+// bytes): kAsync false, and the row is loaded where it is used.
+constexpr int kPlaces = 3, kRowsAhead = kPlaces - 1;
+template <class T, int V, int K, int kT>
+struct Coming {
+    static constexpr bool kAsync = V > 1 || sizeof(T) == 4;
+    static constexpr int kUnit = V > 1 ? 16 : 4, kPer = V > 1 ? K : 2 * K;   // bytes of a copy, copies to a row and thread
+    using S = Slice<T, V, kT>;
+    char* mine;
+    int threads;
+    __device__ __forceinline__ Coming(char* smem) {
+        threads = (int)(blockDim.x * blockDim.y);
+        mine = smem + (threadIdx.y * blockDim.x + threadIdx.x) * kUnit;
+    }
+    __device__ __forceinline__ char* at(int place, int i) const {
+        return mine + (place * kPer + i) * threads * kUnit;
+    }
+    static __device__ __forceinline__ void copy(char* dst, const T* src) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+        if (V > 1) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+    }
+    __device__ __forceinline__ void fetch(int place, const T* row, int dim) const {
+        if (!kAsync) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = S::column(k);
+            if (V > 1) {
+                if (c < dim) copy(at(place, k), row + c);
+            } else {
+                if (c < dim) copy(at(place, 2 * k), row + c);
+                if (c + kT < dim) copy(at(place, 2 * k + 1), row + c + kT);
+            }
+        }
+    }
+    static __device__ __forceinline__ void close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead) : "memory"); }
+    // Slice k, whose first column c is below dim (row: where it is in memory, for kAsync false).
+    __device__ __forceinline__ S read(int place, int k, const T* row, int c, int dim) const {
+        S x;
+        if (!kAsync) {
+            x.load(row, c, dim);
+        } else if (V > 1) {
+            x.raw[0].load(reinterpret_cast<const T*>(at(place, k)));
+        } else {
+            x.raw[0].load(reinterpret_cast<const T*>(at(place, 2 * k)));
+            x.raw[V > 1 ? 0 : 1] = Vec<T, V>{};
+            if (c + kT < dim) x.raw[V > 1 ? 0 : 1].load(reinterpret_cast<const T*>(at(place, 2 * k + 1)));
+        }
+        return x;
+    }
+    static size_t bytes(int threads) { return kAsync ? (size_t)kPlaces * kPer * threads * kUnit : 0; }
+};
+
 // Forward, the row in registers: blockDim.x threads hold a row, blockDim.y rows at a time.  x is read once, y
-// written once; the next row is on its way while this one is reduced.
+// written once.
 template <class TX, class TW, int V, int K, int kT, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) k_norm_forward(const TX* x, int64_t ldx, const TW* __restrict__ w,
                                                                         const TW* __restrict__ b, TX* y, int64_t ldy,
                                                                         float* __restrict__ mean, float* __restrict__ rstd,
                                                                         int64_t rows, int dim, float eps) {
     using S = Slice<TX, V, kT>;
+    extern __shared__ __align__(16) char coming_smem[];
     __shared__ __align__(16) float red[2][2][32];
     clear_sums(red);
+    const Coming<TX, V, K, kT> coming(coming_smem);
     const float inv = 1.0f / (float)dim;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int turn = 0;
+    int turn = 0, place = 0;
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const TX* px = x + r * ldx;
-    S raw[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = S::column(k);
-        if (r < rows && c < dim) raw[k].load(px, c, dim);
+    for (int i = 0; i < kRowsAhead; ++i) {
+        if (r + i * step < rows) coming.fetch(i, x + (r + i * step) * ldx, dim);
+        coming.close();
     }
     for (; r < rows; r += step) {
+        const int into = place == 0 ? kRowsAhead : place - 1;
+        if (r + kRowsAhead * step < rows) coming.fetch(into, x + (r + kRowsAhead * step) * ldx, dim);
+        coming.close();
+        coming.wait();
         F2 f[K][S::n];
         F2 acc = f2(0.0f, 0.0f);
-        px += step * ldx;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = S::column(k);
             if (c < dim) {
-                raw[k].get(f[k]);
+                coming.read(place, k, x + r * ldx, c, dim).get(f[k]);
 #pragma unroll
                 for (int i = 0; i < S::n; ++i) acc = add2(acc, f[k][i]);
-                if (r + step < rows) raw[k].load(px, c, dim);
             }
         }
+        if (++place == kPlaces) place = 0;
         float s[1] = {total(acc)};
         row_sums(s, red, turn);
         const float mu = s[0] * inv;
@@ -503,6 +563,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_long(const TX* __restrict_
     }
 }
 
+constexpr int kMostSmem = 96 * 1024;   // 512 threads with 32 bf16 or 16 fp32 values each
+
 // Partial rows of the weight's gradient at most: 4 CTAs on each of 152 SMs.
 constexpr int kMaxSlices = 608;
 
@@ -551,9 +613,12 @@ int64_t resident(F kernel, int threads, size_t smem, int64_t wanted, std::atomic
 template <class TX, class TW, int V, int K, int kT, int kMax, int kMin>
 int forward_rows(const NormForward& a, const RowShape& sh, cudaStream_t s) {
     auto kernel = k_norm_forward<TX, TW, V, K, kT, kMax, kMin>;
-    static std::atomic<uint64_t> last{0};
-    const int64_t grid = resident(kernel, sh.tx * sh.ty, 0, (a.rows + sh.ty - 1) / sh.ty, last);
-    kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), 0, s>>>(
+    const size_t smem = Coming<TX, V, K, kT>::bytes(sh.tx * sh.ty);
+    static std::atomic<uint64_t> last{0}, allowed{0};
+    const int rc = allow_smem(kernel, kMostSmem, allowed);
+    if (rc) return rc;
+    const int64_t grid = resident(kernel, sh.tx * sh.ty, smem, (a.rows + sh.ty - 1) / sh.ty, last);
+    kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), smem, s>>>(
         static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias),
         static_cast<TX*>(a.y), a.ldy, a.mean, a.rstd, a.rows, (int)a.dim, a.eps);
     return check_cuda(cudaGetLastError(), "layer norm launch");
