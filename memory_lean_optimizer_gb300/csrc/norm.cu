@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "packed.cuh"
 
 namespace lmo {
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward(const TX* dy, 
     using S = Slice<TX, V, kT>;
     __shared__ __align__(16) float red[2][2][32];
     extern __shared__ float cols[];   // [2][dim], only when blockDim.y > 1
+    pdl_release();   // the join may take its place early: it waits for this grid's end
     clear_sums(red);
     const float inv = 1.0f / (float)dim;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
@@ -450,6 +452,7 @@ template <class TW>
 __global__ void __launch_bounds__(kThreads) k_norm_join(const float* __restrict__ partial, int slices, TW* __restrict__ dw,
                                                         TW* __restrict__ db, int64_t dim) {
     __shared__ float red[8][33];
+    pdl_sync();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t j = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.0f;
@@ -646,9 +649,9 @@ int forward_t(const NormForward& a, cudaStream_t s) {
 
 template <class TW>
 int join_slices(const NormBackward& a, int slices, cudaStream_t s) {
-    k_norm_join<TW><<<(unsigned)((2 * a.dim + 31) / 32), kThreads, 0, s>>>(a.partial, slices, static_cast<TW*>(a.dweight),
-                                                                          static_cast<TW*>(a.dbias), a.dim);
-    return check_cuda(cudaGetLastError(), "layer norm weight gradient launch");
+    return check_cuda(launch_after(k_norm_join<TW>, (2 * a.dim + 31) / 32, kThreads, 0, 1, s, a.partial, slices,
+                                   static_cast<TW*>(a.dweight), static_cast<TW*>(a.dbias), a.dim),
+                      "layer norm weight gradient launch");
 }
 
 template <class TX, class TW, int V, int K, int kT, int kMax, bool kAhead>

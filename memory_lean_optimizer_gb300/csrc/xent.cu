@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "tensor.cuh"
 
 namespace lmo {
@@ -68,14 +69,6 @@ struct ProductArgs {
     int64_t lddw;
     int32_t dw_aligned;         // kWeight: the same of dW
 };
-
-// Programmatic dependent launch: the kernels of a call start while their predecessor drains and wait
-// here before they read what it wrote; each lets its own successor start only after that wait, so
-// what lies further back is complete too.
-__device__ __forceinline__ void pdl_sync() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -485,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_rows(const RowArgs a) {
     __shared__ int warp_count[kThreads / 32 + 1];
     __shared__ int list_src[kThreads], list_pos[kThreads];
     // launched without the early start itself: its successor may come as soon as there is room
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) before_s = total_s = 0, top_s = 0u;
     __syncthreads();
@@ -755,25 +748,6 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(OPTIM_ECUDA, "tensor map of a %lld x %lld matrix: error %d", (long long)rows, (long long)cols, (int)r);
     return OPTIM_OK;
-}
-
-// Launches a kernel behind its predecessor in the call (pdl_sync), as clusters of `cta`.
-template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cta, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cta;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = cta > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 template <int kMode, int kCta>
