@@ -1,0 +1,36 @@
+// launch.cuh -- programmatic dependent launch within a call.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace lmo {
+
+// Programmatic dependent launch: the kernels of a call start while their predecessor drains and wait
+// here before they read what it wrote; each lets its own successor start only after that wait, so
+// what lies further back is complete too.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_sync() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_release();
+}
+
+// Launches a kernel behind its predecessor in the call (pdl_sync), as clusters of `cta`.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cta, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cta;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cta > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+}  // namespace lmo
