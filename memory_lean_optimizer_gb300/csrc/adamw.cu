@@ -14,6 +14,7 @@
 // A positive v keeps a code of at least 1: decoded to zero, it would leave a kept m divided by eps
 // alone in a later step whose gradient is zero.
 #include "internal.h"
+#include "launch.cuh"
 #include "packed.cuh"
 
 namespace lmo {
@@ -472,6 +473,7 @@ template <bool kSR, bool kU8>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamWPrm k) {
     extern __shared__ __align__(16) char ring[];   // kU8: kRingBytes
     __shared__ int counted;
+    pdl_sync();
     if (threadIdx.x == 0) counted = 0;
     __syncthreads();
     const Chunk c = L.chunks[blockIdx.x];
@@ -539,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adamw_step(NadamLaunch L, AdamW
 // Moments of every tensor as fp32 values, into flat buffers (tensor i at 64 * slot64 elements).
 template <bool kU8>
 __global__ void __launch_bounds__(kThreads) k_adamw_unpack(NadamLaunch L, float* __restrict__ fm, float* __restrict__ fv) {
+    pdl_sync();
     const Chunk c = L.chunks[blockIdx.x];
     const TensorRec t = L.tensors[c.tensor];
     const bool u8 = kU8 && (t.flags & kFlagSmall) == 0;
@@ -586,26 +589,22 @@ int launch_adamw_step(const NadamLaunch& L, const AdamWScalars& s, bool u8, cuda
     const bool plain_range = s.k1 >= 0x1p-30f && s.k1 <= 0x1p20f && s.k2 >= 1.0f && s.k2 <= 0x1p13f && s.eps <= 1.0f;
     const AdamWPrm k{s.b1, s.omb1, s.b2, s.omb2, s.eps, s.lr_wd, s.k1, s.k2, s.grad_scale, s.step, plain_range,
                      philox_key(s.seed)};
-    const unsigned grid = (unsigned)L.n_chunks_total;
+    // started while the stream's last kernel drains: a step and the unpacking after it are short for small groups
+    auto kernel = u8 ? (s.sr ? k_adamw_step<true, true> : k_adamw_step<false, true>)
+                     : (s.sr ? k_adamw_step<true, false> : k_adamw_step<false, false>);
+    const int smem = u8 ? kRingBytes : 0;
     if (u8) {
-        auto kernel = s.sr ? k_adamw_step<true, true> : k_adamw_step<false, true>;
         static std::atomic<uint64_t> allowed[2];
-        const int rc = allow_smem(kernel, kRingBytes, allowed[s.sr ? 1 : 0]);
+        const int rc = allow_smem(kernel, smem, allowed[s.sr ? 1 : 0]);
         if (rc) return rc;
-        kernel<<<grid, kThreads, kRingBytes, stream>>>(L, k);
-    } else {
-        if (s.sr) k_adamw_step<true, false><<<grid, kThreads, 0, stream>>>(L, k);
-        else k_adamw_step<false, false><<<grid, kThreads, 0, stream>>>(L, k);
     }
-    return check_cuda(cudaGetLastError(), "adamw step launch");
+    return check_cuda(launch_after(kernel, L.n_chunks_total, kThreads, smem, 1, stream, L, k), "adamw step launch");
 }
 
 int launch_adamw_unpack(const NadamLaunch& L, bool u8, float* m, float* v, cudaStream_t stream) {
     if (L.n_chunks_total == 0) return OPTIM_OK;
-    const unsigned grid = (unsigned)L.n_chunks_total;
-    if (u8) k_adamw_unpack<true><<<grid, kThreads, 0, stream>>>(L, m, v);
-    else k_adamw_unpack<false><<<grid, kThreads, 0, stream>>>(L, m, v);
-    return check_cuda(cudaGetLastError(), "adamw unpack launch");
+    return check_cuda(launch_after(u8 ? k_adamw_unpack<true> : k_adamw_unpack<false>, L.n_chunks_total, kThreads, 0, 1, stream,
+                                   L, m, v), "adamw unpack launch");
 }
 
 }  // namespace lmo
