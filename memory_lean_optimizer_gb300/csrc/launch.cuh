@@ -5,21 +5,22 @@
 
 namespace lmo {
 
-// Programmatic dependent launch: the kernels of a call start while their predecessor drains and wait
-// here before they read what it wrote; each lets its own successor start only after that wait, so
-// what lies further back is complete too.
+// Programmatic dependent launch: a kernel starts while its predecessor on the stream drains and waits here
+// before it touches memory; each lets its own successor start only after that wait, so what lies
+// further back is complete too.  (A predecessor that does not let it start early, of whatever
+// origin, is simply waited for.)
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_sync() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     pdl_release();
 }
 
-// Launches a kernel behind its predecessor in the call (pdl_sync), as clusters of `cta`.
+// Launches a kernel that waits for its predecessor itself (pdl_sync), as clusters of `cta`.
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cta, cudaStream_t s, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, dim3 block, size_t smem, int cta, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];

@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) k_norm_forward(const TX
     using S = Slice<TX, V, kT>;
     extern __shared__ __align__(16) char coming_smem[];
     __shared__ __align__(16) float red[2][2][32];
+    pdl_sync();
     clear_sums(red);
     const Coming<TX, V, K, kT> coming(coming_smem);
     const float inv = 1.0f / (float)dim;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward(const TX* dy, 
     using S = Slice<TX, V, kT>;
     __shared__ __align__(16) float red[2][2][32];
     extern __shared__ float cols[];   // [2][dim], only when blockDim.y > 1
-    pdl_release();   // the join may take its place early: it waits for this grid's end
+    pdl_sync();
     clear_sums(red);
     const float inv = 1.0f / (float)dim;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
@@ -621,10 +622,9 @@ int forward_rows(const NormForward& a, const RowShape& sh, cudaStream_t s) {
     const int rc = allow_smem(kernel, kMostSmem, allowed);
     if (rc) return rc;
     const int64_t grid = resident(kernel, sh.tx * sh.ty, smem, (a.rows + sh.ty - 1) / sh.ty, last);
-    kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), smem, s>>>(
-        static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias),
-        static_cast<TX*>(a.y), a.ldy, a.mean, a.rstd, a.rows, (int)a.dim, a.eps);
-    return check_cuda(cudaGetLastError(), "layer norm launch");
+    return check_cuda(launch_after(kernel, grid, dim3(sh.tx, sh.ty), smem, 1, s, static_cast<const TX*>(a.x), a.ldx,
+                                   static_cast<const TW*>(a.weight), static_cast<const TW*>(a.bias), static_cast<TX*>(a.y),
+                                   a.ldy, a.mean, a.rstd, a.rows, (int)a.dim, a.eps), "layer norm launch");
 }
 
 template <class TX, class TW>
@@ -662,10 +662,10 @@ int backward_rows(const NormBackward& a, const RowShape& sh, cudaStream_t s) {
     static std::atomic<uint64_t> last{0};
     const int64_t wanted = std::min<int64_t>((a.rows + sh.ty - 1) / sh.ty, kMaxSlices);
     const int64_t grid = std::max<int64_t>(1, resident(kernel, sh.tx * sh.ty, smem, wanted, last));
-    kernel<<<(unsigned)grid, dim3(sh.tx, sh.ty), smem, s>>>(
-        static_cast<const TX*>(a.dy), a.lddy, static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), a.mean,
-        a.rstd, static_cast<TX*>(a.dx), a.lddx, sums ? a.partial : nullptr, a.rows, (int)a.dim);
-    const int rc = check_cuda(cudaGetLastError(), "layer norm backward launch");
+    const int rc = check_cuda(launch_after(kernel, grid, dim3(sh.tx, sh.ty), smem, 1, s, static_cast<const TX*>(a.dy), a.lddy,
+                                           static_cast<const TX*>(a.x), a.ldx, static_cast<const TW*>(a.weight), a.mean, a.rstd,
+                                           static_cast<TX*>(a.dx), a.lddx, sums ? a.partial : nullptr, a.rows, (int)a.dim),
+                              "layer norm backward launch");
     return rc || !sums ? rc : join_slices<TW>(a, (int)grid, s);
 }
 

@@ -477,8 +477,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_rows(const RowArgs a) {
     __shared__ uint32_t top_s;
     __shared__ int warp_count[kThreads / 32 + 1];
     __shared__ int list_src[kThreads], list_pos[kThreads];
-    // launched without the early start itself: its successor may come as soon as there is room
-    pdl_release();
+    pdl_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) before_s = total_s = 0, top_s = 0u;
     __syncthreads();
@@ -808,8 +807,8 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     }
     // four rows to a CTA while there are few, two CTAs on an SM at most
     ra.per_cta = std::max<int64_t>(4, (c.rows + 2 * sm_count() - 1) / (2 * sm_count()));
-    k_xent_rows<<<(unsigned)std::max<int64_t>(1, (c.rows + ra.per_cta - 1) / ra.per_cta), kThreads, 0, s>>>(ra);
-    int rc = check_cuda(cudaGetLastError(), "row gathering launch");
+    int rc = check_cuda(launch_after(k_xent_rows, std::max<int64_t>(1, (c.rows + ra.per_cta - 1) / ra.per_cta), kThreads, 0, 1, s,
+                                     ra), "row gathering launch");
 
     ProductArgs p{};
     p.head = head;
