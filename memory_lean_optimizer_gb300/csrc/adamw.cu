@@ -347,9 +347,9 @@ __device__ __forceinline__ void read_block(Raw& x, const char* stage, const Tens
 // element before it is bound by their issue and not by memory, so three things are cut:
 //  - the update's root and quotient have no branch (above).
 //  - the codes' roots.  A code is the nearest integer to a root; an approximate root (relative error
-//    2^-23 by the instruction's specification, so below 1e-4 at 255) gives the same integer unless
-//    it lies within 1e-4 of the middle between two, and only a lane that has such a one
-//    (1 in 300) forms its eight codes from the exact roots.
+//    2^-23 by the instruction's specification, 2^-24 the exact one's rounding: 4.6e-5 at 255) gives
+//    the same integer unless it lies within 5e-5 of the middle between two, and only a lane that
+//    has such a one (1 in 600) forms its eight codes from the exact roots.
 //  - the block's constants.  Those of m and of v are the halves of one pair.
 // A block with a moment outside Range (an exact zero, an infinity or a NaN among them) or a weight that comes
 // out infinite or NaN is left to adamw_block as a whole: false, and nothing of it is stored.
@@ -448,7 +448,7 @@ __device__ __forceinline__ bool adamw_block_fast(const AdamWPrm& k, const Tensor
         split2(sub2(z, sub2(c, zero_v)), ya, yb);
         off = fmaxf(off, fmaxf(fabsf(ya), fabsf(yb)));
     }
-    if (off > 0.4999f) {
+    if (off > 0.49995f) {
 #pragma unroll 1
         for (int e = 0; e < 8; ++e) {   // rotated through the first place: no indexed registers
             const float me = m[0], se = -nsv[0];
