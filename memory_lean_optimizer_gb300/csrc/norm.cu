@@ -192,15 +192,16 @@ struct Coming {
         else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
     }
     __device__ __forceinline__ void fetch(int place, const T* row, int dim) const {
-        if (!kAsync) return;
+        if constexpr (kAsync) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = S::column(k);
-            if (V > 1) {
-                if (c < dim) copy(at(place, k), row + c);
-            } else {
-                if (c < dim) copy(at(place, 2 * k), row + c);
-                if (c + kT < dim) copy(at(place, 2 * k + 1), row + c + kT);
+            for (int k = 0; k < K; ++k) {
+                const int c = S::column(k);
+                if (V > 1) {
+                    if (c < dim) copy(at(place, k), row + c);
+                } else {
+                    if (c < dim) copy(at(place, 2 * k), row + c);
+                    if (c + kT < dim) copy(at(place, 2 * k + 1), row + c + kT);
+                }
             }
         }
     }
