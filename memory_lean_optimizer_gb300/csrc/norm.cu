@@ -448,24 +448,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_norm_backward(const TX* dy, 
     }
 }
 
-// Sum of the partial rows: column j of [2][dim] over `slices`, eight threads each a slice in eight, then their
-// sums in order.
+// Sum of the partial rows: column j of [2][dim] over `slices`, sixteen threads each a slice in sixteen, then
+// their sums in order.
 template <class TW>
-__global__ void __launch_bounds__(kThreads) k_norm_join(const float* __restrict__ partial, int slices, TW* __restrict__ dw,
+__global__ void __launch_bounds__(512) k_norm_join(const float* __restrict__ partial, int slices, TW* __restrict__ dw,
                                                         TW* __restrict__ db, int64_t dim) {
-    __shared__ float red[8][33];
+    __shared__ float red[16][33];
     pdl_sync();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t j = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.0f;
     if (j < 2 * dim)
 #pragma unroll 8
-        for (int k = ty; k < slices; k += 8) s += partial[(int64_t)k * 2 * dim + j];
+        for (int k = ty; k < slices; k += 16) s += partial[(int64_t)k * 2 * dim + j];
     red[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && j < 2 * dim) {
         s = red[0][tx];
-        for (int k = 1; k < 8; ++k) s += red[k][tx];
+        for (int k = 1; k < 16; ++k) s += red[k][tx];
         TW* const out = j < dim ? dw : db;
         if (out) store1(out + (j < dim ? j : j - dim), s);
     }
@@ -650,7 +650,7 @@ int forward_t(const NormForward& a, cudaStream_t s) {
 
 template <class TW>
 int join_slices(const NormBackward& a, int slices, cudaStream_t s) {
-    return check_cuda(launch_after(k_norm_join<TW>, (2 * a.dim + 31) / 32, kThreads, 0, 1, s, a.partial, slices,
+    return check_cuda(launch_after(k_norm_join<TW>, (2 * a.dim + 31) / 32, 512, 0, 1, s, a.partial, slices,
                                    static_cast<TW*>(a.dweight), static_cast<TW*>(a.dbias), a.dim),
                       "layer norm weight gradient launch");
 }

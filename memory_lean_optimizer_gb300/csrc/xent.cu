@@ -447,6 +447,7 @@ struct RowArgs {
     int32_t vocab, dim;
     const uint16_t* hidden;
     int64_t ldh;
+    bool vec;               // every row of hidden is whole 16-byte vectors
     int64_t per_cta;        // rows to a CTA, a multiple of kThreads or below it
     XentHead* head;
     uint16_t* hc;           // gathered rows, ldhc elements apart
@@ -539,10 +540,20 @@ __global__ void __launch_bounds__(kThreads) k_xent_rows(const RowArgs a) {
             else a.loss[n] = a.lse[n] = 0.0f;
         }
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < (int64_t)here * vecs; i += kThreads) {
-            const int k = (int)(i / vecs), c = (int)(i - (int64_t)k * vecs) * 8;
-            *reinterpret_cast<uint4*>(a.hc + (int64_t)list_pos[k] * a.ldhc + c) =
-                load_row8(a.hidden + (n0 + list_src[k]) * a.ldh, c, a.dim);
+        if (a.vec) {
+            const int all = here * vecs;   // at most 256 rows of vectors
+#pragma unroll 4
+            for (int i = threadIdx.x; i < all; i += kThreads) {
+                const int k = i / vecs, c = (i - k * vecs) * 8;
+                *reinterpret_cast<uint4*>(a.hc + (int64_t)list_pos[k] * a.ldhc + c) =
+                    *reinterpret_cast<const uint4*>(a.hidden + (n0 + list_src[k]) * a.ldh + c);
+            }
+        } else {
+            for (int64_t i = threadIdx.x; i < (int64_t)here * vecs; i += kThreads) {
+                const int k = (int)(i / vecs), c = (int)(i - (int64_t)k * vecs) * 8;
+                *reinterpret_cast<uint4*>(a.hc + (int64_t)list_pos[k] * a.ldhc + c) =
+                    load_row8(a.hidden + (n0 + list_src[k]) * a.ldh, c, a.dim);
+            }
         }
         if (a.dh && here < (int)min((int64_t)kThreads, end - n0)) {
             for (int64_t m = n0; m < min(end, n0 + kThreads); ++m) {
@@ -788,6 +799,7 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
     ra.dim = (int32_t)c.dim;
     ra.hidden = static_cast<const uint16_t*>(c.hidden);
     ra.ldh = c.ldh;
+    ra.vec = is_aligned(c.hidden, 16) && c.ldh % 8 == 0 && c.dim % 8 == 0 && c.dim < (1 << 22);
     ra.head = head;
     ra.hc = hc;
     ra.ldhc = pl.ldh;
