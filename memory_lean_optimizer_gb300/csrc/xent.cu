@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kTileN = 256;       // accumulator columns
 constexpr int kTileK = 64;        // one 128-byte swizzle row of bf16
-constexpr int kChunk = 8;         // kStats: blocks of K to an accumulator (512)
+constexpr int kChunk = 16;        // kStats: blocks of K to an accumulator (1024 products)
 constexpr int kProductThreads = 384;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-11 finish
 // Stages of 48 KiB (one CTA: 128 rows of A, 256 of B) or 32 KiB (a pair: 128 and 128 each).
 __host__ __device__ constexpr int product_stages(int cta) { return cta == 1 ? 4 : 6; }
