@@ -17,9 +17,9 @@ __device__ __forceinline__ void pdl_sync() {
 
 // Launches a kernel that waits for its predecessor itself (pdl_sync), as clusters of `cta`.
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t grid, dim3 block, size_t smem, int cta, cudaStream_t s, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cta, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

@@ -593,42 +593,45 @@ __global__ void __launch_bounds__(kThreads) k_xent_pack(const uint16_t* __restri
     if (first) pdl_sync();
 }
 
-// Joins a row's (maximum, sum) pairs of all 128-word tiles: 8 rows a CTA, 32 threads a row, a fixed order.
+// Joins a row's (maximum, sum) pairs of all 128-word tiles, kRows rows a CTA: a thread its share of the tiles, then
+// the lanes of a warp, then the warps, in a fixed order.  Latency bounds it: one row a CTA while
+// there are few (256 tiles: 16 rows 5.0 us against 6.0 with eight, 304 rows 5.8 against 6.2, 1024 rows
+// 8.5 against 6.2).
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) k_xent_loss(const XentHead* head, const float2* __restrict__ part, int tiles,
                                                         int64_t rows_pad, const float* __restrict__ target_logit,
                                                         const int32_t* __restrict__ target, const int32_t* __restrict__ row_of,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
-    __shared__ float2 red[32][9];
+    constexpr int kLanes = kThreads / kRows;
+    __shared__ float2 red[kThreads / 32][kRows];
     pdl_sync();
-    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int tx = threadIdx.x % kRows, ty = threadIdx.x / kRows;
     const int rows = head->rows;
     auto join = [](float2 a, float2 b) {
         const float m = fmaxf(a.x, b.x);
         if (m == -INFINITY) return make_float2(m, a.y + b.y);
         return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
     };
-    for (int64_t r0 = (int64_t)blockIdx.x * 8; r0 < rows; r0 += (int64_t)gridDim.x * 8) {
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
         const int64_t c = r0 + tx;
         float2 s = make_float2(-INFINITY, 0.0f);
         if (c < rows) {
-            for (int k = ty; k < tiles; k += 128) {   // four loads at a time
+            for (int k = ty; k < tiles; k += 4 * kLanes) {   // four loads at a time
                 float2 q[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = k + 32 * i < tiles ? part[(k + 32 * i) * rows_pad + c] : make_float2(-INFINITY, 0.0f);
+                for (int i = 0; i < 4; ++i)
+                    q[i] = k + kLanes * i < tiles ? part[(k + kLanes * i) * rows_pad + c] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s = join(s, q[i]);
             }
         }
-        red[ty][tx] = s;
+#pragma unroll
+        for (int o = kRows; o < 32; o <<= 1)
+            s = join(s, make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o), __shfl_xor_sync(0xFFFFFFFFu, s.y, o)));
+        if ((threadIdx.x & 31) < kRows) red[threadIdx.x >> 5][tx] = s;
         __syncthreads();
-        if (ty < 8) {
-            for (int k = ty + 8; k < 32; k += 8) s = join(s, red[k][tx]);
-        }
-        __syncthreads();
-        if (ty < 8) red[ty][tx] = s;
-        __syncthreads();
-        if (ty == 0 && c < rows) {
-            for (int k = 1; k < 8; ++k) s = join(s, red[k][tx]);
+        if (threadIdx.x < kRows && c < rows) {
+            for (int k = 1; k < kThreads / 32; ++k) s = join(s, red[k][tx]);
             const float l = s.x + logf(s.y);
             const int64_t n = row_of[c];
             lse[n] = l;
@@ -638,33 +641,41 @@ __global__ void __launch_bounds__(kThreads) k_xent_loss(const XentHead* head, co
     }
 }
 
-// dH rows from the fp32 parts of a split K, in their order; zero for rows left out.
+// dH rows from the fp32 parts of a split K; zero for rows left out.  A CTA takes 128 columns of a row, 32 lanes
+// four each, its eight warps every eighth part; then the warps' sums in order (16 rows x 4096, nine
+// parts: 4.2 us; 1024 x 2048, two parts: 20 us).
 __global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, const int32_t* __restrict__ pos_of,
                                                           const float* __restrict__ acc, int splits, int64_t rows_pad,
-                                                          int64_t ldacc, uint16_t* __restrict__ dh, int64_t lddh, int64_t rows,
-                                                          int dim, bool vec) {
+                                                          int64_t ldacc, uint16_t* __restrict__ dh, int64_t lddh, int dim,
+                                                          bool vec) {
+    __shared__ float4 red[kThreads / 32][32];
     pdl_sync();
-    const float g = head->grad_scale;
-    for (int64_t n = blockIdx.x; n < rows; n += gridDim.x) {
-        const int64_t c = pos_of[n];
-        for (int i = threadIdx.x * 4; i < dim; i += kThreads * 4) {
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c >= 0) {
-#pragma unroll 4
-                for (int s = 0; s < splits; ++s) {
-                    const float4 y = *reinterpret_cast<const float4*>(acc + ((int64_t)s * rows_pad + c) * ldacc + i);
-                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                }
-            }
-            uint16_t* const o = dh + n * lddh + i;
-            const uint32_t lo = bf16_pair(x.x * g, x.y * g), hi = bf16_pair(x.z * g, x.w * g);
-            if (vec && i + 4 <= dim) {
-                *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
-            } else {
-                const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-                for (int j = 0; j < 4 && i + j < dim; ++j) o[j] = h[j];
-            }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = blockIdx.x, c = pos_of[n];
+    const int i = blockIdx.y * 128 + 4 * lane;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c >= 0 && i < dim) {
+#pragma unroll 8
+        for (int s = warp; s < splits; s += kThreads / 32) {
+            const float4 y = *reinterpret_cast<const float4*>(acc + ((int64_t)s * rows_pad + c) * ldacc + i);
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
+    }
+    red[warp][lane] = x;
+    __syncthreads();
+    if (warp != 0 || i >= dim) return;
+    for (int k = 1; k < kThreads / 32; ++k) {
+        const float4 y = red[k][lane];
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    const float g = head->grad_scale;
+    uint16_t* const o = dh + n * lddh + i;
+    const uint32_t lo = bf16_pair(x.x * g, x.y * g), hi = bf16_pair(x.z * g, x.w * g);
+    if (vec && i + 4 <= dim) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+    } else {
+        const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+        for (int j = 0; j < 4 && i + j < dim; ++j) o[j] = h[j];
     }
 }
 
@@ -817,8 +828,8 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
         ra.loss = c.loss;
         ra.lse = c.lse;
     }
-    // four rows to a CTA while there are few, two CTAs on an SM at most
-    ra.per_cta = std::max<int64_t>(4, (c.rows + 2 * sm_count() - 1) / (2 * sm_count()));
+    // a row to a CTA while there are few (64 rows: 4.3 us against 5.8 with four), two CTAs on an SM at most
+    ra.per_cta = std::max<int64_t>(1, (c.rows + 2 * sm_count() - 1) / (2 * sm_count()));
     int rc = check_cuda(launch_after(k_xent_rows, std::max<int64_t>(1, (c.rows + ra.per_cta - 1) / ra.per_cta), kThreads, 0, 1, s,
                                      ra), "row gathering launch");
 
@@ -897,14 +908,17 @@ int launch_xent(const XentCall& c, cudaStream_t s) {
         }
     }
     if (rc) return rc;
-    if (!c.backward)
-        return check_cuda(launch_after(k_xent_loss, std::min<int64_t>((c.rows + 7) / 8, (int64_t)sm_count() * 8), kThreads, 0, 1, s,
+    if (!c.backward) {
+        const bool few = c.rows <= 2 * sm_count();
+        return check_cuda(launch_after(few ? k_xent_loss<1> : k_xent_loss<8>,
+                                       few ? c.rows : std::min<int64_t>((c.rows + 7) / 8, (int64_t)sm_count() * 8), kThreads, 0, 1, s,
                                        head, p.part, (int)((c.vocab + 127) / 128), pl.rows_pad, p.target_logit, target_of,
                                        row_of, c.loss, c.lse), "loss launch");
+    }
     if (!c.d_hidden || c.rows == 0 || pl.splits == 1) return OPTIM_OK;
     const bool vec = is_aligned(c.d_hidden, 8) && c.lddh % 4 == 0;
-    return check_cuda(launch_after(k_xent_hidden, std::min<int64_t>(c.rows, (int64_t)sm_count() * 16), kThreads, 0, 1, s, head,
-                                   pos_of, p.acc, pl.splits, pl.rows_pad, pl.ldacc, p.dh, c.lddh, c.rows, (int)c.dim, vec),
+    return check_cuda(launch_after(k_xent_hidden, dim3((unsigned)c.rows, (unsigned)((c.dim + 127) / 128)), kThreads, 0, 1, s, head,
+                                   pos_of, p.acc, pl.splits, pl.rows_pad, pl.ldacc, p.dh, c.lddh, (int)c.dim, vec),
                       "hidden gradient launch");
 }
 
