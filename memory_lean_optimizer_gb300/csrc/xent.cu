@@ -29,7 +29,7 @@ constexpr int kChunk = 16;        // kStats: blocks of K to an accumulator (1024
 constexpr int kProductThreads = 384;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-11 finish
 // Stages of 48 KiB (one CTA: 128 rows of A, 256 of B) or 32 KiB (a pair: 128 and 128 each).
 __host__ __device__ constexpr int product_stages(int cta) { return cta == 1 ? 4 : 6; }
-constexpr int kFinishBytes = 8 * 32 * 34 * 2;   // a 32 x 32 bf16 block for each finishing warp, rows 68 bytes apart
+constexpr int kFinishBytes = 8 * 32 * 128;      // 32 rows of 128 bytes for each finishing warp (Stage)
 constexpr uint32_t kTmemColumns = 512; // two accumulators of 256 columns
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -63,7 +63,7 @@ struct ProductArgs {
     int32_t first, last;        // kHidden: the first piece (nothing to add to), the last (dH itself; not if K is split)
     uint16_t* dh;               // kHidden
     int64_t lddh;
-    int32_t dh_aligned;         // bytes that every row of dH starts on a multiple of: 32, 4 or 2
+    int32_t dh_aligned;         // bytes that every row of dH starts on a multiple of: 16, 8, 4 or 2
     const int32_t* row_of;      // kHidden: gathered row -> row of dH
     uint16_t* dw;               // kWeight: dW, row b_off + m
     int64_t lddw;
@@ -87,6 +87,30 @@ __device__ __forceinline__ void store_32b(uint16_t* p, const uint32_t* r) {
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+
+// A finishing warp's corner of shared memory: a lane holds a row of the tile, but memory wants whole lines, so 32
+// rows of 128 bytes are turned round in it -- each lane puts its row, then eight lanes take 16 bytes
+// each of one row, four rows at a time.  The 16-byte pieces of row i lie at their number XOR i mod 8:
+// neither side meets a bank twice.  dW of 16 rows x 4096 x 131072, all of it writing (1.07 GB), takes 235 us
+// so; 32 bytes a lane written straight to memory keep L2 busy with single sectors: 283 us.
+struct Stage {
+    char* base;
+    __device__ __forceinline__ void put(int lane, const uint32_t* w) const {   // 32 words
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(base + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+    __device__ __forceinline__ uint4 get(int row, int q) const {
+        return *reinterpret_cast<const uint4*>(base + row * 128 + ((q ^ (row & 7)) << 4));
+    }
+    __device__ __forceinline__ uint32_t word(int row, int i) const {   // 32 bits
+        return *reinterpret_cast<const uint32_t*>(base + row * 128 + (((i >> 2) ^ (row & 7)) << 4) + 4 * (i & 3));
+    }
+    __device__ __forceinline__ uint16_t half(int row, int i) const {   // 16 bits
+        return *reinterpret_cast<const uint16_t*>(base + row * 128 + (((i >> 3) ^ (row & 7)) << 4) + 2 * (i & 7));
+    }
+};
 
 // Loads one K block of an operand: `rows` rows of M or N from `mn`, 64 of K from `k`.
 template <bool kMn, int kRows, int kCta>
@@ -247,8 +271,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         if (kMode == kStats) regs_up<232>();
         const int w = warp & 3, half = (warp >> 2) - 1;   // tensor memory lanes are dealt to warps by warp % 4
         const uint32_t lanes = (uint32_t)(32 * w) << 16;
-        uint16_t(*const stage)[34] = reinterpret_cast<uint16_t(*)[34]>(
-            smem_raw + (tiles - smem_u32(smem_raw)) + kStages * kStage + (warp - 4) * 32 * 34 * 2);
+        const Stage stage{reinterpret_cast<char*>(smem_raw) + (tiles - smem_u32(smem_raw)) + kStages * kStage + (warp - 4) * 32 * 128};
         int buf = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
@@ -257,10 +280,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         };
+        // Hands the accumulator back.  The arrival waits for the thread's stores to be seen (by the pair, in L2,
+        // if there is one), so it comes before a tile's last stores, not behind them (16 x 4096 x 131072:
+        // backward 664 us behind them, 574 before).
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && ok) mbar_arrive_cluster(kCta == 2 ? cluster_addr(free0 + 8 * buf, 0) : free0 + 8 * buf);
+            if (lane == 0 && ok) {
+                if (kCta == 2) mbar_arrive_cluster(cluster_addr(free0 + 8 * buf, 0));
+                else mbar_arrive(free0 + 8 * buf);
+            }
             if (++buf == 2) buf = 0, buf_phase ^= 1u;
         };
         constexpr float kNan = __builtin_nanf("");
@@ -331,86 +360,114 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) r[j / 2] = bf16_pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                    if (c == 96) release();   // before the last stores: see release
                     store_32b(out + c, r);
                     store_32b(out + c + 16, r + 8);
+                }
+                continue;
+            }
+            const float g = p.head->grad_scale;
+            if (kMode == kHidden) {
+                // fp32, in the order of the pieces: one launch per piece, one lane per element
+                const int64_t to_row = row < rows && p.last ? p.row_of[row] : -1;   // of dH
+                const int first_row = row - lane, q = lane & 7;
+                float* const part = p.acc + ((int64_t)split * p.rows_pad + first_row) * p.ldacc + c0 + 4 * q;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    if (c0 + c >= p.dim) break;
+                    uint32_t r[32];
+                    tmem_load32(acc + c, r);
+                    tmem_wait(r);
+                    if (none || !ok) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = ok ? 0u : 0x7FC00000u;
+                    }
+                    stage.put(lane, r);
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = lane >> 3; i < 32; i += 4) {
+                        const int64_t to = __shfl_sync(0xFFFFFFFFu, to_row, i);
+                        if (first_row + i >= rows) continue;
+                        const uint4 v = stage.get(i, q);
+                        float4 x = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+                        float4* const sum = reinterpret_cast<float4*>(part + i * p.ldacc + c);
+                        if (!p.first) {
+                            const float4 y = *sum;
+                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                        }
+                        if (!p.last) {
+                            *sum = x;
+                            continue;
+                        }
+                        uint16_t* const o = p.dh + to * p.lddh + c0 + c + 4 * q;
+                        const uint2 y = make_uint2(bf16_pair(x.x * g, x.y * g), bf16_pair(x.z * g, x.w * g));
+                        const int left = p.dim - (c0 + c + 4 * q);
+                        if (p.dh_aligned >= 8 && left >= 4) {
+                            *reinterpret_cast<uint2*>(o) = y;
+                        } else {
+                            const uint16_t h[4] = {(uint16_t)y.x, (uint16_t)(y.x >> 16), (uint16_t)y.y, (uint16_t)(y.y >> 16)};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (j < left) o[j] = h[j];
+                        }
+                    }
+                    __syncwarp();
                 }
                 release();
                 continue;
             }
-            // the gradients: this thread's row of dH or dW (-1: none), or of the fp32 sums
-            const bool sums = kMode == kHidden && !p.last;
-            const int64_t out_row = kMode == kHidden ? (row < rows && p.last ? p.row_of[row] : -1)
-                                                     : (p.v_off + row < p.vocab ? p.v_off + row : -1);
-            uint16_t* const out_base = kMode == kHidden ? p.dh : p.dw;
-            const int64_t ld = kMode == kHidden ? p.lddh : p.lddw;
-            const bool aligned = (kMode == kHidden ? p.dh_aligned : p.dw_aligned) == 32;
-            const bool words = (kMode == kHidden ? p.dh_aligned : p.dw_aligned) >= 4;
-            const float g = sums ? 1.0f : p.head->grad_scale;
-            float* const part = kMode == kHidden ? p.acc + ((int64_t)split * p.rows_pad + row) * p.ldacc + c0 : nullptr;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                const int left = p.dim - (c0 + c);
-                if (left <= 0) break;
-                uint32_t r[32];
-                tmem_load32(acc + c, r);
-                tmem_wait(r);
+            const int first_v = p.v_off + row - lane;   // of the warp's 32 rows of dW
+            uint16_t* const out = p.dw + first_v * p.lddw + c0;
+            const int have = min(32, p.vocab - first_v);
+            auto take = [&](int c, uint32_t* o) {       // 64 columns
+#pragma unroll
+                for (int h = 0; h < 64; h += 32) {
+                    uint32_t r[32];
+                    tmem_load32(acc + c + h, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        o[(h + j) / 2] = bf16_pair(__uint_as_float(r[j]) * g, __uint_as_float(r[j + 1]) * g);
+                }
                 if (none || !ok) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = ok ? 0u : 0x7FC00000u;
+                    for (int j = 0; j < 32; ++j) o[j] = ok ? 0u : 0x7FC07FC0u;
                 }
-                if (kMode == kHidden && row < rows) {   // one launch per piece, one thread per element: the order is the pieces'
+            };
+            auto write = [&](int c, const uint32_t* o) {
+                const int left = p.dim - (c0 + c);
+                if (left <= 0) return;
+                stage.put(lane, o);
+                __syncwarp();
+                if (p.dw_aligned == 16 && left >= 64) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        float4* const o = reinterpret_cast<float4*>(part + c) + q;
-                        float4 x = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                               __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-                        if (!p.first) {
-                            const float4 y = *o;
-                            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                        }
-                        if (sums) {
-                            *o = x;
-                        } else {
-                            r[4 * q] = __float_as_uint(x.x), r[4 * q + 1] = __float_as_uint(x.y);
-                            r[4 * q + 2] = __float_as_uint(x.z), r[4 * q + 3] = __float_as_uint(x.w);
-                        }
+                    for (int i = lane >> 3; i < 32; i += 4)
+                        if (i < have) *reinterpret_cast<uint4*>(out + i * p.lddw + c + 8 * (lane & 7)) = stage.get(i, lane & 7);
+                } else if (p.dw_aligned >= 4) {        // a row at a time, two elements a lane
+                    const int l = 2 * lane;
+#pragma unroll 4
+                    for (int i = 0; i < have; ++i) {
+                        const uint32_t x = stage.word(i, lane);
+                        uint16_t* const at = out + i * p.lddw + c + l;
+                        if (l + 1 < left) *reinterpret_cast<uint32_t*>(at) = x;
+                        else if (l < left) *at = (uint16_t)x;
+                    }
+                } else {
+#pragma unroll 4
+                    for (int i = 0; i < have; ++i) {
+                        uint16_t* const at = out + i * p.lddw + c + lane;
+                        if (lane < left) at[0] = stage.half(i, lane);
+                        if (lane + 32 < left) at[32] = stage.half(i, lane + 32);
                     }
                 }
                 __syncwarp();
-                if (sums) continue;
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) r[j / 2] = bf16_pair(__uint_as_float(r[j]) * g, __uint_as_float(r[j + 1]) * g);
-                if (aligned && left >= 32) {
-                    if (out_row >= 0) {
-                        uint16_t* const o = out_base + out_row * ld + c0 + c;
-                        store_32b(o, r);
-                        store_32b(o + 16, r + 8);
-                    }
-                } else {   // through shared memory, so that a warp writes 32 neighbours of one row at a time
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint32_t*>(&stage[lane][2 * j]) = r[j];
-                    __syncwarp();
-                    if (words) {           // rows start on 4 bytes: half a warp to a row, two elements a lane
-                        const int l = 2 * (lane & 15);
-#pragma unroll 4
-                        for (int i = lane >> 4; i < 32; i += 2) {
-                            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
-                            const uint32_t x = *reinterpret_cast<const uint32_t*>(&stage[i][l]);
-                            uint16_t* const o = out_base + to * ld + c0 + c + l;
-                            if (to >= 0 && l + 1 < left) *reinterpret_cast<uint32_t*>(o) = x;
-                            else if (to >= 0 && l < left) *o = (uint16_t)x;
-                        }
-                    } else {
-#pragma unroll 4
-                        for (int i = 0; i < 32; ++i) {
-                            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, i);
-                            if (to >= 0 && lane < left) out_base[to * ld + c0 + c + lane] = stage[i][lane];
-                        }
-                    }
-                }
-                __syncwarp();
-            }
+            };
+            uint32_t o[64];
+            take(0, o);
+            take(64, o + 32);
             release();
+            write(0, o);
+            write(64, o + 32);
         }
     }
     tc_fence_before();
@@ -683,8 +740,9 @@ __global__ void __launch_bounds__(kThreads) k_xent_hidden(const XentHead* head, 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 int row_alignment(const void* p, int64_t ld) {
-    if (is_aligned(p, 32) && ld % 16 == 0) return 32;
-    return is_aligned(p, 4) && ld % 2 == 0 ? 4 : 2;
+    for (int a : {16, 8, 4})
+        if (is_aligned(p, a) && ld % (a / 2) == 0) return a;
+    return 2;
 }
 
 // Sizes and workspace layout of a call.
