@@ -9,6 +9,7 @@ README: per-parameter hook, optimizer groups of 4-10).
 """
 from __future__ import annotations
 
+import functools
 from typing import Sequence
 
 import torch
@@ -125,12 +126,17 @@ class _Group:
         """Copy-out after the last step of a group attached with attach_host()."""
         lmopt.optim_offload_writeback(self.handle, 0 if stream is None else int(stream.cuda_stream))
 
+    @functools.cached_property
+    def _numels(self):
+        return [w.numel() for w in self.weights]
+
     def _grad_ptrs(self, grads):
-        assert len(grads) == len(self.weights)
-        ptrs = []
-        for g, w in zip(grads, self.weights):
-            assert g.dtype == torch.bfloat16 and g.is_contiguous() and g.numel() == w.numel()
-            ptrs.append(g.data_ptr() if g.numel() else None)
+        # on every step's way to the GPU: a third of a microsecond for each tensor
+        assert len(grads) == len(self._numels)
+        bf16, ptrs = torch.bfloat16, []
+        for g, n in zip(grads, self._numels):
+            assert g.dtype is bf16 and g.is_contiguous() and g.numel() == n
+            ptrs.append(g.data_ptr() if n else 0)
         return ptrs
 
 

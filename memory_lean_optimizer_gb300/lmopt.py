@@ -7,6 +7,7 @@ there is no fallback, and a missing library raises at first use.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -176,10 +177,8 @@ def check(rc: int) -> int:
 
 
 def _ptr_array(ptrs):
-    arr = (ctypes.c_void_p * max(1, len(ptrs)))()
-    for i, p in enumerate(ptrs):
-        arr[i] = p
-    return arr
+    """The addresses (None: 0) as a C array of pointers."""
+    return (ctypes.c_void_p * max(1, len(ptrs))).from_buffer(array.array("Q", [p or 0 for p in ptrs] or [0]))
 
 
 # ------------------------------------------------------------------ raw entry points (same names)
