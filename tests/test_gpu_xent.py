@@ -69,6 +69,12 @@ def test_sizes(rows, dim, vocab):
     check(*inputs(rows, dim, vocab))
 
 
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("dim", [32, 33, 96, 160, 257, 288, 320, 400, 520, 776, 1032])
+def test_columns_shared_between_tiles(rows, dim):
+    check(*inputs(rows, dim, 1300))
+
+
 @pytest.mark.parametrize("scale", [0.0, 30.0])
 def test_flat_and_peaked_distributions(scale):
     check(*inputs(200, 256, 3000, scale=scale))
