@@ -456,7 +456,7 @@ int norm_layer_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx
  * hidden [rows][dim] and weight [vocab][dim] are bf16 (the gradients of fp16 logits would underflow), the
  * products and sums fp32, loss and lse fp32 [rows].  A row whose target is ignore_index costs
  * no product and has loss 0 and lse 0, whatever its hidden state holds; a target outside the vocabulary
- * makes its row's loss NaN.  Scratch is the gathered rows and 8 bytes per row and 256 words.
+ * makes its row's loss NaN.  Scratch is the gathered rows and 8 bytes per row and 128 words.
  * weight, ldw and the sizes of loss_xent_workspace are those of the call it is for.  workspace: 256-byte
  * aligned.  Matrices that are not 16-byte aligned with row strides of a multiple of 8 elements are
  * copied on the way (hidden always is; weight by pieces of the vocabulary). */

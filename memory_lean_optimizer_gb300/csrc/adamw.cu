@@ -13,6 +13,10 @@
 //   code_v = rint(sqrt(sqrt(v) r_v)),           v = (z z)(z z), z = code_v q_v
 // A positive v keeps a code of at least 1: decoded to zero, it would leave a kept m divided by eps
 // alone in a later step whose gradient is zero.
+//
+// 278M elements, 8 bits with Kahan residuals: 690 us for 3.9 GB (5.7 TB/s), bound by instruction issue (67 an
+// element: the update's root and quotient, four code roots, their checks); a kernel that moves the same
+// bytes and computes nothing takes 552 us.  120M elements with fp32 states: 467 us, at the copy rate.
 #include "internal.h"
 #include "launch.cuh"
 #include "packed.cuh"

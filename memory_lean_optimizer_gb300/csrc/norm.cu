@@ -4,6 +4,10 @@
 // Values are fp32 from load to store, whatever the types; the variance is taken around the mean
 // (a second sum over the row), not as a difference of squares.  Sums run in a fixed order, so two
 // runs agree bit for bit.
+//
+// 16384 x 4096 bf16: forward 60 us (4.5 TB/s of the bytes that it must move), backward 83 us (4.9 TB/s).
+// Neither waits for memory alone: instructions issue in 60-70 % of the cycles (23 an element over both), and
+// the registers that hold the rows leave few warps to cover the reductions' chains of shuffles.
 #include <cuda_bf16.h>
 
 #include <algorithm>

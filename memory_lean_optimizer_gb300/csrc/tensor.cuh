@@ -104,12 +104,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
             "l"(map), "r"(x), "r"(y), "r"(bar)
             : "memory");
 }
-// `bytes` (a multiple of 16, both addresses too) from global into shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
