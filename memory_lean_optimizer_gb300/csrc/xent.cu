@@ -187,13 +187,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     // unit -> split, then tiles in strips of 8 columns, rows of tiles within a strip: the units in
     // flight at one time share their rows of A and columns of B in L2
     auto unit_tile = [&](int u, int& m, int& n, int& k0, int& k1, int& split) {
-        const int per = m_tiles * p.n_tiles;
-        split = u / per;
-        u -= split * per;
+        split = 0;
+        if (p.splits > 1) {
+            const int per = m_tiles * p.n_tiles;
+            split = u / per;
+            u -= split * per;
+        }
         const int strip = u / (m_tiles * 8), in = u - strip * m_tiles * 8;
         const int width = min(8, p.n_tiles - strip * 8);
-        m = in / width;
-        n = strip * 8 + in % width;
+        m = width == 8 ? in >> 3 : in / width;
+        n = strip * 8 + in - m * width;
         k0 = min(k_blocks, split * per_split);
         k1 = min(k_blocks, k0 + per_split);
     };
