@@ -27,7 +27,10 @@
  *    optim_group_create); LMOPT_FAULT_INJECT=h2d|d2h|alloc makes the offload path fail with
  *    OPTIM_ECUDA / OPTIM_ENOMEM before it enqueues anything, and =timeout makes every bounded
  *    host wait return OPTIM_ETIMEOUT at once (host-side tests of the error paths; nothing on the
- *    GPU is disturbed).
+ *    GPU is disturbed).  =stall_<stats|grad|hidden|weight>_<copy|peer|free> lets the bounded waits
+ *    inside that product kernel of the cross entropy run out after a tenth of a second: its first
+ *    cluster stops copying (one of its CTAs) or keeps its accumulators, and every wait behind that
+ *    ends by its limit.
  */
 #ifndef LMOPT_H
 #define LMOPT_H

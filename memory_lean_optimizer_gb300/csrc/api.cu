@@ -53,6 +53,8 @@ bool fault_injected(const char* what) {
     return f && std::strcmp(f, what) == 0;
 }
 
+bool faults_injected() { return std::getenv("LMOPT_FAULT_INJECT") != nullptr; }
+
 // Bounded host wait: polls the event until it completes or `timeout_s` passes.  With
 // LMOPT_FAULT_INJECT=timeout every wait runs out at once (tests of the error path; nothing on
 // the GPU is disturbed).

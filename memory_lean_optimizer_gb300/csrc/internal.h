@@ -12,8 +12,10 @@
 namespace lmo {
 
 // True when the environment variable LMOPT_FAULT_INJECT equals `what` (host-side fault
-// injection for the error-path tests: h2d, d2h, alloc, timeout).
+// injection for the error-path tests: h2d, d2h, alloc, timeout, stall_*).
 bool fault_injected(const char* what);
+// True when it is set at all.
+bool faults_injected();
 // Records the thread-local error message and returns `code`.
 int set_error(int code, const char* fmt, ...);
 // OPTIM_OK if e == cudaSuccess, else records "<what>: <cuda message>" and returns OPTIM_ECUDA.

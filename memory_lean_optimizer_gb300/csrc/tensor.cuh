@@ -70,10 +70,26 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for the phase `parity` of a barrier, for kWaitNs at most or until another wait of the CTA has
-// given up (*gave_up); false: it did not complete.
+// Counts `bytes` of copies as arrived without a copy.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// A 32-bit word in the shared memory of any CTA of the cluster (address from cluster_addr).
+__device__ __forceinline__ void store_cluster(uint32_t addr, int value) {
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(value) : "memory");
+}
+__device__ __forceinline__ int load_cluster(uint32_t addr) {
+    int value;
+    asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];" : "=r"(value) : "r"(addr) : "memory");
+    return value;
+}
+
+// Waits for the phase `parity` of a barrier, for `ns` at most or until another wait of the cluster has given up
+// (*gave_up, a shared word of each CTA that is raised in both of a pair, so that neither works on alone);
+// false: it did not complete.
 constexpr uint64_t kWaitNs = 4000000000ull;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+template <int kCta>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
     if (mbar_try(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
@@ -81,11 +97,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity)) return true;
         if (*gave_up) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (global_ns() - t0 > ns) {
             *gave_up = 1;
+            if (kCta == 2) store_cluster(cluster_addr(smem_u32(const_cast<int*>(gave_up)), cluster_rank() ^ 1u), 1);
             return false;
         }
     }
+}
+// The same after a wait has given up, for what is in flight.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+    int never = 0;
+    mbar_wait<1>(bar, parity, &never, kWaitNs);
 }
 
 // ---- TMA: a box of a 2-D tensor map into shared memory, completing on `bar` ----

@@ -21,6 +21,7 @@
 // limit's rate.  Few rows: the weight's bytes.  16 x 4096 x 131072 (1.07 GB) takes 182 us forward (5.9 TB/s)
 // and 570 us backward, where it is read twice and written once.
 #include <algorithm>
+#include <cstdio>
 
 #include "internal.h"
 #include "launch.cuh"
@@ -75,7 +76,11 @@ struct ProductArgs {
     uint16_t* dw;               // kWeight: dW, row b_off + m
     int64_t lddw;
     int32_t dw_aligned;         // kWeight: the same of dW
+    uint64_t wait_ns;           // a wait's limit
+    int32_t stall;              // tests of that limit: what the first cluster withholds (Stall), or 0
 };
+// One copying thread's blocks after the second (of the pair's first or second CTA), or the accumulators.
+enum Stall { kStallCopy = 1, kStallPeer = 2, kStallFree = 3 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -137,9 +142,11 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 // long K that is a drift, ten times the error of rounded fp32 sums at K = 4096, which the loss
 // would show.  kStats therefore starts a new accumulator every kChunk blocks of K and adds them up
 // in registers, rounded to nearest; the other accumulator hides the extra reading of tensor memory.
-// Every wait is bounded (mbar_wait); one that runs out raises gave_up and each role stops at its next
-// wait: copies and products in flight are waited for (bounded too), the finishing warps write NaN
-// for what they did not get, and the kernel returns with tensor memory freed.
+// Every wait is bounded (mbar_wait); one that runs out raises gave_up in all CTAs of the cluster and each role
+// stops at its next wait.  A tile is finished only behind its own products' completion (nothing else
+// arrives on the done barriers); the finishing warps write NaN for what they did not get.  When every
+// role has stopped, copies and products in flight are waited for, bounded too, and the kernel returns
+// with tensor memory freed.
 template <int kMode, int kCta>
 __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ CUtensorMap map_a,
                                                                 const __grid_constant__ CUtensorMap map_b,
@@ -149,11 +156,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     constexpr int kRowsB = kTileN / kCta;
     constexpr uint32_t kBytesA = 128 * kTileK * 2, kBytesB = kRowsB * kTileK * 2, kStage = kBytesA + kBytesB;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 * kStages + 4];
+    __shared__ uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up;
+    __shared__ int copied;   // blocks of K that this CTA's copying thread has issued, when it has stopped
     const uint32_t tiles = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, done0 = empty0 + 8 * kStages, free0 = done0 + 16;
+    const uint32_t drained = free0 + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kCta == 2 ? cluster_rank() : 0u;
     if (threadIdx.x == 0) {
@@ -166,6 +175,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
             mbar_init(done0 + 8 * i, 1);
             mbar_init(free0 + 8 * i, 8 * kCta);
         }
+        mbar_init(drained, 1);
         mbar_init_fence();
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
@@ -176,6 +186,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     if (kCta == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<kCta>(bar, parity, &gave_up, p.wait_ns); };
     pdl_sync();
 
     const int rows = p.head->rows;
@@ -206,6 +217,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     if (warp < 4) {
         if (kMode == kStats) regs_down<40>();
         if (warp == 0 && elect_lane()) {
+            const int stop = first_unit == 0 && p.stall == kStallCopy + (int)rank ? 2 : 0x7FFFFFFF;
             int stage = 0;
             uint32_t phase = 0;
             int issued = 0;
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 unit_tile(u, m, n, k0, k1, split);
                 const int am = (m * kCta + (int)rank) * 128, bn = n * kTileN + (int)rank * kRowsB;
                 for (int kb = k0; kb < k1; ++kb) {
-                    ok = mbar_wait(empty0 + 8 * stage, phase ^ 1u, &gave_up);
+                    ok = issued != stop && wait(empty0 + 8 * stage, phase ^ 1u);
                     if (!ok) break;
                     const uint32_t bar = kCta == 2 ? cluster_addr(full0 + 8 * stage, 0) : full0 + 8 * stage;
                     if (rank == 0) mbar_expect_tx(full0 + 8 * stage, kStage * kCta);
@@ -229,14 +241,10 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     if (++stage == kStages) stage = 0, phase ^= 1u;
                 }
             }
-            // copies still in flight land before the CTA ends: on giving up nobody else waits for them
-            if (!ok && rank == 0) {
-                for (int i = 0; i < min(issued, kStages); ++i) {
-                    if (--stage < 0) stage = kStages - 1, phase ^= 1u;
-                    int never = 0;
-                    mbar_wait(full0 + 8 * stage, phase, &never);
-                }
-            }
+            // the last stages come back before the CTA ends: nothing arrives on its barriers after that
+            for (int i = max(0, issued - kStages); ok && i < issued; ++i)
+                ok = wait(empty0 + 8 * (i % kStages), i / kStages & 1);
+            copied = issued;
         } else if (warp == 1 && rank == 0 && elect_lane()) {
             constexpr uint32_t idesc = mma_desc(128 * kCta, kTileN, kAMn, kBMn);
             constexpr uint32_t step_a = kAMn ? 2048u : 32u, step_b = kBMn ? 2048u : 32u;
@@ -249,11 +257,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 int k = k0;
                 do {
                     const int end = chunk_end(k, k1);
-                    ok = mbar_wait(free0 + 8 * buf, buf_phase ^ 1u, &gave_up);
+                    ok = wait(free0 + 8 * buf, buf_phase ^ 1u);
                     if (!ok) break;
                     tc_fence_after();
                     for (int kb = k; kb < end; ++kb) {
-                        ok = mbar_wait(full0 + 8 * stage, phase, &gave_up);
+                        ok = wait(full0 + 8 * stage, phase);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t a = tiles + stage * kStage, b = a + kBytesA;
@@ -270,11 +278,6 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     k = end;
                 } while (k < k1);
             }
-            if (!ok) {   // products in flight end before tensor memory is freed
-                int never = 0;
-                mma_commit<kCta>(done0 + 8 * buf);
-                mbar_wait(done0 + 8 * buf, buf_phase, &never);
-            }
         }
         __syncwarp();
     } else {
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         uint32_t buf_phase = 0;
         bool ok = true;
         auto wait_done = [&]() {
-            if (ok) ok = mbar_wait(done0 + 8 * buf, buf_phase, &gave_up);
+            if (ok) ok = wait(done0 + 8 * buf, buf_phase);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         };
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && ok) {
+            if (lane == 0 && ok && !(p.stall == kStallFree && blockIdx.x < kCta)) {
                 if (kCta == 2) mbar_arrive_cluster(cluster_addr(free0 + 8 * buf, 0));
                 else mbar_arrive(free0 + 8 * buf);
             }
@@ -484,6 +487,26 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     tc_fence_before();
     __syncthreads();
     if (kCta == 2) cluster_sync();
+    // every role of the cluster has stopped: the flag is the same for all of its threads
+    if (*static_cast<volatile int*>(&gave_up)) {
+        const bool leader = kCta == 1 || cluster_rank() == 0u;   // read again: a register less over the loops above
+        if (warp == 0 && elect_lane() && leader) {
+            // Both CTAs' copies are counted on the first one's barriers; their threads may have stopped at different blocks.
+            const int mine = copied, other = kCta == 2 ? load_cluster(cluster_addr(smem_u32(&copied), 1)) : mine;
+            const int most = max(mine, other);
+            for (int i = max(0, most - kStages); i < most; ++i) {   // blocks before these have been multiplied
+                const uint32_t bar = full0 + 8 * (i % kStages);
+                if (i >= mine) mbar_expect_tx(bar, kStage);            // the other's half alone
+                else if (i >= other) mbar_complete_tx(bar, kStage);    // the other's half will not come
+                mbar_drain(bar, i / kStages & 1);
+            }
+        } else if (warp == 1 && elect_lane()) {   // the thread that multiplied, and in the other CTA the one that would
+            if (leader) mma_commit<kCta>(drained);
+            mbar_drain(drained, 0);
+        }
+        __syncthreads();
+        if (kCta == 2) cluster_sync();
+    }
     tc_fence_after();
     if (warp == 2) tmem_free<kCta>(tmem, kTmemColumns);
 }
@@ -848,13 +871,28 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
     return OPTIM_OK;
 }
 
+// LMOPT_FAULT_INJECT=stall_<stats|grad|hidden|weight>_<copy|peer|free>: what that product's first cluster
+// withholds, so that its waits run out (tests).
+int injected_stall(int mode) {
+    static const char* const roles[] = {"stats", "grad", "hidden", "weight"};
+    static const char* const what[] = {"copy", "peer", "free"};
+    char name[32];
+    for (int i = 0; i < 3; ++i) {
+        std::snprintf(name, sizeof name, "stall_%s_%s", roles[mode], what[i]);
+        if (fault_injected(name)) return kStallCopy + i;
+    }
+    return 0;
+}
+
 template <int kMode, int kCta>
-int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p, cudaStream_t s) {
+int launch_product_t(const CUtensorMap& a, const CUtensorMap& b, ProductArgs p, cudaStream_t s) {
     constexpr int kSmem = 1024 + product_stages(kCta) * (128 + kTileN / kCta) * kTileK * 2 + kFinishBytes;
     auto kernel = k_product<kMode, kCta>;
     static std::atomic<uint64_t> allowed{0};
     const int rc = allow_smem(kernel, kSmem, allowed);
     if (rc) return rc;
+    p.stall = faults_injected() ? injected_stall(kMode) : 0;
+    p.wait_ns = p.stall ? kWaitNs / 40 : kWaitNs;
     const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / kCta)) * kCta;
     return check_cuda(launch_after(kernel, grid, kProductThreads, kSmem, kCta, s, a, b, p), "product launch");
