@@ -25,6 +25,13 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _keep_for(stream, tensors) -> None:
+    """The tensors' memory is not given away before `stream` (None: the current one, nothing to do) is done with it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _u16_empty(n: int, device, fill: int | None = None) -> torch.Tensor:
     """A uint16 buffer held as int16 storage (bit pattern only)."""
     t = torch.empty(n, dtype=torch.int16, device=device)
@@ -480,7 +487,9 @@ class AdamWGroup(_Group):
     """AdamW state for a list of bf16 weights: moments in 8 bits with a scale for each 256 elements
     (states="u8"; tensors of up to 4096 elements keep fp32) or in fp32 (states="fp32").  The moments of all
     tensors are views of two allocations, `flat_m` and `flat_v`; fp32 ones lie as unpack_states lays
-    them out.  With `offload` (an OffloadEngine) residuals and moments live in pinned host memory."""
+    them out.  With `offload` (an OffloadEngine) residuals and moments live in pinned host memory.
+    A call's `stream` (default: the current one) takes all that the call makes and runs; the caller has ordered it
+    after the call's inputs, whose memory is kept for it until it is done with them."""
 
     def __init__(self, weights: Sequence[torch.Tensor], residuals: Sequence[torch.Tensor] | None = None,
                  kahan: bool = True, states: str = "u8", offload: OffloadEngine | None = None):
@@ -518,12 +527,12 @@ class AdamWGroup(_Group):
     @classmethod
     def from_masters(cls, masters: Sequence[torch.Tensor], stream=None, states: str = "u8",
                      offload: OffloadEngine | None = None):
-        ws, rs = [], []
-        for x in masters:
-            hi, lo = kahan_split(x.contiguous(), stream=stream)
-            ws.append(hi)
-            rs.append(lo)
-        return cls(ws, rs, states=states, offload=offload)
+        masters = list(masters)
+        with torch.cuda.stream(stream):            # None: the current stream
+            ws, rs = zip(*(kahan_split(x.contiguous()) for x in masters))
+            group = cls(ws, rs, states=states, offload=offload)
+        _keep_for(stream, masters)
+        return group
 
     def attach_host(self):
         super().attach_host()
@@ -539,6 +548,7 @@ class AdamWGroup(_Group):
         lmopt.optim_step_adamw(self.handle, self._grad_ptrs(grads), self.step_count + 1, h,
                                None if grad_scale is None else grad_scale.data_ptr(), _stream_ptr(stream))
         self.step_count += 1
+        _keep_for(stream, grads if grad_scale is None else [*grads, grad_scale])
 
     def set_step(self, step: int):
         """Sets the counter of completed steps (resuming from a checkpoint)."""
@@ -551,11 +561,16 @@ class AdamWGroup(_Group):
 
     def unpack_states(self, m: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
         """The moments as fp32, in two flat buffers (allocated zeroed if not given)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                out = self.unpack_states(m, v)
+            _keep_for(stream, out)
+            return out
         m, v = (torch.zeros(self._unpacked, dtype=torch.float32, device=self.weights[0].device) if x is None else x
                 for x in (m, v))
         for x in (m, v):
             assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.numel() >= self._unpacked
-        lmopt.optim_group_unpack_state(self.handle, m.data_ptr(), v.data_ptr(), _stream_ptr(stream))
+        lmopt.optim_group_unpack_state(self.handle, m.data_ptr(), v.data_ptr(), _stream_ptr(None))
         return m, v
 
     def masters(self):
