@@ -177,8 +177,13 @@ def check(rc: int) -> int:
 
 
 def _ptr_array(ptrs):
-    """The addresses (None: 0) as a C array of pointers."""
-    return (ctypes.c_void_p * max(1, len(ptrs))).from_buffer(array.array("Q", [p or 0 for p in ptrs] or [0]))
+    """The addresses (None: 0) as a C array of pointers: ints in one go, anything else that ctypes takes for a
+    pointer one by one."""
+    kind = ctypes.c_void_p * max(1, len(ptrs))
+    try:
+        return kind.from_buffer(array.array("Q", [p or 0 for p in ptrs] or [0]))
+    except (TypeError, OverflowError):
+        return kind(*ptrs)
 
 
 # ------------------------------------------------------------------ raw entry points (same names)
