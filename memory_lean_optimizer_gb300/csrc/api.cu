@@ -258,7 +258,8 @@ int optim_group_create(const optim_tensor_desc_t* tensors, int32_t n, int32_t ki
             r.slot64 = (int32_t)slot64;
             slot64 += (d.numel + 63) / 64;
         }
-        if (slot64 > INT32_MAX) rc = set_error(OPTIM_EINVAL, "group too large");
+        if ((kind == OPTIM_KIND_ADAMW || kind == OPTIM_KIND_ADAMW_U8) && slot64 > INT32_MAX)   // nothing else reads slot64
+            rc = set_error(OPTIM_EINVAL, "group too large");
         if (kind != OPTIM_KIND_FACTORED) {
             // chunks of kChunkU16 elements for NAdam u16 groups, kChunk for f24 and Adan groups;
             // a group whose chunks would not give every SM a CTA (two for the
