@@ -82,9 +82,12 @@ struct ProductArgs {
 // One copying thread's blocks after the second (of the pair's first or second CTA), or the accumulators.
 enum Stall { kStallCopy = 1, kStallPeer = 2, kStallFree = 3 };
 
-__device__ __forceinline__ float exp2_approx(float x) {
+// e^x for the softmax: the argument is a difference taken before the change of base.  (Subtracting base log2 e
+// from x log2 e in one multiply-add saves an instruction, but rounds base log2 e: an error of the exponent
+// that grows with the logits and overflows it past 2^40.)
+__device__ __forceinline__ float exp_of(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
     return y;
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     if (j >= left) x[j] = -INFINITY;
                     top = fmaxf(top, x[j]);
                 }
-                const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+                const float base = top == -INFINITY ? 0.0f : top;
                 if (t >= 0 && t < 128) {
                     float l = 0.0f;
 #pragma unroll
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     p.target_logit[row] = l;
                 }
 #pragma unroll
-                for (int j = 0; j < 128; ++j) sum += exp2_approx(fmaf(x[j], kLog2e, -base));
+                for (int j = 0; j < 128; ++j) sum += exp_of(x[j] - base);
                 if (row < rows) p.part[(int64_t)((p.v_off + c0) / 128) * p.rows_pad + row] = make_float2(top, ok ? sum : kNan);
                 __syncwarp();
                 continue;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                 const bool live = row < rows;
                 const int t = live ? p.target[row] - p.v_off - c0 : -1;     // the target's column of this half
                 const float g = live ? (ok ? p.scale[row] : kNan) : 0.0f;
-                const float base = live ? p.lse[row] * kLog2e : 0.0f;
+                const float base = live ? p.lse[row] : 0.0f;
                 uint16_t* const out = p.e + row * p.lde + c0;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 32) {
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
                     const int left = p.vocab - (p.v_off + c0 + c);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float x = exp2_approx(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                        float x = exp_of(__uint_as_float(r[j]) - base);
                         if (t == c + j) x -= 1.0f;
                         // rows past the last and columns past the vocabulary are zero, whatever was multiplied
                         r[j] = __float_as_uint(live && j < left ? x * g : 0.0f);
