@@ -105,7 +105,7 @@ enum {
  * one fp32 constant q for each block of OPTIM_U8_BLOCK consecutive elements (the last may be
  * short).  m = t |t| with t = (code - 128) q, v = (code q)^4, q = sqrt(max |m|) / 127 and
  * max(v)^(1/4) / 255 over the block: the companding of the u16 codes, with a scale per block.
- * 12.06 bytes per element per step instead of 26 (weight, residual and gradient included).  Buffers
+ * 14.06 bytes per element per step instead of 26 (weight, residual and gradient included).  Buffers
  * are 4-byte aligned and start as zero bytes (which decode to zero). */
 #define OPTIM_U8_BLOCK 256
 /* ADAN groups: m -> fp32 [3*P] (planes m, v, n, each P = numel rounded up to a multiple of 4
