@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_long(const TX* __restrict_
 
 constexpr int kMostSmem = 96 * 1024;   // 512 threads with 32 bf16 or 16 fp32 values each
 
-// Partial rows of the weight's gradient at most: 4 CTAs on each of 152 SMs.
+// Partial rows of the weight's gradient at most: 4 CTAs on each of 152 SMs (fixed, because the workspace call answers
+// without a device).
 constexpr int kMaxSlices = 608;
 
 unsigned row_grid(int64_t rows) { return (unsigned)std::min<int64_t>(rows, (int64_t)sm_count() * 8); }

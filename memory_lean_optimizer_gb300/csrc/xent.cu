@@ -14,12 +14,17 @@
 //   kHidden E W     -> dH, summed in fp32 over the pieces
 //   kWeight E^T H   -> dW of the piece, finished
 // E is the one rounding to fewer bits before an output: its entries meet bf16 operands in the tensor
-// cores, which want both operands of one type.
+// cores, which want both operands of one type.  The gradients are then 2.0e-3 (2-norm) from 64 bits, where
+// their own rounding to bf16 alone leaves 1.65e-3.
 //
-// Many rows: the tensor cores bound it.  4096 rows x 2048 x 32768 words take 0.29 ms forward and 0.89 ms
-// backward, a product 0.27-0.30 ms or 1.8-2.0 PFLOP/s; 8192 x 4096 x 131072 4.6 and 15.4 ms, the power
-// limit's rate.  Few rows: the weight's bytes.  16 x 4096 x 131072 (1.07 GB) takes 182 us forward (5.9 TB/s)
-// and 570 us backward, where it is read twice and written once.
+// Many rows: the tensor cores bound it, and their power limit once a sequence lasts.  4096 rows x 2048 x 32768
+// words take 0.29 ms forward and 0.88 ms backward in bursts of 30 calls (a product 0.27-0.30 ms or 1.8-2.0
+// PFLOP/s), 0.32 and 0.99 ms over two seconds; 8192 x 4096 x 131072 4.5 and 13.7 ms in bursts of four, 5.0 and
+// 15.3 over two seconds.  Few rows: the weight's bytes.  16 x 4096 x 131072 (1.07 GB) takes 177 us forward
+// (6.1 TB/s) and 563 us backward, where it is read twice and written once.
+// Rows left out save the products of three roles in proportion; dH's tiles and the split of its K are laid out
+// for all rows.  4096 x 2048 x 32768 with nine rows in ten ignored: 59 us forward, 268 backward; the 410 rows
+// given alone: 55 and 171.
 #include <algorithm>
 #include <cstdio>
 
@@ -32,8 +37,11 @@ namespace {
 
 constexpr int kTileN = 256;       // accumulator columns
 constexpr int kTileK = 64;        // one 128-byte swizzle row of bf16
-// kStats: blocks of K to an accumulator, 1024 products (see k_product).  2048 x 4096 x 32768: 300 us and a
-// relative error of lse of 8.4e-8; 512 products 310 us and 4.8e-8, all 4096 298 us and 3.5e-7 (plain fp32: 2.9e-7).
+// kStats: blocks of K to an accumulator, 1024 products (see k_product).  2048 x 4096 x 32768: 299 us and a relative
+// error of lse of 5.4e-7 (2-norm, hidden states that lean towards their targets' rows); 512 products 308 us and
+// 2.6e-7, all 4096 298 us and 2.2e-6; elementary fp32 operations 4.0e-7.  Between 0.9 and 2.3 times as far off as
+// those (300 x 1290 x 5000: 6.4e-7 against 2.8e-7); 512 products would stay within 1.25 times, for 2-8 % of the
+// forward call and 0-1 % of both.
 constexpr int kChunk = 16;
 constexpr int kProductThreads = 384;   // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory, warps 4-11 finish
 // Stages of 48 KiB (one CTA: 128 rows of A, 256 of B) or 32 KiB (a pair: 128 and 128 each).
@@ -142,7 +150,7 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 // Roles by warp: TMA into a ring of stages; tcgen05.mma from them into one of two accumulators;
 // eight warps -- a warp per 32 rows and half of the columns -- take the other accumulator out.
 // The tensor cores cut the accumulator's low bits at each addition, always towards zero: over a
-// long K that is a drift, ten times the error of rounded fp32 sums at K = 4096, which the loss
+// long K that is a drift (products of one sign, K = 4096: lse 1.2e-5 low, 1.8e-6 as it is), which the loss
 // would show.  kStats therefore starts a new accumulator every kChunk blocks of K and adds them up
 // in registers, rounded to nearest; the other accumulator hides the extra reading of tensor memory.
 // Every wait is bounded (mbar_wait); one that runs out raises gave_up in all CTAs of the cluster and each role
@@ -797,7 +805,7 @@ struct XentPlan {
 
 // How much of the vocabulary's gradient exists at a time (bytes of E, of a copied piece of the weight).  Each
 // piece costs three launches with their ramps; backward with 64, 128, 256, 512 MiB: 4096 x 2048 x 32768 894, 871,
-// 870, 870 us, 8192 x 4096 x 131072 16.9, 16.0, 15.4, 15.1 ms.
+// 870, 870 us in bursts, 8192 x 4096 x 131072 16.9, 16.0, 15.4, 15.1 ms under the power limit.
 constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int64_t kPieceMin = 8192;
 
@@ -817,7 +825,8 @@ XentPlan plan_xent(int64_t rows, int64_t dim, int64_t vocab, const void* weight,
     if (p.pack_w) piece = std::min(piece, std::max(kPieceMin, kPieceBytes / (2 * p.ldh) / kTileN * kTileN));
     p.piece = piece;
     p.ldacc = up(dim, 32);
-    // few rows leave dH few tiles: K (the piece) is split until the tiles fill the GPU, 512 columns at least
+    // few rows leave dH few tiles: K (the piece) is split until the tiles fill the GPU (152 SMs; not asked of the
+    // device, because the workspace call answers without one), 512 columns at least
     // (backward of 16 x 4096 x 131072 675 us, 1184 unsplit; 200 x 1024 x 32768 82, 196; 1024 x 2048 x 32768 253, 302)
     const int64_t tiles = p.rows_pad / (128 * p.cta) * ((dim + kTileN - 1) / kTileN);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({152 / p.cta / tiles, p.piece / 512, 64}));

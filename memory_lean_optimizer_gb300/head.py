@@ -3,9 +3,10 @@ cross entropy over the vocabulary, taken straight from the hidden states so that
 never kept.  With ``engine.AdamWGroup`` (or ``hooks.attach_fused_adamw``) they are the memory-lean
 tail of a training step: hidden states -> norm -> loss -> gradients -> optimizer.
 
-The ``*_forward`` / ``*_backward`` functions are the library calls on tensors; ``layer_norm`` and
-``linear_cross_entropy`` are the same with autograd.  Each takes ``stream`` (a torch stream the caller has ordered after its inputs;
-default: the current one).  PyTorch supplies device memory, streams and the graph.
+The ``*_forward`` / ``*_backward`` functions are the library calls on tensors; each takes ``stream`` (a torch
+stream the caller has ordered after its inputs; default: the current one).  ``layer_norm``,
+``linear_cross_entropy`` and ``LMTail`` are the same with autograd and run on the current stream.  PyTorch supplies
+device memory, streams and the graph.
 """
 from __future__ import annotations
 

@@ -121,7 +121,8 @@ def attach_fused_nadam(params: Sequence[torch.nn.Parameter], n_groups: int, hp: 
 
 def attach_fused_adamw(params: Sequence[torch.nn.Parameter], n_groups: int, hp: dict, on_step=None,
                        states: str = "u8", offload: bool = False) -> FusedStepper:
-    """The same with AdamW groups (engine.AdamWGroup, moments in 8 bits or fp32)."""
+    """The same with AdamW groups (engine.AdamWGroup, moments in 8 bits or fp32).  The hooks step without a
+    grad_scale; AdamWGroup.step takes one."""
     from .engine import AdamWGroup
 
     def make(ps):
