@@ -329,7 +329,8 @@ int optim_step_adamw(optim_group_t* group, const void* const* grads_bf16, int64_
 /* The moments of an ADAMW or ADAMW_U8 group as fp32 values, for checkpoints of another format and for
  * inspection: tensor i starts at element sum over j < i of numel_j rounded up to 64 of each flat
  * DEVICE buffer (4-byte aligned; 16-byte aligned buffers take 128-bit stores); the gaps are not
- * written.  One enqueued kernel.  OPTIM_ESTATE for offloaded groups. */
+ * written.  One enqueued kernel; a group of empty tensors writes nothing and takes NULL.
+ * OPTIM_ESTATE for offloaded groups. */
 int optim_group_unpack_state(optim_group_t* group, float* m, float* v, void* stream);
 
 /* Encodes n fp32 moments into u16 codes with the engine's codec.  scale (device, 1 float) is

@@ -571,7 +571,7 @@ int optim_step_adamw(optim_group_t* g, const void* const* grads, int64_t step, c
 }
 
 int optim_group_unpack_state(optim_group_t* g, float* m, float* v, void* stream) {
-    if (!g || !m || !v) return set_error(OPTIM_EINVAL, "group or output is NULL");
+    if (!g || (g->n_chunks_total > 0 && (!m || !v))) return set_error(OPTIM_EINVAL, "group or output is NULL");
     if (g->kind != OPTIM_KIND_ADAMW && g->kind != OPTIM_KIND_ADAMW_U8)
         return set_error(OPTIM_EINVAL, "not an ADAMW group");
     if (g->offload) return set_error(OPTIM_ESTATE, "the group's states are offloaded");
