@@ -484,6 +484,41 @@ int loss_xent_backward(const void* hidden, int64_t ldh, const void* weight, int6
                        int64_t lddh, void* d_weight, int64_t lddw, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* ---- inside a transformer block's training step -----------------------------------------------
+ * Plain buffers, no handle; strides are in elements.  Nothing is kept from one call to the next. */
+
+/* Rotary positions of `rows` tokens' queries and keys (one launch; a side with 0 heads takes NULL): the first
+ * `rotary` elements of every head are pairs (a, b) -- elements j and j + rotary/2, or 2j and 2j + 1 if
+ * interleaved -- which become ((a cos t - b sin t) factor, (b cos t + a sin t) factor); the rest is copied.  t =
+ * 2 pi turns[j] 2^-64 positions[row]; the product is an integer one, so that angles are exact for every
+ * position (any int64).  inverse: -t (the gradient of the call).  Token and head strides; outputs may be the
+ * inputs themselves (same strides), and overlap with nothing else.  type: of all four, OPTIM_BF16 or
+ * OPTIM_F32; arithmetic is fp32, outputs rounded once.  dim <= 1024, rotary even. */
+int rope_apply(const void* q, int64_t q_row, int64_t q_head, void* q_out, int64_t qo_row, int64_t qo_head, int64_t q_heads,
+               const void* k, int64_t k_row, int64_t k_head, void* k_out, int64_t ko_row, int64_t ko_head, int64_t k_heads,
+               const int64_t* positions, const uint64_t* turns, int64_t rows, int64_t dim, int64_t rotary, float factor,
+               int32_t interleaved, int32_t inverse, int32_t type, void* stream);
+
+/* Activations in 8 bits: every 32 elements of a row (the last block may be shorter) keep codes c of
+ * -127..127 and one exponent byte E, x = c 2^(E - 133).  E is the smallest with which no element of the block
+ * rounds past 127 (at most 254: magnitudes from 127.5 2^121 on take the code 127), codes are rounded to nearest even.
+ * E = 255: the block holds an infinity or a NaN and reads as NaN.  codes: 16-byte aligned, ldc a multiple of 32 (the
+ * last block is filled up with zeros); exponents: lde bytes from row to row.  x is bf16 or fp32
+ * (type), rows ldx elements apart.  One enqueued kernel. */
+int act_pack_i8(const void* x, int64_t ldx, int8_t* codes, int64_t ldc, uint8_t* exponents, int64_t lde, int64_t rows,
+                int64_t cols, int32_t type, void* stream);
+int act_unpack_i8(const int8_t* codes, int64_t ldc, const uint8_t* exponents, int64_t lde, void* x, int64_t ldx, int64_t rows,
+                  int64_t cols, int32_t type, void* stream);
+
+/* The gated activation h = g s(g) u, s(g) = 1 / (1 + e^-g), of rows that hold g (cols elements) and then u.
+ * codes, exponents (both or neither NULL): g and u of row r in the form above, as rows 2r and 2r + 1. */
+int act_swiglu_forward(const void* gate_up, int64_t ldg, void* h, int64_t ldh, int8_t* codes, int64_t ldc, uint8_t* exponents,
+                       int64_t lde, int64_t rows, int64_t cols, int32_t type, void* stream);
+/* Its gradients at the g and u that the codes stand for: d_gate_up (dg, then du) with dg = dh u s(g) (1 + g (1 - s(g))) and
+ * du = dh g s(g), and h of those g and u (NULL: not wanted). */
+int act_swiglu_backward(const void* dh, int64_t lddh, const int8_t* codes, int64_t ldc, const uint8_t* exponents, int64_t lde,
+                        void* d_gate_up, int64_t ldg, void* h, int64_t ldh, int64_t rows, int64_t cols, int32_t type, void* stream);
+
 const char* optim_last_error(void);
 
 #ifdef __cplusplus

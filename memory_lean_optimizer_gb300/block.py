@@ -1,0 +1,305 @@
+"""The inside of a transformer block's training step over liblmopt.so: rotary positions, and activations kept in 8
+bits between the forward and the backward pass, alone and in the gated activation that reads
+them.  With ``head`` (norm, loss) and the optimizer groups they are a memory-lean training step.
+
+The ``*_forward`` / ``*_backward`` functions and ``pack_activation`` / ``unpack_activation`` are the library calls on
+tensors; each takes ``stream`` (a torch stream the caller has ordered after its inputs; default: the
+current one).  ``rotary``, ``swiglu``, ``gated_mlp`` are the same with autograd and run on
+the current stream.  PyTorch supplies device memory, streams, the graph and plain matrix products.
+"""
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+from fractions import Fraction
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import lmopt
+from .engine import _stream_ptr
+from .head import _on_stream, _rows, _type
+
+ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.h, act_pack_i8)
+
+
+def _on_gpu(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU")
+
+
+def _heads(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t [tokens, heads, dim] with the elements of a head next to each other: t itself, or a copy."""
+    _on_gpu(t, name)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
+    return t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
+
+
+# ---------------------------------------------------------------------------------- rotary positions
+_PI = Fraction(3141592653589793238462643383279502884197169399375105820974944592307816406286208998, 10 ** 81)
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original_length: int | None = None) -> tuple[list[float], float]:
+    """Radians per position of each pair, base^(-2j/rotary_dim) scaled for `factor` times the length, and the factor on
+    the rotated elements.
+    scaling: None; "linear": positions divided by factor; "ntk": the base times factor^(d/(d-2)); "yarn": pairs
+    that turn fewer than once in original_length are divided by factor, those that turn more than 32 times
+    kept, in between in proportion, and the rotated elements times 0.1 ln(factor) + 1."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even, not {rotary_dim}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (base > 0 and math.isfinite(base)) or not (factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive")
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = [base ** (-2.0 * j / rotary_dim) for j in range(rotary_dim // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    if scaling == "yarn":
+        if not original_length or original_length < 1:
+            raise ValueError("yarn scaling needs original_length")
+        keep = [min(max((original_length * f / (2 * math.pi) - 1.0) / 31.0, 0.0), 1.0) for f in freq]
+        return [f * g + f / factor * (1.0 - g) for f, g in zip(freq, keep)], 1.0 + 0.1 * math.log(factor)
+    return freq, 1.0
+
+
+class RotaryPlan:
+    """What rotary positions need of a model: the pairs' layout and their frequencies, on the device as turns per
+    position in 64-bit fixed point.  Arguments as rotary_frequencies; interleaved: pairs are neighbours
+    (2j, 2j + 1), not half the rotated part apart.  `rotary_dim` may be less than a head: the rest is kept."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+                 factor: float = 1.0, original_length: int | None = None, device="cuda"):
+        freq, self.factor = rotary_frequencies(rotary_dim, base, scaling, factor, original_length)
+        self.rotary_dim, self.interleaved = rotary_dim, interleaved
+        turns = [round(Fraction(f) / (2 * _PI) * 2 ** 64) % 2 ** 64 for f in freq]
+        self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device=device)
+
+
+def _rope(q, k, positions, plan, inverse, names):
+    q, k = _heads(q, names[0]), _heads(k, names[1])
+    rows, _, dim = q.shape
+    if k.shape[0] != rows or k.shape[2] != dim or k.dtype != q.dtype:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same tokens, head size and type")
+    dtype = _type(q, names[0])
+    if plan.rotary_dim > dim:
+        raise ValueError(f"{plan.rotary_dim} rotated elements in heads of {dim}")
+    if positions.dtype != torch.int64 or positions.shape != (rows,) or positions.get_device() != q.get_device():
+        raise ValueError(f"positions must be int64 [{rows}] on {q.device}")
+    if plan.turns.get_device() != q.get_device():
+        raise ValueError("the plan is on another device")
+    if not positions.is_contiguous():
+        positions = positions.contiguous()
+    out, sides = [], []
+    for t in (q, k):
+        o = t.new_empty(t.shape)
+        out.append(o)
+        heads = t.shape[1]
+        sides.append((t.data_ptr(), t.stride(0), t.stride(1), o.data_ptr(), heads * dim, dim, heads))
+    lmopt.rope_apply(*sides, positions.data_ptr(), plan.turns.data_ptr(), rows, dim, plan.rotary_dim, plan.factor,
+                     plan.interleaved, inverse, dtype, _stream_ptr(None))
+    return out[0], out[1]
+
+
+@_on_stream
+def rotary_forward(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan):
+    """(q, k) turned by their tokens' positions.  q [tokens, heads, dim], k [tokens, kv_heads, dim] (bf16 or fp32, any strides;
+    kv_heads may be 0), positions int64 [tokens], of any size.  New tensors."""
+    return _rope(q, k, positions, plan, False, ("q", "k"))
+
+
+@_on_stream
+def rotary_backward(dq: torch.Tensor, dk: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan):
+    """Gradients of rotary_forward's inputs from those of its outputs."""
+    return _rope(dq, dk, positions, plan, True, ("dq", "dk"))
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, plan):
+        ctx.save_for_backward(positions)
+        ctx.plan = plan
+        return rotary_forward(q, k, positions, plan)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        return *rotary_backward(dq, dk, ctx.saved_tensors[0], ctx.plan), None, None
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan):
+    """rotary_forward with autograd."""
+    return _Rotary.apply(q, k, positions, plan)
+
+
+# ------------------------------------------------------------------------- activations kept in 8 bits
+@dataclass(frozen=True)
+class PackedActivation:
+    """An activation in 8 bits: int8 codes of rows of its last dimension, a uint8 exponent per 32 of them (the last block of a
+    row is filled up with zeros), value = code * 2^(exponent - 133); the shape and type it was packed from."""
+    codes: torch.Tensor
+    exponents: torch.Tensor
+    shape: torch.Size
+    dtype: torch.dtype
+
+    def __post_init__(self):
+        cols = self.shape[-1]
+        rows = math.prod(self.shape[:-1])
+        blocks = -(-cols // ACT_BLOCK)
+        if (self.codes.dtype != torch.int8 or self.codes.shape != (rows, blocks * ACT_BLOCK) or not self.codes.is_contiguous() or
+                self.exponents.dtype != torch.uint8 or self.exponents.shape != (rows, blocks) or not self.exponents.is_contiguous()):
+            raise ValueError(f"codes and exponents do not fit {list(self.shape)}")
+
+
+def _new_codes(t: torch.Tensor, rows: int, cols: int):
+    blocks = -(-cols // ACT_BLOCK)
+    return t.new_empty((rows, blocks * ACT_BLOCK), dtype=torch.int8), t.new_empty((rows, blocks), dtype=torch.uint8)
+
+
+@_on_stream
+def pack_activation(x: torch.Tensor) -> PackedActivation:
+    """x (bf16 or fp32) in 8 bits: off by at most half a step, 2^-7 of the largest magnitude among its block of 32
+    elements of the last dimension.  A block with an infinity or a NaN comes back as NaN."""
+    dtype = _type(x, "x")
+    m = _rows(x, "x")
+    rows, cols = m.shape
+    if cols == 0:
+        raise ValueError("x needs at least one element in a row")
+    codes, exponents = _new_codes(m, rows, cols)
+    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), codes.data_ptr(), codes.shape[1], exponents.data_ptr(), exponents.shape[1],
+                      rows, cols, dtype, _stream_ptr(None))
+    return PackedActivation(codes, exponents, x.shape, x.dtype)
+
+
+def _packed(p: PackedActivation, name: str) -> None:
+    _on_gpu(p.codes, name)
+    _on_gpu(p.exponents, name)
+
+
+def _unpack(p: PackedActivation) -> torch.Tensor:
+    _packed(p, "the packed activation")
+    x = p.codes.new_empty(p.shape, dtype=p.dtype)
+    rows, cols = p.codes.shape[0], p.shape[-1]
+    lmopt.act_unpack_i8(p.codes.data_ptr(), p.codes.shape[1], p.exponents.data_ptr(), p.exponents.shape[1], x.data_ptr(), cols,
+                        rows, cols, _type(x, "x"), _stream_ptr(None))
+    return x
+
+
+def _on_stream_packed(fn, *args, packed: PackedActivation, stream, **kw):
+    """fn with the packed activation's tensors kept for `stream`."""
+    if stream is None:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        out = fn(*args, **kw)
+    for t in (packed.codes, packed.exponents, *args, *kw.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return out
+
+
+def unpack_activation(p: PackedActivation, stream=None) -> torch.Tensor:
+    """The values that a packed activation stands for, in its shape and type."""
+    return _on_stream_packed(_unpack, p, packed=p, stream=stream)
+
+
+@_on_stream
+def swiglu_forward(gate_up: torch.Tensor, keep: bool = True):
+    """(h, packed): h = g sigmoid(g) u of gate_up [..., 2 n], g its first and u its last n elements, and both in 8
+    bits ([..., 2, n]; None if keep is false) for swiglu_backward."""
+    dtype = _type(gate_up, "gate_up")
+    m = _rows(gate_up, "gate_up")
+    rows, cols = m.shape[0], m.shape[1] // 2
+    if m.shape[1] != 2 * cols or cols == 0:
+        raise ValueError(f"gate_up's last dimension must be even and not 0, not {m.shape[1]}")
+    h = m.new_empty((*gate_up.shape[:-1], cols))
+    packed = None
+    if keep:
+        codes, exponents = _new_codes(m, 2 * rows, cols)
+        packed = PackedActivation(codes, exponents, torch.Size((*gate_up.shape[:-1], 2, cols)), gate_up.dtype)
+        lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, codes.data_ptr(), codes.shape[1],
+                                 exponents.data_ptr(), exponents.shape[1], rows, cols, dtype, _stream_ptr(None))
+    else:
+        lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, None, 0, None, 0, rows, cols, dtype,
+                                 _stream_ptr(None))
+    return h, packed
+
+
+def _swiglu_backward(dh, packed, need_h):
+    _packed(packed, "the packed activation")
+    *lead, two, cols = packed.shape
+    if two != 2 or dh.shape != (*lead, cols) or dh.dtype != packed.dtype:
+        raise ValueError(f"dh must be {packed.dtype} {[*lead, cols]} for a packed {list(packed.shape)}")
+    d = _rows(dh, "dh")
+    rows = d.shape[0]
+    d_gate_up = d.new_empty((*lead, 2 * cols))
+    h = d.new_empty((*lead, cols)) if need_h else None
+    lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), packed.codes.data_ptr(), packed.codes.shape[1],
+                              packed.exponents.data_ptr(), packed.exponents.shape[1], d_gate_up.data_ptr(), 2 * cols,
+                              None if h is None else h.data_ptr(), cols, rows, cols, _type(d, "dh"), _stream_ptr(None))
+    return d_gate_up, h
+
+
+def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = False, stream=None):
+    """(d_gate_up, h) from the gradient of h and what swiglu_forward kept: the gradients at the gate and up values that
+    the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
+    return _on_stream_packed(_swiglu_backward, dh, packed, need_h, packed=packed, stream=stream)
+
+
+class _SwiGLU(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate_up):
+        h, packed = swiglu_forward(gate_up)
+        ctx.save_for_backward(packed.codes, packed.exponents)
+        ctx.kept = packed.shape, packed.dtype
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        return swiglu_backward(dh, PackedActivation(*ctx.saved_tensors, *ctx.kept))[0]
+
+
+def swiglu(gate_up: torch.Tensor) -> torch.Tensor:
+    """g sigmoid(g) u with autograd; for the backward pass g and u are kept in 8 bits."""
+    if torch.is_grad_enabled() and gate_up.requires_grad:
+        return _SwiGLU.apply(gate_up)
+    return swiglu_forward(gate_up, keep=False)[0]
+
+
+class _GatedMLP(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_in, w_out):
+        h, kept = swiglu_forward(torch.nn.functional.linear(x, w_in))
+        x8 = pack_activation(x) if ctx.needs_input_grad[1] else None
+        ctx.save_for_backward(w_in, w_out, kept.codes, kept.exponents, *((x8.codes, x8.exponents) if x8 else ()))
+        ctx.kept, ctx.x = (kept.shape, kept.dtype), (x.shape, x.dtype)
+        return torch.nn.functional.linear(h, w_out)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        w_in, w_out, codes, exponents, *x8 = ctx.saved_tensors
+        need_x, need_in, need_out = ctx.needs_input_grad
+        d_gate_up, h = swiglu_backward(dy @ w_out, PackedActivation(codes, exponents, *ctx.kept), need_h=need_out)
+        dx = d_in = d_out = None
+        if need_out:
+            d_out = dy.flatten(0, -2).t() @ h.flatten(0, -2)
+            del h
+        if need_in:
+            d_in = d_gate_up.flatten(0, -2).t() @ unpack_activation(PackedActivation(*x8, *ctx.x)).flatten(0, -2)
+        if need_x:
+            dx = d_gate_up @ w_in
+        return dx, d_in, d_out
+
+
+def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch.Tensor:
+    """swiglu(x w_in^T) w_out^T with autograd, w_in [2 n, dim], w_out [dim, n].  What is kept for the backward pass is x and
+    the gate and up values in 8 bits (x for w_in's gradient; gate and up for everything else: h is formed again)."""
+    if x.dim() < 2 or w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or x.shape[-1] != w_in.shape[1]:
+        raise ValueError(f"x {list(x.shape)}, w_in {list(w_in.shape)} and w_out {list(w_out.shape)} do not fit")
+    if not torch.is_grad_enabled():
+        return torch.nn.functional.linear(swiglu_forward(torch.nn.functional.linear(x, w_in), keep=False)[0], w_out)
+    return _GatedMLP.apply(x, w_in, w_out)

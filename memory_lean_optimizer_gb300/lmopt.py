@@ -52,6 +52,7 @@ EXPORTED = (
     "optim_prodigy_finish", "optim_step_adamw", "optim_group_unpack_state",
     "norm_layer_forward", "norm_layer_backward", "norm_layer_workspace",
     "loss_xent_forward", "loss_xent_backward", "loss_xent_workspace",
+    "rope_apply", "act_pack_i8", "act_unpack_i8", "act_swiglu_forward", "act_swiglu_backward",
 )
 
 
@@ -123,6 +124,11 @@ def load(path: str = LIB_PATH):
             "norm_layer_forward": [P, I64, P, P, P, I64, P, P, I64, I64, F, I32, I32, P],
             "norm_layer_workspace": [I64, I64, ctypes.POINTER(ctypes.c_size_t)],
             "norm_layer_backward": [P, I64, P, I64, P, P, P, P, I64, P, P, I64, I64, I32, I32, P, ctypes.c_size_t, P],
+            "rope_apply": [*[P, I64, I64, P, I64, I64, I64] * 2, P, P, I64, I64, I64, F, I32, I32, I32, P],
+            "act_pack_i8": [P, I64, P, I64, P, I64, I64, I64, I32, P],
+            "act_unpack_i8": [P, I64, P, I64, P, I64, I64, I64, I32, P],
+            "act_swiglu_forward": [P, I64, P, I64, P, I64, P, I64, I64, I64, I32, P],
+            "act_swiglu_backward": [P, I64, P, I64, P, I64, P, I64, P, I64, I64, I64, I32, P],
             "loss_xent_workspace": [I64, I64, I64, P, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
             "loss_xent_forward": [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, ctypes.c_size_t, P],
             "loss_xent_backward": [P, I64, P, I64, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, ctypes.c_size_t, P],
@@ -423,3 +429,30 @@ def loss_xent_backward(hidden: int, ldh: int, weight: int, ldw: int, target: int
                        d_weight: int | None, lddw: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
     check(load().loss_xent_backward(hidden, ldh, weight, ldw, target, lse, grad_loss, rows, dim, vocab, ignore_index,
                                     d_hidden, lddh, d_weight, lddw, workspace, workspace_bytes, stream))
+
+
+# ------------------------------------------------------------- inside a transformer block (plain buffers)
+def rope_apply(q, k, positions: int | None, turns: int | None, rows: int, dim: int, rotary: int, factor: float,
+               interleaved: bool, inverse: bool, dtype: int, stream: int = 0) -> None:
+    """q, k: (pointer, row stride, head stride, output pointer, its row stride, its head stride, heads)."""
+    check(load().rope_apply(*q, *k, positions, turns, rows, dim, rotary, factor, int(interleaved), int(inverse), dtype, stream))
+
+
+def act_pack_i8(x: int, ldx: int, codes: int, ldc: int, exponents: int, lde: int, rows: int, cols: int, dtype: int,
+                stream: int = 0) -> None:
+    check(load().act_pack_i8(x, ldx, codes, ldc, exponents, lde, rows, cols, dtype, stream))
+
+
+def act_unpack_i8(codes: int, ldc: int, exponents: int, lde: int, x: int, ldx: int, rows: int, cols: int, dtype: int,
+                  stream: int = 0) -> None:
+    check(load().act_unpack_i8(codes, ldc, exponents, lde, x, ldx, rows, cols, dtype, stream))
+
+
+def act_swiglu_forward(gate_up: int, ldg: int, h: int, ldh: int, codes: int | None, ldc: int, exponents: int | None, lde: int,
+                       rows: int, cols: int, dtype: int, stream: int = 0) -> None:
+    check(load().act_swiglu_forward(gate_up, ldg, h, ldh, codes, ldc, exponents, lde, rows, cols, dtype, stream))
+
+
+def act_swiglu_backward(dh: int, lddh: int, codes: int, ldc: int, exponents: int, lde: int, d_gate_up: int, ldg: int,
+                        h: int | None, ldh: int, rows: int, cols: int, dtype: int, stream: int = 0) -> None:
+    check(load().act_swiglu_backward(dh, lddh, codes, ldc, exponents, lde, d_gate_up, ldg, h, ldh, rows, cols, dtype, stream))
