@@ -30,7 +30,7 @@
  *    GPU is disturbed).  =stall_<stats|grad|hidden|weight>_<copy|peer|free> lets the bounded waits
  *    inside that product kernel of the cross entropy run out after a tenth of a second: its first
  *    cluster stops copying (one of its CTAs) or keeps its accumulators, and every wait behind that
- *    ends by its limit.
+ *    ends by its limit; =stall_attention[_dq|_dkv]_<copy|softmax> does so in the first CTA of an attention kernel.
  */
 #ifndef LMOPT_H
 #define LMOPT_H
@@ -518,6 +518,31 @@ int act_swiglu_forward(const void* gate_up, int64_t ldg, void* h, int64_t ldh, i
  * du = dh g s(g), and h of those g and u (NULL: not wanted). */
 int act_swiglu_backward(const void* dh, int64_t lddh, const int8_t* codes, int64_t ldc, const uint8_t* exponents, int64_t lde,
                         void* d_gate_up, int64_t ldg, void* h, int64_t ldh, int64_t rows, int64_t cols, int32_t type, void* stream);
+
+/* Causal attention over packed sequences with grouped heads.  q and out are bf16 [rows][heads][dim], k and v [rows][kv_heads]
+ * [dim] (token and head strides, heads on 16 bytes; dim a multiple of 8, at most 128); query head h
+ * reads key head h / (heads / kv_heads).  Sequence i is rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (int32, sequences + 1
+ * values on the device, not falling, of any lengths, 0 among them); cu_seqlens NULL: `sequences` of rows / sequences each.
+ *   s_ij = scale q_i k_j for j <= i of i's sequence,  lse_i = log sum_j exp s_ij,  out_i = sum_j exp(s_ij - lse_i) v_j
+ * lse is fp32 [heads][rows].  Rows of no sequence (before the first, behind the last) are set to 0 in both.  Nothing that a row
+ * does not see reaches it, NaN and infinities included.  Products and sums are fp32, p is rounded to bf16 for its
+ * product; two runs agree bit for bit.  Values of cu_seqlens outside [0, rows] are taken as the nearest of them; what falls
+ * gives undefined values, within the buffers.  scale > 0.  One enqueued kernel; its waits are bounded (seconds): should
+ * one run out, the results it held up are NaN. */
+int attn_forward(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                 int64_t v_head, void* out, int64_t out_row, int64_t out_head, float* lse, const int32_t* cu_seqlens, int64_t sequences,
+                 int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, float scale, void* stream);
+/* Scratch bytes of attn_backward (cu_seqlens: only whether it is NULL counts). */
+int attn_workspace(const int32_t* cu_seqlens, int64_t sequences, int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, size_t* bytes);
+/* Gradients of the above from d_out and what forward gave, bf16: with p_ij = exp(s_ij - lse_i), delta_i = d_out_i out_i and
+ * dS_ij = p_ij (d_out_i v_j - delta_i): dq_i = scale sum_j dS_ij k_j, and, summed over the heads that share j, dk_j = scale
+ * sum_i dS_ij q_i, dv_j = sum_i p_ij d_out_i.  dq NULL, or dk and dv NULL: not wanted.  p and dS are rounded to bf16 for their
+ * products.  Rows of no sequence get 0.  workspace: 256-byte aligned. */
+int attn_backward(const void* d_out, int64_t do_row, int64_t do_head, const void* q, int64_t q_row, int64_t q_head, const void* k,
+                  int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head, const void* out, int64_t out_row,
+                  int64_t out_head, const float* lse, void* dq, int64_t dq_row, int64_t dq_head, void* dk, int64_t dk_row, int64_t dk_head,
+                  void* dv, int64_t dv_row, int64_t dv_head, const int32_t* cu_seqlens, int64_t sequences, int64_t rows, int64_t heads,
+                  int64_t kv_heads, int64_t dim, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 const char* optim_last_error(void);
 

@@ -1,14 +1,15 @@
-"""The inside of a transformer block's training step over liblmopt.so: rotary positions, and activations kept in 8
-bits between the forward and the backward pass, alone and in the gated activation that reads
-them.  With ``head`` (norm, loss) and the optimizer groups they are a memory-lean training step.
+"""The inside of a transformer block's training step over liblmopt.so: causal attention over packed sequences with
+grouped heads, rotary positions, and activations kept in 8 bits between the forward and the backward pass,
+alone and in the gated activation that reads them.  With ``head`` (norm, loss) and the optimizer groups they are a memory-lean training step.
 
 The ``*_forward`` / ``*_backward`` functions and ``pack_activation`` / ``unpack_activation`` are the library calls on
 tensors; each takes ``stream`` (a torch stream the caller has ordered after its inputs; default: the
-current one).  ``rotary``, ``swiglu``, ``gated_mlp`` are the same with autograd and run on
+current one).  ``attention``, ``rotary``, ``swiglu``, ``gated_mlp`` are the same with autograd and run on
 the current stream.  PyTorch supplies device memory, streams, the graph and plain matrix products.
 """
 from __future__ import annotations
 
+import functools
 import math
 from dataclasses import dataclass
 from fractions import Fraction
@@ -34,6 +35,127 @@ def _heads(t: torch.Tensor, name: str) -> torch.Tensor:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
     return t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
+
+
+# ----------------------------------------------------------------------------------------- attention
+def _attn_heads(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t [tokens, heads, dim], bf16, as the kernels read it: heads on 16 bytes, rows and heads apart; t itself, or a copy."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+    t = _heads(t, name)
+    rows, heads, dim = t.shape
+    row, head = t.stride(0), t.stride(1)
+    if (t.data_ptr() % 16 or rows > 1 and (row % 8 or row < dim) or heads > 1 and (head % 8 or head < dim) or
+            dim > 1 and t.stride(2) != 1):
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _at(t: torch.Tensor | None):
+    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _attn_args(q, k, v, cu_seqlens, scale):
+    """(q, k, v) as [tokens, heads, dim], the borders' pointer, sequences, rows, heads, kv_heads, dim, scale."""
+    batch = None
+    if q.dim() == 4:
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens are for [tokens, heads, dim]; [batch, length, heads, dim] are sequences of one length")
+        if k.dim() != 4 or v.dim() != 4 or k.shape[:2] != q.shape[:2] or v.shape[:2] != q.shape[:2]:
+            raise ValueError("q, k and v must have the same batch and length")
+        batch = q.shape[0]
+        q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
+    q, k, v = _attn_heads(q, "q"), _attn_heads(k, "k"), _attn_heads(v, "v")
+    rows, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    if k.shape != v.shape or k.shape[0] != rows or k.shape[2] != dim:
+        raise ValueError(f"q {list(q.shape)}, k {list(k.shape)} and v {list(v.shape)} do not fit")
+    if heads < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} query heads cannot share {kv_heads} key heads")
+    if dim < 8 or dim > 128 or dim % 8:
+        raise ValueError(f"heads must have 8 to 128 elements, a multiple of 8, not {dim}")
+    borders = None
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != q.get_device():
+            raise ValueError(f"cu_seqlens must be int32 [sequences + 1] on {q.device}")
+        if not cu_seqlens.is_contiguous():
+            cu_seqlens = cu_seqlens.contiguous()
+        borders, batch = cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+    elif batch is None or batch == 0:
+        batch = 1
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    return q, k, v, cu_seqlens, (borders, batch, rows, heads, kv_heads, dim, scale)
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_bytes(packed: bool, sequences: int, rows: int, heads: int, kv_heads: int, dim: int) -> int:
+    return lmopt.attn_workspace(256 if packed else None, sequences, rows, heads, kv_heads, dim)
+
+
+@_on_stream
+def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                      scale: float | None = None):
+    """(out, lse): every query attends to the keys of its sequence up to its own, softmax(scale q k) v with scale
+    dim^-1/2 by default.  q [tokens, heads, dim], k and v [tokens, kv_heads, dim] bf16 (dim a multiple of 8 up to 128, heads a multiple of
+    kv_heads), sequence i rows cu_seqlens[i] to cu_seqlens[i + 1] - 1 (int32, on the device; None: one sequence), or all with
+    a batch dimension before, sequences of one length.  lse, fp32 [heads, tokens], is the log of the softmax's
+    denominator.  Rows of no sequence are 0 in both."""
+    shape = q.shape
+    q, k, v, _cu, args = _attn_args(q, k, v, cu_seqlens, scale)
+    out = q.new_empty(q.shape)
+    lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
+    lmopt.attn_forward(_at(q), _at(k), _at(v), _at(out), lse.data_ptr(), *args, _stream_ptr(None))
+    return out.view(shape), lse
+
+
+@_on_stream
+def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                       cu_seqlens: torch.Tensor | None = None, scale: float | None = None, need_q: bool = True, need_kv: bool = True):
+    """(dq, dk, dv) from the gradient of out and what the forward call was given and returned; None for those that are not
+    needed (dk and dv go together).  Rows of no sequence get 0."""
+    if d_out.shape != q.shape or out.shape != q.shape:
+        raise ValueError(f"d_out and out must be {list(q.shape)}")
+    shapes = q.shape, k.shape, v.shape
+    if d_out.dim() == 4:
+        d_out, out = (t.reshape(-1, *t.shape[2:]) for t in (d_out, out))
+    q, k, v, _cu, args = _attn_args(q, k, v, cu_seqlens, scale)
+    d_out, out = _attn_heads(d_out, "d_out"), _attn_heads(out, "out")
+    if lse.dtype != torch.float32 or lse.shape != (q.shape[1], q.shape[0]) or lse.get_device() != q.get_device():
+        raise ValueError(f"lse must be float32 {[q.shape[1], q.shape[0]]} on {q.device}")
+    if not lse.is_contiguous():
+        lse = lse.contiguous()
+    dq = q.new_empty(q.shape) if need_q else None
+    dk, dv = (k.new_empty(k.shape), v.new_empty(v.shape)) if need_kv else (None, None)
+    borders, sequences, rows, heads, kv_heads, dim, _ = args
+    nbytes = _attn_bytes(borders is not None, sequences, rows, heads, kv_heads, dim)
+    work = q.new_empty(nbytes, dtype=torch.uint8)
+    lmopt.attn_backward(_at(d_out), _at(q), _at(k), _at(v), _at(out), lse.data_ptr(), _at(dq), _at(dk), _at(dv), *args,
+                        work.data_ptr(), nbytes, _stream_ptr(None))
+    return tuple(None if t is None else t.view(s) for t, s in zip((dq, dk, dv), shapes))
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        out, lse = attention_forward(q, k, v, cu_seqlens, scale)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dq, dk, dv = attention_backward(d_out, q, k, v, out, lse, cu_seqlens, ctx.scale, need[0], need[1] or need[2])
+        return dq, dk if need[1] else None, dv if need[2] else None, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor | None = None, scale: float | None = None):
+    """attention_forward's out with autograd (cu_seqlens must not change until the backward pass)."""
+    return _Attention.apply(q, k, v, cu_seqlens, scale)
 
 
 # ---------------------------------------------------------------------------------- rotary positions

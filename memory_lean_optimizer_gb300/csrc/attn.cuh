@@ -1,0 +1,159 @@
+// attn.cuh -- what the attention kernels share: where the packed sequences' tiles are, and their operands.
+#pragma once
+
+#include <algorithm>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "packed.cuh"
+#include "tensor.cuh"
+#include "tensor_map.h"
+
+namespace lmo {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The sequences of a call: rows cu[i] .. cu[i + 1] - 1 of its buffers, or (cu NULL) `n` of rows / n each.
+struct Sequences {
+    const int32_t* cu;
+    int32_t n;
+    int64_t rows;
+    // Borders of n + 2 segments: the rows before the first sequence, the sequences, the rows behind the last.
+    // Whatever cu holds, they lie within the buffers.
+    __device__ __forceinline__ int64_t border(int i) const {
+        if (i == 0) return 0;
+        if (i == n + 2) return rows;
+        if (!cu) return (int64_t)(i - 1) * (rows / n);
+        return min(max((int64_t)cu[i - 1], (int64_t)0), rows);
+    }
+};
+// bf16 [rows][heads][dim], strides in elements.
+struct HeadRows {
+    void* p;
+    int64_t row, head;
+};
+struct AttnCall {
+    HeadRows q, k, v, out, d_out, dq, dk, dv;
+    float* lse;
+    Sequences seq;
+    int64_t heads, kv_heads, dim;
+    float scale;
+    void* workspace;      // backward
+};
+int launch_attn_forward(const AttnCall& c, cudaStream_t s);
+int launch_attn_backward(const AttnCall& c, cudaStream_t s);
+size_t attn_workspace_bytes(const AttnCall& c);
+
+// Tiles of kRows rows start at each segment's start.  A segment's tiles are numbered from border / kRows + its
+// number on: that leaves room for all of them and needs no pass over the segments before it.
+inline int64_t tile_slots(const Sequences& s, int rows) { return s.rows / rows + s.n + 2; }
+
+struct Tile {
+    int segment;          // 0 and n + 1: no sequence, rows to be set to zero
+    int64_t start, end;   // the segment's rows
+    int64_t first;        // the tile's first row; no tile if it is `end` or behind it
+};
+// The tile of a slot.  All threads of the CTA call it; each probes one border a round.
+template <int kRows>
+__device__ __forceinline__ Tile find_tile(const Sequences& s, int64_t slot) {
+    int lo = 0, count = s.n + 2;                      // segments lo .. lo + count - 1
+    while (count > 1) {
+        const int step = (count + (int)blockDim.x - 1) / (int)blockDim.x;
+        const int i = (int)threadIdx.x * step;
+        const bool at = i < count && s.border(lo + i) / kRows + (lo + i) <= slot;
+        const int below = max(__syncthreads_count(at), 1) - 1;
+        lo += below * step;
+        count = min(step, count - below * step);
+    }
+    Tile t;
+    t.segment = lo;
+    t.start = s.border(lo);
+    t.end = max(s.border(lo + 1), t.start);
+    t.first = t.start + (slot - (t.start / kRows + lo)) * kRows;
+    if (t.first < t.start) t.first = t.end;           // borders that fall
+    return t;
+}
+
+// One of q, k, v, d_out as a map of boxes of one head's rows, 64 elements wide (what lies past the head reads as zero).
+inline int make_head_map(CUtensorMap* map, const void* base, int64_t rows, int64_t heads, int64_t dim, int64_t ld, int64_t hs, int box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return set_error(OPTIM_ECUDA, "cuTensorMapEncodeTiled is not available");
+    // a dimension of one element has no stride of its own
+    if (heads == 1) hs = dim;
+    if (rows == 1) ld = heads * dim;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(OPTIM_ECUDA, "tensor map of %lld x %lld heads of %lld: error %d", (long long)rows, (long long)heads, (long long)dim, (int)r);
+    return OPTIM_OK;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A tile's rows in shared memory: boxes of 64 elements (128 bytes) of kRows rows, one after the other.
+// One box or two of a head's rows.
+template <int kRows>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, int dim, int head, int64_t row, uint32_t bar) {
+    tma_load_3d(dst, map, 0, head, (int)row, bar);
+    if (dim > 64) tma_load_3d(dst + kRows * 128, map, 64, head, (int)row, bar);
+}
+
+// Zeroes the infinities and NaN of a tile in shared memory, thread `i` in row i, for a product with weights of which
+// some are masked: 0 times those is NaN.  True if there was any (then the thread's stores are made visible to the tensor cores).
+// Rows lie 128 bytes apart, so the threads of a warp start at different banks.
+template <int kRows>
+__device__ __forceinline__ bool clear_non_finite(char* tile, int dim, int i) {
+    bool any = false;
+    for (int box = 0; box < (dim > 64 ? 2 : 1); ++box) {
+        char* const row = tile + box * kRows * 128 + i * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint4* const at = reinterpret_cast<uint4*>(row + ((q + i) & 7) * 16);
+            const uint4 v = *at;
+            // an exponent of ones and the bit below it make a carry into the sign's place
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t bad = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+            if (bad) {
+                any = true;
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t b = ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                    o[k] = w[k] & ~((b >> 15) * 0xFFFFu);
+                }
+                *at = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+    if (any) smem_to_async();
+    return any;
+}
+
+// What clear_non_finite took out of rows a..b-1 (elements c .. c + 31 of a head), added to sums whose weights are positive.
+__device__ __forceinline__ void add_non_finite(float (&x)[32], const uint16_t* base, int64_t ld, int64_t a, int64_t b, int c, int dim) {
+    for (int64_t r = a; r < b; ++r)
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (c + k < dim) {
+                const uint32_t h = base[r * ld + c + k];
+                if ((h & 0x7F80u) == 0x7F80u) x[k] += bf16_to_f32(h);
+            }
+}
+
+}  // namespace lmo

@@ -1,0 +1,410 @@
+// attn_backward.cu -- the gradients of causal attention over packed sequences with grouped heads.
+//   p_ij = exp(s_ij - lse_i),  delta_i = dO_i o_i,  dS_ij = p_ij (dO_i v_j - delta_i)
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i   (i: of all heads that share j)
+// Scores are formed again.  Two product kernels, one for dq (a tile of queries, the keys stream by) and one for dk and
+// dv (a tile of keys, the queries of the group's heads stream by): every sum has one owner and one order, at the
+// price of forming p and dS twice (7 products, not 5); adding dq up from the tiles of keys would need atomics, whose order changes
+// results, or a buffer of fp32.
+//
+// Both are one kernel in two roles.  A CTA holds two operands of 128 rows (Q and dO, or K and V) and streams pairs of
+// blocks of 64 rows of the other two.  X = A0 B0' and Y = A1 B1' go into one of two pairs of accumulators (64 columns each), four warps
+// turn them into p and dS, in bf16, in place (the tensor cores want both operands of one type), and those are the A operands, from tensor
+// memory, of the sums' products (with B0 and B1 read along their rows).  For keys X and Y are the transposed
+// scores: nothing is ever transposed through shared memory.  Blocks of 64 so that two pairs and the two sums fit in the 512
+// columns; while four warps work on one pair the tensor cores fill the other.
+#include <cstdio>
+
+#include "attn.cuh"
+
+namespace lmo {
+namespace {
+
+constexpr int kTile = 128, kStep = 64;           // rows of a CTA's tile and of a streamed block
+constexpr int kAttnThreads = 384;                // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory; 4-7 and 8-11: every other block
+constexpr uint32_t kTileBytes = kTile * 256, kStepBytes = kStep * 256;
+constexpr int kStages = 4;
+constexpr size_t kSmem = 2 * kTileBytes + kStages * (2 * kStepBytes + kStep * 8) + 1024;
+
+// The rows' lse (times log2 e) and delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
+// of 64 (find_tile), `slots` a head; rows behind a sequence's end have lse inf (p is 0) and delta 0.
+struct RowBlock {
+    float lse[kStep], delta[kStep];
+};
+
+struct PrepArgs {
+    Sequences seq;
+    int64_t slots;
+    int32_t heads, dim;
+    const uint16_t* out;
+    int64_t ldo, hso;
+    const uint16_t* d_out;
+    int64_t lddo, hsdo;
+    const float* lse;
+    RowBlock* rows;
+};
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+        s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+    }
+    return s;
+}
+
+// A block of 64 rows of one head to a CTA: four threads to a row.
+__global__ void __launch_bounds__(256) k_attn_rows(const PrepArgs p) {
+    pdl_sync();
+    const int head = (int)(blockIdx.x % (unsigned)p.heads);
+    const int64_t slot = blockIdx.x / (unsigned)p.heads;
+    const Tile tile = find_tile<kStep>(p.seq, slot);
+    if (tile.first >= tile.end || tile.segment == 0 || tile.segment == p.seq.n + 1) return;
+    const int in = threadIdx.x >> 2, part = threadIdx.x & 3;
+    const int64_t row = tile.first + in;
+    const bool live = row < tile.end;
+    float s = 0.0f;
+    if (live) {
+        const uint16_t* const o = p.out + row * p.ldo + head * p.hso;
+        const uint16_t* const g = p.d_out + row * p.lddo + head * p.hsdo;
+        for (int c = 8 * part; c < p.dim; c += 32)
+            s += dot8(*reinterpret_cast<const uint4*>(o + c), *reinterpret_cast<const uint4*>(g + c));
+    }
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+    if (part == 0) {
+        RowBlock& b = p.rows[head * p.slots + slot];
+        b.lse[in] = live ? p.lse[head * p.seq.rows + row] * kLog2e : INFINITY;
+        b.delta[in] = live ? s : 0.0f;
+    }
+}
+
+enum { kQueries = 0, kKeys = 1 };
+
+struct BackwardArgs {
+    Sequences seq;
+    int64_t slots, row_slots;           // tiles of 128, blocks of 64
+    int32_t heads, kv_heads, group, dim;
+    float scale;
+    const RowBlock* rows;
+    HeadRows out0, out1;                // dq; or dk, dv
+    const uint16_t* d_out;              // kKeys: for what is taken out of masked blocks
+    int64_t lddo, hsdo;
+    uint64_t wait_ns;
+    int32_t stall;
+};
+enum Stall { kStallCopy = 1, kStallSoftmax = 2 };
+
+// maps: the tile's operands (a0, a1), the streamed ones (b0, b1): Q, dO, K, V for queries, K, V, Q, dO for keys
+template <int kRole>
+__global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
+                                                                   const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
+                                                                   const BackwardArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int gave_up, found, copied;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_sync();
+    const int heads = kRole == kQueries ? p.heads : p.kv_heads;
+    const int head = (int)(blockIdx.x % (unsigned)heads);
+    // the tiles with the most work first: the last queries, the first keys
+    const int64_t slot = blockIdx.x / (unsigned)heads;
+    const Tile tile = find_tile<kTile>(p.seq, kRole == kQueries ? p.slots - 1 - slot : slot);
+    if (tile.first >= tile.end) return;
+    if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
+        const int rows = (int)min((int64_t)kTile, tile.end - tile.first), vecs = p.dim / 8;
+        for (int i = threadIdx.x; i < rows * vecs; i += kAttnThreads) {
+            const int64_t row = tile.first + i / vecs;
+            const int c = i % vecs * 8;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out0.p) + head * p.out0.head + row * p.out0.row + c) = make_uint4(0, 0, 0, 0);
+            if (kRole == kKeys)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out1.p) + head * p.out1.head + row * p.out1.row + c) = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
+    const uint32_t stages = base + 2 * kTileBytes;                       // stage: B0, B1
+    const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
+    const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
+                   sums_done = ready + 16, drained = sums_done + 8;
+    if (threadIdx.x == 0) {
+        gave_up = found = copied = 0;
+        mbar_init(a_full, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(x_done + 8 * i, 1);
+            mbar_init(ready + 8 * i, 4);
+        }
+        mbar_init(sums_done, 1);
+        mbar_init(drained, 1);
+        mbar_init_fence();
+    }
+    if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
+    auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
+
+    // Streamed blocks: for queries those of the keys up to the tile's last row, for keys those of the queries from the tile's first row
+    // on, head by head.
+    const int64_t stream_first = kRole == kQueries ? tile.start : tile.first;
+    const int64_t stream_end = kRole == kQueries ? min(tile.first + kTile, tile.end) : tile.end;
+    const int per_head = (int)((stream_end - stream_first + kStep - 1) / kStep);
+    const int blocks = per_head * (kRole == kQueries ? 1 : p.group);
+
+    if (warp < 4) {
+        regs_down<56>();
+        if (warp == 0 && elect_lane()) {
+            const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
+            const uint32_t boxes = p.dim > 64 ? 2 : 1;
+            mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
+            load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, a_full);
+            load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, a_full);
+            int issued = 0, in = 0;
+            int of = kRole == kQueries ? head / p.group : head * p.group;     // head of the streamed operands
+            const int64_t row_slot = kRole == kKeys ? (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep : 0;
+            bool ok = true;
+            for (int i = 0; ok && i < blocks; ++i) {
+                const int stage = i % kStages;
+                ok = issued != stop && wait(empty + 8 * stage, (i / kStages & 1) ^ 1u);
+                if (!ok) break;
+                const uint32_t bar = full + 8 * stage, b = stages + stage * 2 * kStepBytes;
+                mbar_expect_tx(bar, 2 * boxes * kStep * 128 + (kRole == kKeys ? (uint32_t)sizeof(RowBlock) : 0u));
+                const int64_t row = stream_first + (int64_t)in * kStep;
+                load_rows<kStep>(b, &map_b0, p.dim, of, row, bar);
+                load_rows<kStep>(b + kStepBytes, &map_b1, p.dim, of, row, bar);
+                if (kRole == kKeys)
+                    bulk_load(row_stages + stage * (uint32_t)sizeof(RowBlock), p.rows + of * p.row_slots + row_slot + in, sizeof(RowBlock), bar);
+                ++issued;
+                if (++in == per_head) in = 0, ++of;
+            }
+            // the last stages come back before the CTA ends: nothing arrives on its barriers after that
+            for (int i = max(0, blocks - kStages); ok && i < blocks; ++i) ok = wait(empty + 8 * (i % kStages), i / kStages & 1);
+            copied = issued;
+        } else if (warp == 1 && elect_lane()) {
+            const int steps = (p.dim + 15) / 16;                               // of 16 elements along the head
+            const uint32_t desc_x = mma_desc(128, kStep, false, false), desc_sum = mma_desc(128, steps * 16, false, true);
+            bool ok = wait(a_full, 0);
+            auto scores = [&](int i) {
+                ok = wait(full + 8 * (i % kStages), i / kStages & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t b = stages + i % kStages * 2 * kStepBytes, d = tmem + (i & 1) * kStep;
+                for (int h = 0; h < 2; ++h)
+                    for (int j = 0; j < steps; ++j)
+                        mma_bf16<1>(d + h * 128, operand_desc(base + h * kTileBytes + (j >> 2) * (kTile * 128) + (j & 3) * 32, 8192, 1024),
+                                    operand_desc(b + h * kStepBytes + (j >> 2) * (kStep * 128) + (j & 3) * 32, 8192, 1024), desc_x, j > 0);
+                mma_commit<1>(x_done + 8 * (i & 1));
+            };
+            if (ok) scores(0);
+            for (int i = 0; ok && i < blocks; ++i) {
+                if (i + 1 < blocks) scores(i + 1);      // over p and dS of block i - 1, behind the products that read them
+                if (ok) ok = wait(ready + 8 * (i & 1), i / 2 & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b = stages + i % kStages * 2 * kStepBytes, a = tmem + (i & 1) * kStep;
+                if (kRole == kKeys)
+                    for (int j = 0; j < kStep / 16; ++j)     // dv += p' dO
+                        mma_bf16_ta(tmem + 384, a + j * 8, operand_desc(b + kStepBytes + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
+                    mma_bf16_ta(tmem + 256, a + 128 + j * 8, operand_desc(b + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                mma_commit<1>(empty + 8 * (i % kStages));
+            }
+            if (ok) mma_commit<1>(sums_done);
+        }
+        __syncwarp();
+    } else {
+        regs_up<224>();
+        const int t = (warp >> 2) - 1;                                         // blocks t, t + 2, ..
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int in = 32 * (warp & 3) + lane;                                 // this thread's row of the tile
+        const int64_t row = tile.first + in;
+        const uint32_t x_at = tmem + lanes + t * kStep;
+        const float c = p.scale * kLog2e;
+        const F2 c2 = f2(c, c);
+        float my_lse = 0.0f, my_delta = 0.0f;
+        if (kRole == kQueries) {
+            // tiles of 128 start at a block of 64
+            const RowBlock& b = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
+            if (row < tile.end) my_lse = b.lse[in % kStep], my_delta = b.delta[in % kStep];
+        }
+        const F2 my_lse2 = f2(-my_lse, -my_lse), my_delta2 = f2(-my_delta, -my_delta);
+        bool ok = true;
+        for (int i = t; i < blocks; i += 2) {
+            const int stage = i % kStages, at = kRole == kQueries ? i : i % per_head;
+            const int64_t first = stream_first + (int64_t)at * kStep;          // the block's first row
+            // keys behind the row's own, queries before it, or rows behind the sequence
+            const bool masked = kRole == kQueries ? first + kStep > tile.first : first < tile.first + kTile || first + kStep > tile.end;
+            ok = wait(x_done + 8 * t, i / 2 & 1);
+            // what the copies brought is read here too
+            if (ok && (kRole == kKeys || masked)) ok = wait(full + 8 * stage, i / kStages & 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[2][32], y[2][32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                tmem_load32(x_at + 32 * q, x[q]);
+                tmem_load32(x_at + 128 + 32 * q, y[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                tmem_wait(x[q]);
+                tmem_wait(y[q]);
+            }
+            const RowBlock* const rb = reinterpret_cast<const RowBlock*>(base_ptr + (row_stages - base)) + stage;
+            uint32_t pw[32], dw[32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    F2 l[2] = {my_lse2, my_lse2}, d[2] = {my_delta2, my_delta2};
+                    if (kRole == kKeys) {
+                        const float4 a = *reinterpret_cast<const float4*>(&rb->lse[32 * q + k]), b = *reinterpret_cast<const float4*>(&rb->delta[32 * q + k]);
+                        l[0] = f2(-a.x, -a.y), l[1] = f2(-a.z, -a.w), d[0] = f2(-b.x, -b.y), d[1] = f2(-b.z, -b.w);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = k + 2 * h;
+                        float a, b, u, w;
+                        split2(fma2(f2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), c2, l[h]), a, b);
+                        a = exp2_approx(a), b = exp2_approx(b);
+                        split2(mul2(f2(a, b), add2(f2(__uint_as_float(y[q][e]), __uint_as_float(y[q][e + 1])), d[h])), u, w);
+                        if (masked) {                                          // whatever was multiplied
+                            const int64_t other = first + 32 * q + e;
+                            const bool off0 = kRole == kQueries ? other > row : other < row || other >= tile.end;
+                            const bool off1 = kRole == kQueries ? other + 1 > row : other + 1 < row || other + 1 >= tile.end;
+                            if (off0) a = u = 0.0f;
+                            if (off1) b = w = 0.0f;
+                        }
+                        pw[(32 * q + e) / 2] = pack_bf16(a, b);
+                        dw[(32 * q + e) / 2] = pack_bf16(u, w);
+                    }
+                }
+            if (kRole == kKeys) tmem_store32(x_at, pw);
+            tmem_store32(x_at + 128, dw);
+            tmem_store_wait();
+            if (masked && in < kStep) {      // rows of masked places are not multiplied, not even by 0
+                char* const b = base_ptr + (stages - base) + stage * 2 * kStepBytes;
+                clear_non_finite<kStep>(b, p.dim, in);
+                if (kRole == kKeys && clear_non_finite<kStep>(b + kStepBytes, p.dim, in)) found = 1;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && !(blockIdx.x == 0 && p.stall == kStallSoftmax)) mbar_arrive(ready + 8 * t);
+        }
+        ok = ok && wait(sums_done, 0);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        // the first four warps write dq, or dk; the others half of dq, or dv
+        const bool live = row < tile.end;
+        const bool had = kRole == kKeys && t == 1 && *static_cast<volatile int*>(&found) != 0;
+        const HeadRows& o = kRole == kKeys && t == 1 ? p.out1 : p.out0;
+        uint16_t* const to = static_cast<uint16_t*>(o.p) + head * o.head + row * o.row;
+        const float f = !ok ? __builtin_nanf("") : kRole == kKeys && t == 1 ? 1.0f : p.scale;
+        const uint32_t sum_at = tmem + lanes + 256 + (kRole == kKeys ? 128 * t : 0);
+#pragma unroll 1
+        for (int q = kRole == kQueries ? 32 * t : 0; q < p.dim; q += kRole == kQueries ? 64 : 32) {
+            uint32_t r[32];
+            tmem_load32(sum_at + q, r);
+            tmem_wait(r);
+            if (live) {
+                float z[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(r[k]) * f;
+                if (had)      // masked blocks of each head: the tile's own rows and the sequence's last block
+                    for (int g = 0; g < p.group; ++g) {
+                        const uint16_t* const d_out = p.d_out + (int64_t)(head * p.group + g) * p.hsdo;
+                        const int64_t own = min(tile.first + kTile, tile.end);
+                        const int64_t last = tile.first + (tile.end - tile.first) / kStep * kStep;   // first row of a block that is not whole
+                        add_non_finite(z, d_out, p.lddo, row, own, q, p.dim);
+                        add_non_finite(z, d_out, p.lddo, max(own, last), tile.end, q, p.dim);
+                    }
+#pragma unroll
+                for (int k = 0; k < 32; k += 8)
+                    if (q + k < p.dim)
+                        *reinterpret_cast<uint4*>(to + q + k) = make_uint4(pack_bf16(z[k], z[k + 1]), pack_bf16(z[k + 2], z[k + 3]),
+                                                                           pack_bf16(z[k + 4], z[k + 5]), pack_bf16(z[k + 6], z[k + 7]));
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // every role has stopped; after a wait that ran out, what is in flight is waited for, bounded too
+    if (*static_cast<volatile int*>(&gave_up)) {
+        if (warp == 1 && elect_lane()) {
+            mma_commit<1>(drained);
+            mbar_drain(drained, 0);
+        }
+        if (warp == 0 && elect_lane()) {
+            const int n = copied;
+            mbar_drain(a_full, 0);
+            for (int i = max(0, n - kStages); i < n; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 2) tmem_free<1>(tmem, 512);
+}
+
+int injected_stall(int role) {
+    const char* const names[2][2] = {{"stall_attention_dq_copy", "stall_attention_dq_softmax"}, {"stall_attention_dkv_copy", "stall_attention_dkv_softmax"}};
+    return fault_injected(names[role][0]) ? kStallCopy : fault_injected(names[role][1]) ? kStallSoftmax : 0;
+}
+
+template <int kRole>
+int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s) {
+    const bool queries = kRole == kQueries;
+    CUtensorMap map[4];
+    for (int i = 0; i < 4; ++i) {
+        const HeadRows& t = operands[i];
+        const int rc = make_head_map(&map[i], t.p, c.seq.rows, (i < 2) == queries ? c.heads : c.kv_heads, c.dim, t.row, t.head, i < 2 ? kTile : kStep);
+        if (rc) return rc;
+    }
+    static std::atomic<uint64_t> allowed{0};
+    const int rc = allow_smem(k_attn_backward<kRole>, (int)kSmem, allowed);
+    if (rc) return rc;
+    BackwardArgs a{};
+    a.seq = c.seq;
+    a.slots = tile_slots(c.seq, kTile), a.row_slots = tile_slots(c.seq, kStep);
+    a.heads = (int)c.heads, a.kv_heads = (int)c.kv_heads, a.group = (int)(c.heads / c.kv_heads), a.dim = (int)c.dim;
+    a.scale = c.scale;
+    a.rows = static_cast<const RowBlock*>(c.workspace);
+    a.out0 = queries ? c.dq : c.dk, a.out1 = c.dv;
+    a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
+    a.stall = faults_injected() ? injected_stall(kRole) : 0;
+    a.wait_ns = a.stall ? kWaitNs / 40 : kWaitNs;
+    return check_cuda(launch_after(k_attn_backward<kRole>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads)), kAttnThreads, kSmem, 1, s,
+                                   map[0], map[1], map[2], map[3], a),
+                      "attention backward launch");
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const AttnCall& c) { return (size_t)tile_slots(c.seq, kStep) * c.heads * sizeof(RowBlock); }
+
+int launch_attn_backward(const AttnCall& c, cudaStream_t s) {
+    PrepArgs a{};
+    a.seq = c.seq;
+    a.slots = tile_slots(c.seq, kStep);
+    a.heads = (int)c.heads, a.dim = (int)c.dim;
+    a.out = static_cast<const uint16_t*>(c.out.p), a.ldo = c.out.row, a.hso = c.out.head;
+    a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
+    a.lse = c.lse;
+    a.rows = static_cast<RowBlock*>(c.workspace);
+    int rc = check_cuda(launch_after(k_attn_rows, (unsigned)(a.slots * c.heads), 256, 0, 1, s, a), "attention backward launch");
+    if (!rc && c.dk.p) rc = launch_role<kKeys>(c, {c.k, c.v, c.q, c.d_out}, s);
+    if (!rc && c.dq.p) rc = launch_role<kQueries>(c, {c.q, c.d_out, c.k, c.v}, s);
+    return rc;
+}
+
+}  // namespace lmo

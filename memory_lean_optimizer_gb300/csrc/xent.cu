@@ -31,6 +31,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "tensor.cuh"
+#include "tensor_map.h"
 
 namespace lmo {
 namespace {
@@ -852,22 +853,6 @@ XentPlan plan_xent(int64_t rows, int64_t dim, int64_t vocab, const void* weight,
     }
     p.bytes = at;
     return p;
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static EncodeFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult st;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-            st != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeFn>(f);
-    }();
-    return fn;
 }
 
 // Map of a [rows][cols] bf16 matrix (row stride ld elements) for boxes of box_rows rows of 64 elements.

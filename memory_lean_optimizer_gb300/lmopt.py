@@ -53,6 +53,7 @@ EXPORTED = (
     "norm_layer_forward", "norm_layer_backward", "norm_layer_workspace",
     "loss_xent_forward", "loss_xent_backward", "loss_xent_workspace",
     "rope_apply", "act_pack_i8", "act_unpack_i8", "act_swiglu_forward", "act_swiglu_backward",
+    "attn_forward", "attn_backward", "attn_workspace",
 )
 
 
@@ -129,6 +130,9 @@ def load(path: str = LIB_PATH):
             "act_unpack_i8": [P, I64, P, I64, P, I64, I64, I64, I32, P],
             "act_swiglu_forward": [P, I64, P, I64, P, I64, P, I64, I64, I64, I32, P],
             "act_swiglu_backward": [P, I64, P, I64, P, I64, P, I64, P, I64, I64, I64, I32, P],
+            "attn_forward": [*[P, I64, I64] * 4, P, P, I64, I64, I64, I64, I64, F, P],
+            "attn_workspace": [P, I64, I64, I64, I64, I64, ctypes.POINTER(ctypes.c_size_t)],
+            "attn_backward": [*[P, I64, I64] * 5, P, *[P, I64, I64] * 3, P, I64, I64, I64, I64, I64, F, P, ctypes.c_size_t, P],
             "loss_xent_workspace": [I64, I64, I64, P, I64, I32, ctypes.POINTER(ctypes.c_size_t)],
             "loss_xent_forward": [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, ctypes.c_size_t, P],
             "loss_xent_backward": [P, I64, P, I64, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, ctypes.c_size_t, P],
@@ -456,3 +460,21 @@ def act_swiglu_forward(gate_up: int, ldg: int, h: int, ldh: int, codes: int | No
 def act_swiglu_backward(dh: int, lddh: int, codes: int, ldc: int, exponents: int, lde: int, d_gate_up: int, ldg: int,
                         h: int | None, ldh: int, rows: int, cols: int, dtype: int, stream: int = 0) -> None:
     check(load().act_swiglu_backward(dh, lddh, codes, ldc, exponents, lde, d_gate_up, ldg, h, ldh, rows, cols, dtype, stream))
+
+
+# q, k, v, out, d_out, dq, dk, dv: (pointer, row stride, head stride)
+def attn_forward(q, k, v, out, lse: int, cu_seqlens: int | None, sequences: int, rows: int, heads: int, kv_heads: int, dim: int,
+                 scale: float, stream: int = 0) -> None:
+    check(load().attn_forward(*q, *k, *v, *out, lse, cu_seqlens, sequences, rows, heads, kv_heads, dim, scale, stream))
+
+
+def attn_workspace(cu_seqlens: int | None, sequences: int, rows: int, heads: int, kv_heads: int, dim: int) -> int:
+    n = ctypes.c_size_t()
+    check(load().attn_workspace(cu_seqlens, sequences, rows, heads, kv_heads, dim, ctypes.byref(n)))
+    return n.value
+
+
+def attn_backward(d_out, q, k, v, out, lse: int, dq, dk, dv, cu_seqlens: int | None, sequences: int, rows: int, heads: int,
+                  kv_heads: int, dim: int, scale: float, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    check(load().attn_backward(*d_out, *q, *k, *v, *out, lse, *dq, *dk, *dv, cu_seqlens, sequences, rows, heads, kv_heads, dim,
+                               scale, workspace, workspace_bytes, stream))
