@@ -145,11 +145,12 @@ __device__ __forceinline__ bool clear_non_finite(char* tile, int dim, int i) {
     return any;
 }
 
-// What clear_non_finite took out of rows a..b-1 (elements c .. c + 31 of a head), added to sums whose weights are positive.
-__device__ __forceinline__ void add_non_finite(float (&x)[32], const uint16_t* base, int64_t ld, int64_t a, int64_t b, int c, int dim) {
+// What clear_non_finite took out of rows a..b-1 (elements c .. c + N - 1 of a head), added to sums whose weights are positive.
+template <int N>
+__device__ __forceinline__ void add_non_finite(float (&x)[N], const uint16_t* base, int64_t ld, int64_t a, int64_t b, int c, int dim) {
     for (int64_t r = a; r < b; ++r)
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
+        for (int k = 0; k < N; ++k)
             if (c + k < dim) {
                 const uint32_t h = base[r * ld + c + k];
                 if ((h & 0x7F80u) == 0x7F80u) x[k] += bf16_to_f32(h);

@@ -25,8 +25,8 @@ constexpr uint32_t kTileBytes = kTile * 256, kStepBytes = kStep * 256;
 constexpr int kStages = 4;
 constexpr size_t kSmem = 2 * kTileBytes + kStages * (2 * kStepBytes + kStep * 8) + 1024;
 
-// The rows' lse (times log2 e) and delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
-// of 64 (find_tile), `slots` a head; rows behind a sequence's end have lse inf (p is 0) and delta 0.
+// The rows' -lse (times log2 e) and -delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
+// of 64 (find_tile), `slots` a head; rows behind a sequence's end have -inf (p is 0) and 0.
 struct RowBlock {
     float lse[kStep], delta[kStep];
 };
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(256) k_attn_rows(const PrepArgs p) {
     s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
     if (part == 0) {
         RowBlock& b = p.rows[head * p.slots + slot];
-        b.lse[in] = live ? p.lse[head * p.seq.rows + row] * kLog2e : INFINITY;
-        b.delta[in] = live ? s : 0.0f;
+        b.lse[in] = live ? p.lse[head * p.seq.rows + row] * -kLog2e : -INFINITY;
+        b.delta[in] = live ? -s : 0.0f;
     }
 }
 
@@ -86,6 +86,7 @@ struct BackwardArgs {
     Sequences seq;
     int64_t slots, row_slots;           // tiles of 128, blocks of 64
     int32_t heads, kv_heads, group, dim;
+    int32_t splits;                     // kKeys: CTAs (a cluster) that share a tile's blocks
     float scale;
     const RowBlock* rows;
     HeadRows out0, out1;                // dq; or dk, dv
@@ -95,6 +96,25 @@ struct BackwardArgs {
     int32_t stall;
 };
 enum Stall { kStallCopy = 1, kStallSoftmax = 2 };
+
+// What was cleared of d_out in the masked blocks of a tile of keys (its own rows and the sequence's last block), for the sums of one key.
+template <int N>
+__device__ __forceinline__ void add_cleared(const BackwardArgs& p, const Tile& tile, int kv, int64_t row, int c, float (&z)[N]) {
+    const int64_t own = min(tile.first + kTile, tile.end);
+    const int64_t last = tile.first + (tile.end - tile.first) / kStep * kStep;   // first row of a block that is not whole
+    for (int g = 0; g < p.group; ++g) {
+        const uint16_t* const d_out = p.d_out + (int64_t)(kv * p.group + g) * p.hsdo;
+        add_non_finite(z, d_out, p.lddo, row, own, c, p.dim);
+        add_non_finite(z, d_out, p.lddo, max(own, last), tile.end, c, p.dim);
+    }
+}
+__device__ __forceinline__ void store8(uint16_t* to, float a, float b, float c, float d, float e, float f, float g, float h) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(a, b), pack_bf16(c, d), pack_bf16(e, f), pack_bf16(g, h));
+}
+// A CTA's sums for its cluster, over the operands that it is done with: four elements of 128 rows next to each other.
+__device__ __forceinline__ float4* part_at(char* base, int which, int c, int row) {
+    return reinterpret_cast<float4*>(base + which * (kTile * 512)) + (c / 4) * kTile + row;
+}
 
 // maps: the tile's operands (a0, a1), the streamed ones (b0, b1): Q, dO, K, V for queries, K, V, Q, dO for keys
 template <int kRole>
@@ -108,14 +128,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_sync();
     const int heads = kRole == kQueries ? p.heads : p.kv_heads;
-    const int head = (int)(blockIdx.x % (unsigned)heads);
+    const int splits = kRole == kQueries ? 1 : p.splits, rank = splits > 1 ? (int)cluster_rank() : 0;
+    const unsigned unit = blockIdx.x / (unsigned)splits;
+    const int head = (int)(unit % (unsigned)heads);
     // the tiles with the most work first: the last queries, the first keys
-    const int64_t slot = blockIdx.x / (unsigned)heads;
+    const int64_t slot = unit / (unsigned)heads;
     const Tile tile = find_tile<kTile>(p.seq, kRole == kQueries ? p.slots - 1 - slot : slot);
     if (tile.first >= tile.end) return;
     if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
         const int rows = (int)min((int64_t)kTile, tile.end - tile.first), vecs = p.dim / 8;
-        for (int i = threadIdx.x; i < rows * vecs; i += kAttnThreads) {
+        for (int i = threadIdx.x; rank == 0 && i < rows * vecs; i += kAttnThreads) {
             const int64_t row = tile.first + i / vecs;
             const int c = i % vecs * 8;
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out0.p) + head * p.out0.head + row * p.out0.row + c) = make_uint4(0, 0, 0, 0);
@@ -140,7 +162,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(x_done + 8 * i, 1);
-            mbar_init(ready + 8 * i, 4);
+            mbar_init(ready + 8 * i, 8);
         }
         mbar_init(sums_done, 1);
         mbar_init(drained, 1);
@@ -158,18 +180,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const int64_t stream_first = kRole == kQueries ? tile.start : tile.first;
     const int64_t stream_end = kRole == kQueries ? min(tile.first + kTile, tile.end) : tile.end;
     const int per_head = (int)((stream_end - stream_first + kStep - 1) / kStep);
-    const int blocks = per_head * (kRole == kQueries ? 1 : p.group);
+    const int all_blocks = per_head * (kRole == kQueries ? 1 : p.group);
+    const int first_block = (int)((int64_t)all_blocks * rank / splits), blocks = (int)((int64_t)all_blocks * (rank + 1) / splits) - first_block;
 
     if (warp < 4) {
-        regs_down<56>();
+        regs_down<88>();
         if (warp == 0 && elect_lane()) {
             const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const uint32_t boxes = p.dim > 64 ? 2 : 1;
             mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
             load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, a_full);
             load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, a_full);
-            int issued = 0, in = 0;
-            int of = kRole == kQueries ? head / p.group : head * p.group;     // head of the streamed operands
+            int issued = 0, in = first_block % per_head;
+            int of = kRole == kQueries ? head / p.group : head * p.group + first_block / per_head;     // head of the streamed operands
             const int64_t row_slot = kRole == kKeys ? (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep : 0;
             bool ok = true;
             for (int i = 0; ok && i < blocks; ++i) {
@@ -204,7 +227,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                                     operand_desc(b + h * kStepBytes + (j >> 2) * (kStep * 128) + (j & 3) * 32, 8192, 1024), desc_x, j > 0);
                 mma_commit<1>(x_done + 8 * (i & 1));
             };
-            if (ok) scores(0);
+            if (ok && blocks) scores(0);
             for (int i = 0; ok && i < blocks; ++i) {
                 if (i + 1 < blocks) scores(i + 1);      // over p and dS of block i - 1, behind the products that read them
                 if (ok) ok = wait(ready + 8 * (i & 1), i / 2 & 1);
@@ -213,21 +236,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 const uint32_t b = stages + i % kStages * 2 * kStepBytes, a = tmem + (i & 1) * kStep;
                 if (kRole == kKeys)
                     for (int j = 0; j < kStep / 16; ++j)     // dv += p' dO
-                        mma_bf16_ta(tmem + 384, a + j * 8, operand_desc(b + kStepBytes + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                        mma_bf16_ta(tmem + 384, a + (j >> 1) * 32 + (j & 1) * 8, operand_desc(b + kStepBytes + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
                 for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
-                    mma_bf16_ta(tmem + 256, a + 128 + j * 8, operand_desc(b + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                    mma_bf16_ta(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, operand_desc(b + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
                 mma_commit<1>(empty + 8 * (i % kStages));
             }
             if (ok) mma_commit<1>(sums_done);
         }
         __syncwarp();
     } else {
-        regs_up<224>();
-        const int t = (warp >> 2) - 1;                                         // blocks t, t + 2, ..
+        regs_up<208>();
+        const int t = (warp >> 2) - 1;                                         // columns 32 t .. 32 t + 31 of every block
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int in = 32 * (warp & 3) + lane;                                 // this thread's row of the tile
         const int64_t row = tile.first + in;
-        const uint32_t x_at = tmem + lanes + t * kStep;
         const float c = p.scale * kLog2e;
         const F2 c2 = f2(c, c);
         float my_lse = 0.0f, my_delta = 0.0f;
@@ -236,77 +258,71 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             const RowBlock& b = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
             if (row < tile.end) my_lse = b.lse[in % kStep], my_delta = b.delta[in % kStep];
         }
-        const F2 my_lse2 = f2(-my_lse, -my_lse), my_delta2 = f2(-my_delta, -my_delta);
+        const F2 my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
+        int at = first_block % per_head;                                       // the block's place in its head
         bool ok = true;
-        for (int i = t; i < blocks; i += 2) {
-            const int stage = i % kStages, at = kRole == kQueries ? i : i % per_head;
+        for (int i = 0; i < blocks; ++i) {
+            const int stage = i % kStages;
             const int64_t first = stream_first + (int64_t)at * kStep;          // the block's first row
+            if (++at == per_head) at = 0;
             // keys behind the row's own, queries before it, or rows behind the sequence
             const bool masked = kRole == kQueries ? first + kStep > tile.first : first < tile.first + kTile || first + kStep > tile.end;
-            ok = wait(x_done + 8 * t, i / 2 & 1);
+            ok = wait(x_done + 8 * (i & 1), i / 2 & 1);
             // what the copies brought is read here too
             if (ok && (kRole == kKeys || masked)) ok = wait(full + 8 * stage, i / kStages & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[2][32], y[2][32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                tmem_load32(x_at + 32 * q, x[q]);
-                tmem_load32(x_at + 128 + 32 * q, y[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                tmem_wait(x[q]);
-                tmem_wait(y[q]);
-            }
+            const uint32_t x_at = tmem + lanes + (i & 1) * kStep + 32 * t;
+            uint32_t x[32], y[32];
+            tmem_load32(x_at, x);
+            tmem_load32(x_at + 128, y);
+            tmem_wait(x);
+            tmem_wait(y);
             const RowBlock* const rb = reinterpret_cast<const RowBlock*>(base_ptr + (row_stages - base)) + stage;
-            uint32_t pw[32], dw[32];
+            uint32_t pw[16], dw[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    F2 l[2] = {my_lse2, my_lse2}, d[2] = {my_delta2, my_delta2};
-                    if (kRole == kKeys) {
-                        const float4 a = *reinterpret_cast<const float4*>(&rb->lse[32 * q + k]), b = *reinterpret_cast<const float4*>(&rb->delta[32 * q + k]);
-                        l[0] = f2(-a.x, -a.y), l[1] = f2(-a.z, -a.w), d[0] = f2(-b.x, -b.y), d[1] = f2(-b.z, -b.w);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int e = k + 2 * h;
-                        float a, b, u, w;
-                        split2(fma2(f2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), c2, l[h]), a, b);
-                        a = exp2_approx(a), b = exp2_approx(b);
-                        split2(mul2(f2(a, b), add2(f2(__uint_as_float(y[q][e]), __uint_as_float(y[q][e + 1])), d[h])), u, w);
-                        if (masked) {                                          // whatever was multiplied
-                            const int64_t other = first + 32 * q + e;
-                            const bool off0 = kRole == kQueries ? other > row : other < row || other >= tile.end;
-                            const bool off1 = kRole == kQueries ? other + 1 > row : other + 1 < row || other + 1 >= tile.end;
-                            if (off0) a = u = 0.0f;
-                            if (off1) b = w = 0.0f;
-                        }
-                        pw[(32 * q + e) / 2] = pack_bf16(a, b);
-                        dw[(32 * q + e) / 2] = pack_bf16(u, w);
-                    }
+            for (int k = 0; k < 32; k += 4) {
+                F2 l[2] = {my_lse2, my_lse2}, d[2] = {my_delta2, my_delta2};
+                if (kRole == kKeys) {
+                    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&rb->lse[32 * t + k]), b = *reinterpret_cast<const ulonglong2*>(&rb->delta[32 * t + k]);
+                    l[0].x = a.x, l[1].x = a.y, d[0].x = b.x, d[1].x = b.y;
                 }
-            if (kRole == kKeys) tmem_store32(x_at, pw);
-            tmem_store32(x_at + 128, dw);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = k + 2 * h;
+                    float a, b, u, w;
+                    split2(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l[h]), a, b);
+                    a = exp2_approx(a), b = exp2_approx(b);
+                    split2(mul2(f2(a, b), add2(f2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), d[h])), u, w);
+                    if (masked) {                                              // whatever was multiplied
+                        const int64_t other = first + 32 * t + e;
+                        const bool off0 = kRole == kQueries ? other > row : other < row || other >= tile.end;
+                        const bool off1 = kRole == kQueries ? other + 1 > row : other + 1 < row || other + 1 >= tile.end;
+                        if (off0) a = u = 0.0f;
+                        if (off1) b = w = 0.0f;
+                    }
+                    pw[e / 2] = pack_bf16(a, b);
+                    dw[e / 2] = pack_bf16(u, w);
+                }
+            }
+            if (kRole == kKeys) tmem_store16(x_at, pw);
+            tmem_store16(x_at + 128, dw);
             tmem_store_wait();
             if (masked && in < kStep) {      // rows of masked places are not multiplied, not even by 0
                 char* const b = base_ptr + (stages - base) + stage * 2 * kStepBytes;
-                clear_non_finite<kStep>(b, p.dim, in);
-                if (kRole == kKeys && clear_non_finite<kStep>(b + kStepBytes, p.dim, in)) found = 1;
+                if (t == 0) clear_non_finite<kStep>(b, p.dim, in);
+                else if (kRole == kKeys && clear_non_finite<kStep>(b + kStepBytes, p.dim, in)) found = 1;
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !(blockIdx.x == 0 && p.stall == kStallSoftmax)) mbar_arrive(ready + 8 * t);
+            if (lane == 0 && !(blockIdx.x == 0 && p.stall == kStallSoftmax)) mbar_arrive(ready + 8 * (i & 1));
         }
         ok = ok && wait(sums_done, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        // the first four warps write dq, or dk; the others half of dq, or dv
+        // the first four warps take dq's first half or dk out, the others its second half or dv
         const bool live = row < tile.end;
-        const bool had = kRole == kKeys && t == 1 && *static_cast<volatile int*>(&found) != 0;
         const HeadRows& o = kRole == kKeys && t == 1 ? p.out1 : p.out0;
         uint16_t* const to = static_cast<uint16_t*>(o.p) + head * o.head + row * o.row;
         const float f = !ok ? __builtin_nanf("") : kRole == kKeys && t == 1 ? 1.0f : p.scale;
@@ -316,26 +332,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             uint32_t r[32];
             tmem_load32(sum_at + q, r);
             tmem_wait(r);
-            if (live) {
-                float z[32];
+            float z[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(r[k]) * f;
-                if (had)      // masked blocks of each head: the tile's own rows and the sequence's last block
-                    for (int g = 0; g < p.group; ++g) {
-                        const uint16_t* const d_out = p.d_out + (int64_t)(head * p.group + g) * p.hsdo;
-                        const int64_t own = min(tile.first + kTile, tile.end);
-                        const int64_t last = tile.first + (tile.end - tile.first) / kStep * kStep;   // first row of a block that is not whole
-                        add_non_finite(z, d_out, p.lddo, row, own, q, p.dim);
-                        add_non_finite(z, d_out, p.lddo, max(own, last), tile.end, q, p.dim);
-                    }
+            for (int k = 0; k < 32; ++k) z[k] = blocks ? __uint_as_float(r[k]) * f : 0.0f;
+            if (splits > 1) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                    *part_at(base_ptr, t, q + k, in) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
+            } else if (live) {
+                if (kRole == kKeys && t == 1 && *static_cast<volatile int*>(&found)) add_cleared(p, tile, head, row, q, z);
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
-                    if (q + k < p.dim)
-                        *reinterpret_cast<uint4*>(to + q + k) = make_uint4(pack_bf16(z[k], z[k + 1]), pack_bf16(z[k + 2], z[k + 3]),
-                                                                           pack_bf16(z[k + 4], z[k + 5]), pack_bf16(z[k + 6], z[k + 7]));
+                    if (q + k < p.dim) store8(to + q + k, z[k], z[k + 1], z[k + 2], z[k + 3], z[k + 4], z[k + 5], z[k + 6], z[k + 7]);
             }
             __syncwarp();
         }
+    }
+    if (kRole == kKeys && splits > 1) {
+        // the cluster's sums, in the order of its CTAs; each finishes its share of the tile's rows
+        __syncwarp();
+        cluster_sync();
+        const int share = kTile / splits, vecs = p.dim / 8;
+        bool had = false, late = false;
+        for (int r = 0; r < splits; ++r) {
+            had |= load_cluster(cluster_addr(smem_u32(&found), r)) != 0;
+            late |= load_cluster(cluster_addr(smem_u32(&gave_up), r)) != 0;
+        }
+        for (int i = threadIdx.x; i < 2 * vecs * share; i += kAttnThreads) {
+            const int in = rank * share + i % share, which = i / share % 2, c = i / share / 2 * 8;
+            float z[8] = {};
+            for (int r = 0; r < splits; ++r) {
+                const uint32_t from = cluster_addr(smem_u32(part_at(base_ptr, which, c, in)), r);
+                const float4 a = load_cluster_f4(from), b = load_cluster_f4(from + kTile * 16);
+                z[0] += a.x, z[1] += a.y, z[2] += a.z, z[3] += a.w, z[4] += b.x, z[5] += b.y, z[6] += b.z, z[7] += b.w;
+            }
+            const int64_t row = tile.first + in;
+            if (row >= tile.end) continue;
+            if (late) z[0] = z[1] = z[2] = z[3] = z[4] = z[5] = z[6] = z[7] = __builtin_nanf("");
+            if (which && had) add_cleared(p, tile, head, row, c, z);
+            const HeadRows& o = which ? p.out1 : p.out0;
+            store8(static_cast<uint16_t*>(o.p) + head * o.head + row * o.row + c, z[0], z[1], z[2], z[3], z[4], z[5], z[6], z[7]);
+        }
+        __syncwarp();
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
@@ -361,6 +400,14 @@ int injected_stall(int role) {
     return fault_injected(names[role][0]) ? kStallCopy : fault_injected(names[role][1]) ? kStallSoftmax : 0;
 }
 
+// CTAs that share a tile of keys: more while there are fewer than four units to an SM.
+int key_splits(const AttnCall& c) {
+    const int64_t units = tile_slots(c.seq, kTile) * c.kv_heads;
+    int splits = 1;
+    while (splits < 8 && units * splits < 4 * sm_count()) splits *= 2;
+    return splits;
+}
+
 template <int kRole>
 int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s) {
     const bool queries = kRole == kQueries;
@@ -377,13 +424,14 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
     a.seq = c.seq;
     a.slots = tile_slots(c.seq, kTile), a.row_slots = tile_slots(c.seq, kStep);
     a.heads = (int)c.heads, a.kv_heads = (int)c.kv_heads, a.group = (int)(c.heads / c.kv_heads), a.dim = (int)c.dim;
+    a.splits = queries ? 1 : key_splits(c);
     a.scale = c.scale;
     a.rows = static_cast<const RowBlock*>(c.workspace);
     a.out0 = queries ? c.dq : c.dk, a.out1 = c.dv;
     a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
     a.stall = faults_injected() ? injected_stall(kRole) : 0;
     a.wait_ns = a.stall ? kWaitNs / 40 : kWaitNs;
-    return check_cuda(launch_after(k_attn_backward<kRole>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads)), kAttnThreads, kSmem, 1, s,
+    return check_cuda(launch_after(k_attn_backward<kRole>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads) * a.splits), kAttnThreads, kSmem, a.splits, s,
                                    map[0], map[1], map[2], map[3], a),
                       "attention backward launch");
 }
