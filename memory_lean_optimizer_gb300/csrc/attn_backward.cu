@@ -20,10 +20,11 @@ namespace lmo {
 namespace {
 
 constexpr int kTile = 128, kStep = 64;           // rows of a CTA's tile and of a streamed block
-constexpr int kAttnThreads = 384;                // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory; 4-7 and 8-11: every other block
+constexpr int kAttnThreads = 384;                // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory; 4-11: p and dS
 constexpr uint32_t kTileBytes = kTile * 256, kStepBytes = kStep * 256;
-constexpr int kStages = 4;
-constexpr size_t kSmem = 2 * kTileBytes + kStages * (2 * kStepBytes + kStep * 8) + 1024;
+// Stages of a pair of blocks; a tile of queries is in tensor memory and leaves its place to more of them.
+__host__ __device__ constexpr int stages_of(int role) { return role == 0 ? 6 : 4; }
+constexpr size_t kSmem = 6 * 2 * kStepBytes + 4 * kStep * 8 + 1024;
 
 // The rows' -lse (times log2 e) and -delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
 // of 64 (find_tile), `slots` a head; rows behind a sequence's end have -inf (p is 0) and 0.
@@ -89,6 +90,7 @@ struct BackwardArgs {
     int32_t splits;                     // kKeys: CTAs (a cluster) that share a tile's blocks
     float scale;
     const RowBlock* rows;
+    HeadRows a0, a1;                    // kQueries: Q, dO
     HeadRows out0, out1;                // dq; or dk, dv
     const uint16_t* d_out;              // kKeys: for what is taken out of masked blocks
     int64_t lddo, hsdo;
@@ -117,10 +119,11 @@ __device__ __forceinline__ float4* part_at(char* base, int which, int c, int row
 }
 
 // maps: the tile's operands (a0, a1), the streamed ones (b0, b1): Q, dO, K, V for queries, K, V, Q, dO for keys
-template <int kRole>
+template <int kRole, int kSteps>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
                                                                    const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
                                                                    const BackwardArgs p) {
+    constexpr int kStages = stages_of(kRole);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[1 + 2 * kStages + 4 + 2];
     __shared__ uint32_t tmem_base;
@@ -149,13 +152,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
-    const uint32_t stages = base + 2 * kTileBytes;                       // stage: B0, B1
+    const uint32_t stages = base + (kRole == kKeys ? 2 * kTileBytes : 0);   // stage: B0, B1
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
     const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
                    sums_done = ready + 16, drained = sums_done + 8;
     if (threadIdx.x == 0) {
         gave_up = found = copied = 0;
-        mbar_init(a_full, 1);
+        mbar_init(a_full, kRole == kKeys ? 1 : 8);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
@@ -188,9 +191,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         if (warp == 0 && elect_lane()) {
             const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const uint32_t boxes = p.dim > 64 ? 2 : 1;
-            mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
-            load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, a_full);
-            load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, a_full);
+            if (kRole == kKeys) {
+                mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
+                load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, a_full);
+                load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, a_full);
+            }
             int issued = 0, in = first_block % per_head;
             int of = kRole == kQueries ? head / p.group : head * p.group + first_block / per_head;     // head of the streamed operands
             const int64_t row_slot = kRole == kKeys ? (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep : 0;
@@ -213,18 +218,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             for (int i = max(0, blocks - kStages); ok && i < blocks; ++i) ok = wait(empty + 8 * (i % kStages), i / kStages & 1);
             copied = issued;
         } else if (warp == 1 && elect_lane()) {
-            const int steps = (p.dim + 15) / 16;                               // of 16 elements along the head
-            const uint32_t desc_x = mma_desc(128, kStep, false, false), desc_sum = mma_desc(128, steps * 16, false, true);
+            constexpr uint32_t desc_x = mma_desc(128, kStep, false, false), desc_sum = mma_desc(128, kSteps * 16, false, true);
+            constexpr uint32_t up = desc_upper(1024);
+            const uint32_t a_lo = desc_lower(base, 8192), b_lo = desc_lower(stages, kStep * 128);
             bool ok = wait(a_full, 0);
+            tc_fence_after();
             auto scores = [&](int i) {
                 ok = wait(full + 8 * (i % kStages), i / kStages & 1);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t b = stages + i % kStages * 2 * kStepBytes, d = tmem + (i & 1) * kStep;
+                const uint32_t b = b_lo + i % kStages * (2 * kStepBytes >> 4), d = tmem + (i & 1) * kStep;
+#pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    for (int j = 0; j < steps; ++j)
-                        mma_bf16<1>(d + h * 128, operand_desc(base + h * kTileBytes + (j >> 2) * (kTile * 128) + (j & 3) * 32, 8192, 1024),
-                                    operand_desc(b + h * kStepBytes + (j >> 2) * (kStep * 128) + (j & 3) * 32, 8192, 1024), desc_x, j > 0);
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j)
+                        if (kRole == kQueries)
+                            mma_ts(d + h * 128, tmem + 384 + h * 64 + j * 8, b + h * (kStepBytes >> 4) + (j >> 2) * (kStep * 8) + (j & 3) * 2, up, desc_x, j == 0);
+                        else
+                            mma_ss(d + h * 128, a_lo + h * (kTileBytes >> 4) + (j >> 2) * (kTile * 8) + (j & 3) * 2,
+                                   b + h * (kStepBytes >> 4) + (j >> 2) * (kStep * 8) + (j & 3) * 2, up, desc_x, j == 0);
                 mma_commit<1>(x_done + 8 * (i & 1));
             };
             if (ok && blocks) scores(0);
@@ -233,12 +245,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (ok) ok = wait(ready + 8 * (i & 1), i / 2 & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b = stages + i % kStages * 2 * kStepBytes, a = tmem + (i & 1) * kStep;
-                if (kRole == kKeys)
+                const uint32_t b = b_lo + i % kStages * (2 * kStepBytes >> 4), a = tmem + (i & 1) * kStep;
+                if (kRole == kKeys) {
+#pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)     // dv += p' dO
-                        mma_bf16_ta(tmem + 384, a + (j >> 1) * 32 + (j & 1) * 8, operand_desc(b + kStepBytes + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                        mma_ts(tmem + 384, a + (j >> 1) * 32 + (j & 1) * 8, b + (kStepBytes >> 4) + j * 128, up, desc_sum, i == 0 && j == 0);
+                }
+#pragma unroll
                 for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
-                    mma_bf16_ta(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, operand_desc(b + j * 2048, kStep * 128, 1024), desc_sum, i > 0 || j > 0);
+                    mma_ts(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, i == 0 && j == 0);
                 mma_commit<1>(empty + 8 * (i % kStages));
             }
             if (ok) mma_commit<1>(sums_done);
@@ -254,6 +269,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         const F2 c2 = f2(c, c);
         float my_lse = 0.0f, my_delta = 0.0f;
         if (kRole == kQueries) {
+            // Q (four warps) and dO (the others) into tensor memory, two elements a column
+            const HeadRows& from = t ? p.a1 : p.a0;
+            const uint16_t* const x = static_cast<const uint16_t*>(from.p) + head * from.head + row * from.row;
+#pragma unroll 1
+            for (int h = 0; h < (p.dim > 64 ? 2 : 1); ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const bool there = row < tile.end && 64 * h + 2 * k < p.dim;
+                    const uint4 v = there ? *reinterpret_cast<const uint4*>(x + 64 * h + 2 * k) : make_uint4(0, 0, 0, 0);
+                    w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
+                }
+                tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, w);
+            }
+            tmem_store_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(a_full);
             // tiles of 128 start at a block of 64
             const RowBlock& b = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
             if (row < tile.end) my_lse = b.lse[in % kStep], my_delta = b.delta[in % kStep];
@@ -321,12 +354,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         ok = ok && wait(sums_done, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        // the first four warps take dq's first half or dk out, the others its second half or dv
+        // the first four warps take half of dq or dk out, the others the other half or dv
         const bool live = row < tile.end;
-        const HeadRows& o = kRole == kKeys && t == 1 ? p.out1 : p.out0;
+        const int which = kRole == kKeys ? t : 0;
+        const HeadRows& o = which ? p.out1 : p.out0;
         uint16_t* const to = static_cast<uint16_t*>(o.p) + head * o.head + row * o.row;
-        const float f = !ok ? __builtin_nanf("") : kRole == kKeys && t == 1 ? 1.0f : p.scale;
-        const uint32_t sum_at = tmem + lanes + 256 + (kRole == kKeys ? 128 * t : 0);
+        const float f = !ok ? __builtin_nanf("") : which ? 1.0f : p.scale;
+        const uint32_t sum_at = tmem + lanes + 256 + 128 * which;
 #pragma unroll 1
         for (int q = kRole == kQueries ? 32 * t : 0; q < p.dim; q += kRole == kQueries ? 64 : 32) {
             uint32_t r[32];
@@ -338,9 +372,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             if (splits > 1) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
-                    *part_at(base_ptr, t, q + k, in) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
+                    *part_at(base_ptr, which, q + k, in) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
             } else if (live) {
-                if (kRole == kKeys && t == 1 && *static_cast<volatile int*>(&found)) add_cleared(p, tile, head, row, q, z);
+                if (which && *static_cast<volatile int*>(&found)) add_cleared(p, tile, head, row, q, z);
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
                     if (q + k < p.dim) store8(to + q + k, z[k], z[k + 1], z[k + 2], z[k + 3], z[k + 4], z[k + 5], z[k + 6], z[k + 7]);
@@ -386,7 +420,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         if (warp == 0 && elect_lane()) {
             const int n = copied;
-            mbar_drain(a_full, 0);
+            if (kRole == kKeys) mbar_drain(a_full, 0);
             for (int i = max(0, n - kStages); i < n; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1);
         }
         __syncthreads();
@@ -408,7 +442,7 @@ int key_splits(const AttnCall& c) {
     return splits;
 }
 
-template <int kRole>
+template <int kRole, int kSteps>
 int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s) {
     const bool queries = kRole == kQueries;
     CUtensorMap map[4];
@@ -418,7 +452,7 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
         if (rc) return rc;
     }
     static std::atomic<uint64_t> allowed{0};
-    const int rc = allow_smem(k_attn_backward<kRole>, (int)kSmem, allowed);
+    const int rc = allow_smem(k_attn_backward<kRole, kSteps>, (int)kSmem, allowed);
     if (rc) return rc;
     BackwardArgs a{};
     a.seq = c.seq;
@@ -427,11 +461,12 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
     a.splits = queries ? 1 : key_splits(c);
     a.scale = c.scale;
     a.rows = static_cast<const RowBlock*>(c.workspace);
+    a.a0 = operands[0], a.a1 = operands[1];
     a.out0 = queries ? c.dq : c.dk, a.out1 = c.dv;
     a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
     a.stall = faults_injected() ? injected_stall(kRole) : 0;
     a.wait_ns = a.stall ? kWaitNs / 40 : kWaitNs;
-    return check_cuda(launch_after(k_attn_backward<kRole>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads) * a.splits), kAttnThreads, kSmem, a.splits, s,
+    return check_cuda(launch_after(k_attn_backward<kRole, kSteps>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads) * a.splits), kAttnThreads, kSmem, a.splits, s,
                                    map[0], map[1], map[2], map[3], a),
                       "attention backward launch");
 }
@@ -450,8 +485,11 @@ int launch_attn_backward(const AttnCall& c, cudaStream_t s) {
     a.lse = c.lse;
     a.rows = static_cast<RowBlock*>(c.workspace);
     int rc = check_cuda(launch_after(k_attn_rows, (unsigned)(a.slots * c.heads), 256, 0, 1, s, a), "attention backward launch");
-    if (!rc && c.dk.p) rc = launch_role<kKeys>(c, {c.k, c.v, c.q, c.d_out}, s);
-    if (!rc && c.dq.p) rc = launch_role<kQueries>(c, {c.q, c.d_out, c.k, c.v}, s);
+    // heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and
+    // tests of the number of steps between the products cost more than products
+    const HeadRows keys[4] = {c.k, c.v, c.q, c.d_out}, queries[4] = {c.q, c.d_out, c.k, c.v};
+    if (!rc && c.dk.p) rc = c.dim <= 64 ? launch_role<kKeys, 4>(c, keys, s) : launch_role<kKeys, 8>(c, keys, s);
+    if (!rc && c.dq.p) rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);
     return rc;
 }
 

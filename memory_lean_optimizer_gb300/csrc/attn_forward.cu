@@ -40,6 +40,7 @@ struct ForwardArgs {
 };
 enum Stall { kStallCopy = 1, kStallSoftmax = 2 };
 
+template <int kSteps>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_constant__ CUtensorMap map_q,
                                                                const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v, const ForwardArgs p) {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
     const int blocks = max(n0, n1);
 
     if (warp < 4) {
-        regs_down<40>();
+        regs_down<72>();
         if (warp == 0 && elect_lane()) {
             const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const int kv = head / p.group;
@@ -130,14 +131,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                 ok = wait(k_empty + 8 * (j % kStages), j / kStages & 1) && wait(v_empty + 8 * (j % kStages), j / kStages & 1);
             copied[0] = copied_k, copied[1] = copied_v;
         } else if (warp == 1 && elect_lane()) {
-            const int steps = (p.dim + 15) / 16;                                // of 16 elements along the head
-            const uint32_t desc_s = mma_desc(128, kTile, false, false), desc_o = mma_desc(128, steps * 16, false, true);
+            constexpr uint32_t desc_s = mma_desc(128, kTile, false, false), desc_o = mma_desc(128, kSteps * 16, false, true);
             bool ok = true;
+            constexpr uint32_t up = desc_upper(1024);
+            const uint32_t q_lo = desc_lower(q_tile, 8192), k_lo = desc_lower(k_tile, 8192), v_lo = desc_lower(v_tile, kTile * 128);
             auto scores = [&](int t, int j) {                                   // S_t = Q_t K_j'
-                const uint32_t a = q_tile + t * kTileBytes, b = k_tile + j % kStages * kTileBytes;
-                for (int i = 0; i < steps; ++i) {
-                    const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
-                    mma_bf16<1>(tmem + t * 128, operand_desc(a + off, 8192, 1024), operand_desc(b + off, 8192, 1024), desc_s, i > 0);
+                const uint32_t a = q_lo + t * (kTileBytes >> 4), b = k_lo + j % kStages * (kTileBytes >> 4);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const uint32_t off = (i >> 2) * (kTile * 8) + (i & 3) * 2;
+                    mma_ss(tmem + t * 128, a + off, b + off, up, desc_s, i == 0);
                 }
                 mma_commit<1>(s_done + 8 * t);
             };
@@ -159,9 +162,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                     ok = wait(p_ready + 8 * t, j & 1);
                     if (!ok) break;
                     tc_fence_after();
+#pragma unroll
                     for (int i = 0; i < kTile / 16; ++i)
-                        mma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
-                                    operand_desc(v_tile + stage * kTileBytes + i * 2048, kTile * 128, 1024), desc_o, j > 0 || i > 0);
+                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, v_lo + stage * (kTileBytes >> 4) + i * 128, up, desc_o, i == 0 && j == 0);
                     mma_commit<1>(o_done + 8 * t);
                     if (j + 1 < n) scores(t, j + 1);      // into the columns of P, behind the product that reads it
                 }
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
         }
         __syncwarp();
     } else {
-        regs_up<232>();
+        regs_up<216>();
         const int t = (warp >> 2) - 1, n = t ? n1 : n0;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
@@ -317,13 +320,14 @@ int injected_stall() { return fault_injected("stall_attention_copy") ? kStallCop
 
 }  // namespace
 
-int launch_attn_forward(const AttnCall& c, cudaStream_t s) {
+template <int kSteps>
+static int launch_steps(const AttnCall& c, cudaStream_t s) {
     CUtensorMap q, k, v;
     int rc = make_head_map(&q, c.q.p, c.seq.rows, c.heads, c.dim, c.q.row, c.q.head, kTile);
     if (!rc) rc = make_head_map(&k, c.k.p, c.seq.rows, c.kv_heads, c.dim, c.k.row, c.k.head, kTile);
     if (!rc) rc = make_head_map(&v, c.v.p, c.seq.rows, c.kv_heads, c.dim, c.v.row, c.v.head, kTile);
     static std::atomic<uint64_t> allowed{0};
-    if (!rc) rc = allow_smem(k_attn_forward, (int)kSmem, allowed);
+    if (!rc) rc = allow_smem(k_attn_forward<kSteps>, (int)kSmem, allowed);
     if (rc) return rc;
     ForwardArgs a{};
     a.seq = c.seq;
@@ -335,7 +339,11 @@ int launch_attn_forward(const AttnCall& c, cudaStream_t s) {
     a.v = static_cast<const uint16_t*>(c.v.p), a.ldv = c.v.row, a.hsv = c.v.head;
     a.stall = faults_injected() ? injected_stall() : 0;
     a.wait_ns = a.stall ? kWaitNs / 40 : kWaitNs;
-    return check_cuda(launch_after(k_attn_forward, (unsigned)(a.slots * c.heads), kAttnThreads, kSmem, 1, s, q, k, v, a), "attention launch");
+    return check_cuda(launch_after(k_attn_forward<kSteps>, (unsigned)(a.slots * c.heads), kAttnThreads, kSmem, 1, s, q, k, v, a), "attention launch");
 }
+
+// Heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and tests of the
+// number of steps between the products cost more than products.
+int launch_attn_forward(const AttnCall& c, cudaStream_t s) { return c.dim <= 64 ? launch_steps<4>(c, s) : launch_steps<8>(c, s); }
 
 }  // namespace lmo

@@ -94,8 +94,7 @@ __device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
 // false: it did not complete.
 constexpr uint64_t kWaitNs = 4000000000ull;
 template <int kCta>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
-    if (mbar_try(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
     const uint64_t t0 = global_ns();
     for (;;) {
 #pragma unroll 1
@@ -108,6 +107,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             return false;
         }
     }
+}
+// Reading the timer takes as long as many a wait lasts: it begins after a while.
+template <int kCta>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try(bar, parity)) return true;
+    return mbar_wait_long<kCta>(bar, parity, gave_up, ns);
 }
 // The same after a wait has given up, for what is in flight.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
@@ -197,11 +204,21 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
             "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
             : "memory");
 }
-// The same with A in tensor memory: a lane is a row, a column two bf16 values next to each other along K.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// Products of a loop: descriptors whose lower halves alone move (by bytes / 16), the upper half that of operand_desc with
+// this sbo; `first`: the accumulator is written, not added to.
+__host__ __device__ constexpr uint32_t desc_upper(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lower(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc, bool first) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
-        "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\tsetp.eq.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)first), "r"(upper)
+        : "memory");
+}
+// The same with A in tensor memory: a lane is a row, a column two bf16 values next to each other along K.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc, bool first) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\tsetp.eq.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)first), "r"(upper)
         : "memory");
 }
 // Arrives on `bar` -- of both CTAs for kCta = 2 -- when the thread's MMAs so far are done.
