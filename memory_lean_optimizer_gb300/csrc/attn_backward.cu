@@ -12,7 +12,7 @@
 // memory, of the sums' products (with B0 and B1 read along their rows).  For keys X and Y are the transposed
 // scores: nothing is ever transposed through shared memory.  Blocks of 64 so that two pairs and the two sums fit in the 512
 // columns; while four warps work on one pair the tensor cores fill the other.
-#include <cstdio>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -314,31 +314,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             tmem_wait(y);
             const RowBlock* const rb = reinterpret_cast<const RowBlock*>(base_ptr + (row_stages - base)) + stage;
             uint32_t pw[16], dw[16];
+            // the columns that the row sees: from .. to - 1 (tests of them only where some are masked: they cost as much as the rest)
+            const int from = kRole == kQueries ? 0 : (int)max(row - first, (int64_t)0) - 32 * t;
+            const int to = (int)min((kRole == kQueries ? row + 1 : tile.end) - first, (int64_t)kStep) - 32 * t;
+            auto weights = [&](auto some) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                F2 l[2] = {my_lse2, my_lse2}, d[2] = {my_delta2, my_delta2};
-                if (kRole == kKeys) {
-                    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&rb->lse[32 * t + k]), b = *reinterpret_cast<const ulonglong2*>(&rb->delta[32 * t + k]);
-                    l[0].x = a.x, l[1].x = a.y, d[0].x = b.x, d[1].x = b.y;
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = k + 2 * h;
-                    float a, b, u, w;
-                    split2(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l[h]), a, b);
-                    a = exp2_approx(a), b = exp2_approx(b);
-                    split2(mul2(f2(a, b), add2(f2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), d[h])), u, w);
-                    if (masked) {                                              // whatever was multiplied
-                        const int64_t other = first + 32 * t + e;
-                        const bool off0 = kRole == kQueries ? other > row : other < row || other >= tile.end;
-                        const bool off1 = kRole == kQueries ? other + 1 > row : other + 1 < row || other + 1 >= tile.end;
-                        if (off0) a = u = 0.0f;
-                        if (off1) b = w = 0.0f;
+                for (int k = 0; k < 32; k += 4) {
+                    F2 l[2] = {my_lse2, my_lse2}, d[2] = {my_delta2, my_delta2};
+                    if (kRole == kKeys) {
+                        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(&rb->lse[32 * t + k]), b = *reinterpret_cast<const ulonglong2*>(&rb->delta[32 * t + k]);
+                        l[0].x = a.x, l[1].x = a.y, d[0].x = b.x, d[1].x = b.y;
                     }
-                    pw[e / 2] = pack_bf16(a, b);
-                    dw[e / 2] = pack_bf16(u, w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = k + 2 * h;
+                        float a, b, u, w;
+                        split2(fma2(f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, l[h]), a, b);
+                        a = exp2_approx(a), b = exp2_approx(b);
+                        split2(mul2(f2(a, b), add2(f2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), d[h])), u, w);
+                        if constexpr (decltype(some)::value) {                 // 0 whatever was multiplied
+                            if (e < from || e >= to) a = u = 0.0f;
+                            if (e + 1 < from || e + 1 >= to) b = w = 0.0f;
+                        }
+                        pw[e / 2] = pack_bf16(a, b);
+                        dw[e / 2] = pack_bf16(u, w);
+                    }
                 }
-            }
+            };
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
             if (kRole == kKeys) tmem_store16(x_at, pw);
             tmem_store16(x_at + 128, dw);
             tmem_store_wait();

@@ -11,8 +11,6 @@
 //
 // m follows the running maximum only when that has grown by 8 (p then stays below 2^8, far from any limit of fp32 or
 // bf16): the outputs in tensor memory are rescaled a few times a row, not once a block.
-#include <cstdio>
-
 #include "attn.cuh"
 
 namespace lmo {
