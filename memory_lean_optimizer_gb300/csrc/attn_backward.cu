@@ -200,9 +200,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             int of = kRole == kQueries ? head / p.group : head * p.group + first_block / per_head;     // head of the streamed operands
             const int64_t row_slot = kRole == kKeys ? (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep : 0;
             bool ok = true;
+            uint32_t stage = 0, phase = 0;
             for (int i = 0; ok && i < blocks; ++i) {
-                const int stage = i % kStages;
-                ok = issued != stop && wait(empty + 8 * stage, (i / kStages & 1) ^ 1u);
+                ok = issued != stop && wait(empty + 8 * stage, phase ^ 1u);
                 if (!ok) break;
                 const uint32_t bar = full + 8 * stage, b = stages + stage * 2 * kStepBytes;
                 mbar_expect_tx(bar, 2 * boxes * kStep * 128 + (kRole == kKeys ? (uint32_t)sizeof(RowBlock) : 0u));
@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (kRole == kKeys)
                     bulk_load(row_stages + stage * (uint32_t)sizeof(RowBlock), p.rows + of * p.row_slots + row_slot + in, sizeof(RowBlock), bar);
                 ++issued;
+                if (++stage == kStages) stage = 0, phase ^= 1u;
                 if (++in == per_head) in = 0, ++of;
             }
             // the last stages come back before the CTA ends: nothing arrives on its barriers after that
@@ -223,11 +224,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             const uint32_t a_lo = desc_lower(base, 8192), b_lo = desc_lower(stages, kStep * 128);
             bool ok = wait(a_full, 0);
             tc_fence_after();
+            uint32_t next = 0, parity = 0, stage = 0;       // of the block whose scores, and whose sums, come next
             auto scores = [&](int i) {
-                ok = wait(full + 8 * (i % kStages), i / kStages & 1);
+                ok = wait(full + 8 * next, parity);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t b = b_lo + i % kStages * (2 * kStepBytes >> 4), d = tmem + (i & 1) * kStep;
+                const uint32_t b = b_lo + next * (2 * kStepBytes >> 4), d = tmem + (i & 1) * kStep;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -238,6 +240,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                             mma_ss(d + h * 128, a_lo + h * (kTileBytes >> 4) + (j >> 2) * (kTile * 8) + (j & 3) * 2,
                                    b + h * (kStepBytes >> 4) + (j >> 2) * (kStep * 8) + (j & 3) * 2, up, desc_x, j == 0);
                 mma_commit<1>(x_done + 8 * (i & 1));
+                if (++next == kStages) next = 0, parity ^= 1u;
             };
             if (ok && blocks) scores(0);
             for (int i = 0; ok && i < blocks; ++i) {
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (ok) ok = wait(ready + 8 * (i & 1), i / 2 & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b = b_lo + i % kStages * (2 * kStepBytes >> 4), a = tmem + (i & 1) * kStep;
+                const uint32_t b = b_lo + stage * (2 * kStepBytes >> 4), a = tmem + (i & 1) * kStep;
                 if (kRole == kKeys) {
 #pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)     // dv += p' dO
@@ -254,7 +257,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
 #pragma unroll
                 for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
                     mma_ts(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, i == 0 && j == 0);
-                mma_commit<1>(empty + 8 * (i % kStages));
+                mma_commit<1>(empty + 8 * stage);
+                if (++stage == kStages) stage = 0;
             }
             if (ok) mma_commit<1>(sums_done);
         }
@@ -294,15 +298,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         const F2 my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
         int at = first_block % per_head;                                       // the block's place in its head
         bool ok = true;
-        for (int i = 0; i < blocks; ++i) {
-            const int stage = i % kStages;
+        uint32_t stage = 0, phase = 0;
+        for (int i = 0; i < blocks; ++i, stage = stage == kStages - 1 ? 0 : stage + 1, phase ^= stage == 0 ? 1u : 0u) {
             const int64_t first = stream_first + (int64_t)at * kStep;          // the block's first row
             if (++at == per_head) at = 0;
             // keys behind the row's own, queries before it, or rows behind the sequence
             const bool masked = kRole == kQueries ? first + kStep > tile.first : first < tile.first + kTile || first + kStep > tile.end;
             ok = wait(x_done + 8 * (i & 1), i / 2 & 1);
             // what the copies brought is read here too
-            if (ok && (kRole == kKeys || masked)) ok = wait(full + 8 * stage, i / kStages & 1);
+            if (ok && (kRole == kKeys || masked)) ok = wait(full + 8 * stage, phase);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
