@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import functools
 import math
-from dataclasses import dataclass
 from fractions import Fraction
 
 import torch
@@ -25,7 +24,7 @@ ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.
 
 
 def _on_gpu(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU")
 
 
@@ -38,55 +37,72 @@ def _heads(t: torch.Tensor, name: str) -> torch.Tensor:
 
 
 # ----------------------------------------------------------------------------------------- attention
-def _attn_heads(t: torch.Tensor, name: str) -> torch.Tensor:
-    """t [tokens, heads, dim], bf16, as the kernels read it: heads on 16 bytes, rows and heads apart; t itself, or a copy."""
-    if t.dtype != torch.bfloat16:
+def _attn_side(t: torch.Tensor, name: str):
+    """t [tokens, heads, dim], bf16, as the kernels read it: heads on 16 bytes, rows and heads apart; t itself, or a copy.  (t,
+    its shape, its pointer and strides)"""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
-    t = _heads(t, name)
-    rows, heads, dim = t.shape
-    row, head = t.stride(0), t.stride(1)
-    if (t.data_ptr() % 16 or rows > 1 and (row % 8 or row < dim) or heads > 1 and (head % 8 or head < dim) or
-            dim > 1 and t.stride(2) != 1):
+    _on_gpu(t, name)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
+    shape = t.shape
+    rows, heads, dim = shape
+    row, head, one = t.stride()
+    at = t.data_ptr()
+    if (at % 16 or rows > 1 and (row % 8 or row < dim) or heads > 1 and (head % 8 or head < dim) or dim > 1 and one != 1):
         t = t.clone(memory_format=torch.contiguous_format)
-    return t
+        at, row, head = t.data_ptr(), heads * dim, dim
+    return t, shape, (at, row, head)
 
 
-def _at(t: torch.Tensor | None):
-    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(0), t.stride(1))
+def _new_side(shape, like: torch.Tensor):
+    """A new bf16 tensor of [tokens, heads, dim], and its pointer and strides."""
+    t = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
+_NO_SIDE = (None, 0, 0)
+
+
+def _flat(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [batch, length, heads, dim], not {list(t.shape)}")
+    return t.reshape(-1, *t.shape[2:])
 
 
 def _attn_args(q, k, v, cu_seqlens, scale):
-    """(q, k, v) as [tokens, heads, dim], the borders' pointer, sequences, rows, heads, kv_heads, dim, scale."""
-    batch = None
+    """(tensors that the call reads, shape of q, shape of k, sides of q, k, v, the call's sizes) of [tokens, heads, dim] or, for
+    sequences of one length, [batch, length, heads, dim]."""
+    batch = 1
     if q.dim() == 4:
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens are for [tokens, heads, dim]; [batch, length, heads, dim] are sequences of one length")
-        if k.dim() != 4 or v.dim() != 4 or k.shape[:2] != q.shape[:2] or v.shape[:2] != q.shape[:2]:
+        if k.shape[:2] != q.shape[:2] or v.shape[:2] != q.shape[:2]:
             raise ValueError("q, k and v must have the same batch and length")
-        batch = q.shape[0]
-        q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
-    q, k, v = _attn_heads(q, "q"), _attn_heads(k, "k"), _attn_heads(v, "v")
-    rows, heads, dim = q.shape
-    kv_heads = k.shape[1]
-    if k.shape != v.shape or k.shape[0] != rows or k.shape[2] != dim:
-        raise ValueError(f"q {list(q.shape)}, k {list(k.shape)} and v {list(v.shape)} do not fit")
+        batch = q.shape[0] or 1
+        q, k, v = _flat(q, "q"), _flat(k, "k"), _flat(v, "v")
+    q, q_shape, q_side = _attn_side(q, "q")
+    k, k_shape, k_side = _attn_side(k, "k")
+    v, v_shape, v_side = _attn_side(v, "v")
+    rows, heads, dim = q_shape
+    kv_heads = k_shape[1]
+    if k_shape != v_shape or k_shape[0] != rows or k_shape[2] != dim:
+        raise ValueError(f"q {list(q_shape)}, k {list(k_shape)} and v {list(v_shape)} do not fit")
     if heads < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} query heads cannot share {kv_heads} key heads")
     if dim < 8 or dim > 128 or dim % 8:
         raise ValueError(f"heads must have 8 to 128 elements, a multiple of 8, not {dim}")
     borders = None
     if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != q.get_device():
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != q.get_device():
             raise ValueError(f"cu_seqlens must be int32 [sequences + 1] on {q.device}")
         if not cu_seqlens.is_contiguous():
             cu_seqlens = cu_seqlens.contiguous()
         borders, batch = cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
-    elif batch is None or batch == 0:
-        batch = 1
     scale = dim ** -0.5 if scale is None else float(scale)
     if not (scale > 0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
-    return q, k, v, cu_seqlens, (borders, batch, rows, heads, kv_heads, dim, scale)
+    return (q, k, v, cu_seqlens), q_shape, k_shape, (q_side, k_side, v_side), (borders, batch, rows, heads, kv_heads, dim, scale)
 
 
 @functools.lru_cache(maxsize=256)
@@ -102,12 +118,11 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     kv_heads), sequence i rows cu_seqlens[i] to cu_seqlens[i + 1] - 1 (int32, on the device; None: one sequence), or all with
     a batch dimension before, sequences of one length.  lse, fp32 [heads, tokens], is the log of the softmax's
     denominator.  Rows of no sequence are 0 in both."""
-    shape = q.shape
-    q, k, v, _cu, args = _attn_args(q, k, v, cu_seqlens, scale)
-    out = q.new_empty(q.shape)
-    lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
-    lmopt.attn_forward(_at(q), _at(k), _at(v), _at(out), lse.data_ptr(), *args, _stream_ptr(None))
-    return out.view(shape), lse
+    reads, shape, _, sides, args = _attn_args(q, k, v, cu_seqlens, scale)
+    out, out_side = _new_side(shape, reads[0])
+    lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=out.device)
+    lmopt.attn_forward(*sides, out_side, lse.data_ptr(), *args, _stream_ptr(None))
+    return out.view(q.shape) if q.dim() == 4 else out, lse
 
 
 @_on_stream
@@ -117,23 +132,28 @@ def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     needed (dk and dv go together).  Rows of no sequence get 0."""
     if d_out.shape != q.shape or out.shape != q.shape:
         raise ValueError(f"d_out and out must be {list(q.shape)}")
-    shapes = q.shape, k.shape, v.shape
-    if d_out.dim() == 4:
-        d_out, out = (t.reshape(-1, *t.shape[2:]) for t in (d_out, out))
-    q, k, v, _cu, args = _attn_args(q, k, v, cu_seqlens, scale)
-    d_out, out = _attn_heads(d_out, "d_out"), _attn_heads(out, "out")
-    if lse.dtype != torch.float32 or lse.shape != (q.shape[1], q.shape[0]) or lse.get_device() != q.get_device():
-        raise ValueError(f"lse must be float32 {[q.shape[1], q.shape[0]]} on {q.device}")
+    batched = q.dim() == 4
+    reads, q_shape, k_shape, sides, args = _attn_args(q, k, v, cu_seqlens, scale)
+    d_out, _, do_side = _attn_side(_flat(d_out, "d_out") if batched else d_out, "d_out")
+    out, _, out_side = _attn_side(_flat(out, "out") if batched else out, "out")
+    if lse.dtype is not torch.float32 or lse.shape != (q_shape[1], q_shape[0]) or lse.get_device() != out.get_device():
+        raise ValueError(f"lse must be float32 {[q_shape[1], q_shape[0]]} on {out.device}")
     if not lse.is_contiguous():
         lse = lse.contiguous()
-    dq = q.new_empty(q.shape) if need_q else None
-    dk, dv = (k.new_empty(k.shape), v.new_empty(v.shape)) if need_kv else (None, None)
+    dq = dk = dv = None
+    dq_side = dk_side = dv_side = _NO_SIDE
+    if need_q:
+        dq, dq_side = _new_side(q_shape, out)
+    if need_kv:
+        (dk, dk_side), (dv, dv_side) = _new_side(k_shape, out), _new_side(k_shape, out)
     borders, sequences, rows, heads, kv_heads, dim, _ = args
     nbytes = _attn_bytes(borders is not None, sequences, rows, heads, kv_heads, dim)
-    work = q.new_empty(nbytes, dtype=torch.uint8)
-    lmopt.attn_backward(_at(d_out), _at(q), _at(k), _at(v), _at(out), lse.data_ptr(), _at(dq), _at(dk), _at(dv), *args,
-                        work.data_ptr(), nbytes, _stream_ptr(None))
-    return tuple(None if t is None else t.view(s) for t, s in zip((dq, dk, dv), shapes))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=out.device)
+    lmopt.attn_backward(do_side, *sides, out_side, lse.data_ptr(), dq_side, dk_side, dv_side, *args, work.data_ptr(), nbytes,
+                        _stream_ptr(None))
+    if batched:
+        dq, dk, dv = (None if t is None else t.view(s) for t, s in ((dq, q.shape), (dk, k.shape), (dv, v.shape)))
+    return dq, dk, dv
 
 
 class _Attention(torch.autograd.Function):
@@ -206,21 +226,22 @@ def _rope(q, k, positions, plan, inverse, names):
     rows, _, dim = q.shape
     if k.shape[0] != rows or k.shape[2] != dim or k.dtype != q.dtype:
         raise ValueError(f"{names[0]} and {names[1]} must have the same tokens, head size and type")
-    dtype = _type(q, names[0])
+    dtype, device = _type(q, names[0]), q.device
     if plan.rotary_dim > dim:
         raise ValueError(f"{plan.rotary_dim} rotated elements in heads of {dim}")
-    if positions.dtype != torch.int64 or positions.shape != (rows,) or positions.get_device() != q.get_device():
-        raise ValueError(f"positions must be int64 [{rows}] on {q.device}")
+    if positions.dtype is not torch.int64 or positions.shape != (rows,) or positions.get_device() != q.get_device():
+        raise ValueError(f"positions must be int64 [{rows}] on {device}")
     if plan.turns.get_device() != q.get_device():
         raise ValueError("the plan is on another device")
     if not positions.is_contiguous():
         positions = positions.contiguous()
     out, sides = [], []
     for t in (q, k):
-        o = t.new_empty(t.shape)
+        shape = t.shape
+        o = torch.empty(shape, dtype=t.dtype, device=device)
         out.append(o)
-        heads = t.shape[1]
-        sides.append((t.data_ptr(), t.stride(0), t.stride(1), o.data_ptr(), heads * dim, dim, heads))
+        row, head, _ = t.stride()
+        sides.append((t.data_ptr(), row, head, o.data_ptr(), shape[1] * dim, dim, shape[1]))
     lmopt.rope_apply(*sides, positions.data_ptr(), plan.turns.data_ptr(), rows, dim, plan.rotary_dim, plan.factor,
                      plan.interleaved, inverse, dtype, _stream_ptr(None))
     return out[0], out[1]
@@ -258,27 +279,34 @@ def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: Rota
 
 
 # ------------------------------------------------------------------------- activations kept in 8 bits
-@dataclass(frozen=True)
 class PackedActivation:
     """An activation in 8 bits: int8 codes of rows of its last dimension, a uint8 exponent per 32 of them (the last block of a
     row is filled up with zeros), value = code * 2^(exponent - 133); the shape and type it was packed from."""
-    codes: torch.Tensor
-    exponents: torch.Tensor
-    shape: torch.Size
-    dtype: torch.dtype
+    __slots__ = ("codes", "exponents", "shape", "dtype")
 
-    def __post_init__(self):
-        cols = self.shape[-1]
-        rows = math.prod(self.shape[:-1])
-        blocks = -(-cols // ACT_BLOCK)
-        if (self.codes.dtype != torch.int8 or self.codes.shape != (rows, blocks * ACT_BLOCK) or not self.codes.is_contiguous() or
-                self.exponents.dtype != torch.uint8 or self.exponents.shape != (rows, blocks) or not self.exponents.is_contiguous()):
-            raise ValueError(f"codes and exponents do not fit {list(self.shape)}")
+    def __init__(self, codes: torch.Tensor, exponents: torch.Tensor, shape: torch.Size, dtype: torch.dtype):
+        rows, blocks = math.prod(shape[:-1]), -(-shape[-1] // ACT_BLOCK)
+        if (codes.dtype is not torch.int8 or codes.shape != (rows, blocks * ACT_BLOCK) or not codes.is_contiguous() or
+                exponents.dtype is not torch.uint8 or exponents.shape != (rows, blocks) or not exponents.is_contiguous()):
+            raise ValueError(f"codes and exponents do not fit {list(shape)}")
+        self.codes, self.exponents, self.shape, self.dtype = codes, exponents, shape, dtype
 
 
-def _new_codes(t: torch.Tensor, rows: int, cols: int):
+def _new_packed(like: torch.Tensor, rows: int, cols: int, shape, dtype):
+    """A PackedActivation of new memory, and what a call takes of it."""
     blocks = -(-cols // ACT_BLOCK)
-    return t.new_empty((rows, blocks * ACT_BLOCK), dtype=torch.int8), t.new_empty((rows, blocks), dtype=torch.uint8)
+    p = PackedActivation.__new__(PackedActivation)
+    p.codes = torch.empty((rows, blocks * ACT_BLOCK), dtype=torch.int8, device=like.device)
+    p.exponents = torch.empty((rows, blocks), dtype=torch.uint8, device=like.device)
+    p.shape, p.dtype = shape, dtype
+    return p, (p.codes.data_ptr(), blocks * ACT_BLOCK, p.exponents.data_ptr(), blocks)
+
+
+def _packed_at(p: PackedActivation):
+    """What a call takes of a packed activation."""
+    _on_gpu(p.codes, "the packed activation")
+    _on_gpu(p.exponents, "the packed activation")
+    return p.codes.data_ptr(), p.codes.shape[1], p.exponents.data_ptr(), p.exponents.shape[1]
 
 
 @_on_stream
@@ -290,23 +318,16 @@ def pack_activation(x: torch.Tensor) -> PackedActivation:
     rows, cols = m.shape
     if cols == 0:
         raise ValueError("x needs at least one element in a row")
-    codes, exponents = _new_codes(m, rows, cols)
-    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), codes.data_ptr(), codes.shape[1], exponents.data_ptr(), exponents.shape[1],
-                      rows, cols, dtype, _stream_ptr(None))
-    return PackedActivation(codes, exponents, x.shape, x.dtype)
-
-
-def _packed(p: PackedActivation, name: str) -> None:
-    _on_gpu(p.codes, name)
-    _on_gpu(p.exponents, name)
+    p, at = _new_packed(m, rows, cols, x.shape, x.dtype)
+    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), *at, rows, cols, dtype, _stream_ptr(None))
+    return p
 
 
 def _unpack(p: PackedActivation) -> torch.Tensor:
-    _packed(p, "the packed activation")
-    x = p.codes.new_empty(p.shape, dtype=p.dtype)
-    rows, cols = p.codes.shape[0], p.shape[-1]
-    lmopt.act_unpack_i8(p.codes.data_ptr(), p.codes.shape[1], p.exponents.data_ptr(), p.exponents.shape[1], x.data_ptr(), cols,
-                        rows, cols, _type(x, "x"), _stream_ptr(None))
+    at = _packed_at(p)
+    shape = p.shape
+    x = torch.empty(shape, dtype=p.dtype, device=p.codes.device)
+    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.codes.shape[0], shape[-1], _type(x, "x"), _stream_ptr(None))
     return x
 
 
@@ -336,31 +357,24 @@ def swiglu_forward(gate_up: torch.Tensor, keep: bool = True):
     rows, cols = m.shape[0], m.shape[1] // 2
     if m.shape[1] != 2 * cols or cols == 0:
         raise ValueError(f"gate_up's last dimension must be even and not 0, not {m.shape[1]}")
-    h = m.new_empty((*gate_up.shape[:-1], cols))
-    packed = None
-    if keep:
-        codes, exponents = _new_codes(m, 2 * rows, cols)
-        packed = PackedActivation(codes, exponents, torch.Size((*gate_up.shape[:-1], 2, cols)), gate_up.dtype)
-        lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, codes.data_ptr(), codes.shape[1],
-                                 exponents.data_ptr(), exponents.shape[1], rows, cols, dtype, _stream_ptr(None))
-    else:
-        lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, None, 0, None, 0, rows, cols, dtype,
-                                 _stream_ptr(None))
+    lead, device = gate_up.shape[:-1], m.device
+    h = torch.empty((*lead, cols), dtype=gate_up.dtype, device=device)
+    packed, at = _new_packed(m, 2 * rows, cols, torch.Size((*lead, 2, cols)), gate_up.dtype) if keep else (None, (None, 0, None, 0))
+    lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, *at, rows, cols, dtype, _stream_ptr(None))
     return h, packed
 
 
 def _swiglu_backward(dh, packed, need_h):
-    _packed(packed, "the packed activation")
+    at = _packed_at(packed)
     *lead, two, cols = packed.shape
-    if two != 2 or dh.shape != (*lead, cols) or dh.dtype != packed.dtype:
+    if two != 2 or dh.shape != (*lead, cols) or dh.dtype is not packed.dtype:
         raise ValueError(f"dh must be {packed.dtype} {[*lead, cols]} for a packed {list(packed.shape)}")
     d = _rows(dh, "dh")
-    rows = d.shape[0]
-    d_gate_up = d.new_empty((*lead, 2 * cols))
-    h = d.new_empty((*lead, cols)) if need_h else None
-    lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), packed.codes.data_ptr(), packed.codes.shape[1],
-                              packed.exponents.data_ptr(), packed.exponents.shape[1], d_gate_up.data_ptr(), 2 * cols,
-                              None if h is None else h.data_ptr(), cols, rows, cols, _type(d, "dh"), _stream_ptr(None))
+    rows, device = d.shape[0], d.device
+    d_gate_up = torch.empty((*lead, 2 * cols), dtype=packed.dtype, device=device)
+    h = torch.empty((*lead, cols), dtype=packed.dtype, device=device) if need_h else None
+    lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), *at, d_gate_up.data_ptr(), 2 * cols, h.data_ptr() if need_h else None,
+                              cols, rows, cols, _type(d, "dh"), _stream_ptr(None))
     return d_gate_up, h
 
 

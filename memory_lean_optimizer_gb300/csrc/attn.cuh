@@ -54,22 +54,31 @@ struct Tile {
     int64_t start, end;   // the segment's rows
     int64_t first;        // the tile's first row; no tile if it is `end` or behind it
 };
-// The tile of a slot.  All threads of the CTA call it; each probes one border a round.
+// The tile of a slot.  All threads of the CTA call it, once; each probes one border a round (one round for as many
+// segments as threads).
 template <int kRows>
 __device__ __forceinline__ Tile find_tile(const Sequences& s, int64_t slot) {
+    __shared__ int64_t border[2];
     int lo = 0, count = s.n + 2;                      // segments lo .. lo + count - 1
-    while (count > 1) {
+    for (;;) {
         const int step = (count + (int)blockDim.x - 1) / (int)blockDim.x;
         const int i = (int)threadIdx.x * step;
-        const bool at = i < count && s.border(lo + i) / kRows + (lo + i) <= slot;
-        const int below = max(__syncthreads_count(at), 1) - 1;
+        int64_t at = 0, next = 0;
+        if (i < count) {
+            at = s.border(lo + i);
+            if (step == 1) next = s.border(lo + i + 1);
+        }
+        const int below = max(__syncthreads_count(i < count && at / kRows + (lo + i) <= slot), 1) - 1;
+        if (step == 1 && (int)threadIdx.x == below) border[0] = at, border[1] = next;
         lo += below * step;
         count = min(step, count - below * step);
+        if (step == 1) break;
     }
+    __syncthreads();
     Tile t;
     t.segment = lo;
-    t.start = s.border(lo);
-    t.end = max(s.border(lo + 1), t.start);
+    t.start = border[0];
+    t.end = max(border[1], t.start);
     t.first = t.start + (slot - (t.start / kRows + lo)) * kRows;
     if (t.first < t.start) t.first = t.end;           // borders that fall
     return t;

@@ -24,6 +24,7 @@ constexpr int kAttnThreads = 384;                // warp 0 copies, warp 1 multip
 constexpr uint32_t kTileBytes = kTile * 256, kStepBytes = kStep * 256;
 // Stages of a pair of blocks; a tile of queries is in tensor memory and leaves its place to more of them.
 __host__ __device__ constexpr int stages_of(int role) { return role == 0 ? 6 : 4; }
+constexpr int kFewBlocks = 12;
 constexpr size_t kSmem = 6 * 2 * kStepBytes + 4 * kStep * 8 + 1024;
 
 // The rows' -lse (times log2 e) and -delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_sync();
     const int heads = kRole == kQueries ? p.heads : p.kv_heads;
-    const int splits = kRole == kQueries ? 1 : p.splits, rank = splits > 1 ? (int)cluster_rank() : 0;
-    const unsigned unit = blockIdx.x / (unsigned)splits;
+    const int rank = kRole == kKeys && p.splits > 1 ? (int)cluster_rank() : 0;
+    const unsigned unit = kRole == kKeys ? blockIdx.x / (unsigned)p.splits : blockIdx.x;
     const int head = (int)(unit % (unsigned)heads);
     // the tiles with the most work first: the last queries, the first keys
     const int64_t slot = unit / (unsigned)heads;
@@ -149,6 +150,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         return;
     }
+
+    // Streamed blocks: for queries those of the keys up to the tile's last row, for keys those of the queries from the tile's first row
+    // on, head by head.
+    const int64_t stream_first = kRole == kQueries ? tile.start : tile.first;
+    const int64_t stream_end = kRole == kQueries ? min(tile.first + kTile, tile.end) : tile.end;
+    const int per_head = (int)((stream_end - stream_first + kStep - 1) / kStep);
+    const int all_blocks = per_head * (kRole == kQueries ? 1 : p.group);
+    // CTAs of the cluster that take part: each has a start and an end of its own that cost as much as several blocks
+    const int splits = kRole == kKeys ? min(p.splits, max(1, all_blocks / kFewBlocks)) : 1;
+    if (rank >= splits) return;
+    const int first_block = (int)((int64_t)all_blocks * rank / splits), blocks = (int)((int64_t)all_blocks * (rank + 1) / splits) - first_block;
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
@@ -177,14 +189,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     tc_fence_after();
     const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
-
-    // Streamed blocks: for queries those of the keys up to the tile's last row, for keys those of the queries from the tile's first row
-    // on, head by head.
-    const int64_t stream_first = kRole == kQueries ? tile.start : tile.first;
-    const int64_t stream_end = kRole == kQueries ? min(tile.first + kTile, tile.end) : tile.end;
-    const int per_head = (int)((stream_end - stream_first + kStep - 1) / kStep);
-    const int all_blocks = per_head * (kRole == kQueries ? 1 : p.group);
-    const int first_block = (int)((int64_t)all_blocks * rank / splits), blocks = (int)((int64_t)all_blocks * (rank + 1) / splits) - first_block;
 
     if (warp < 4) {
         regs_down<88>();
@@ -394,14 +398,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         // the cluster's sums, in the order of its CTAs; each finishes its share of the tile's rows
         __syncwarp();
         cluster_sync();
-        const int share = kTile / splits, vecs = p.dim / 8;
+        const int low = kTile * rank / splits, share = kTile * (rank + 1) / splits - low, vecs = p.dim / 8;
         bool had = false, late = false;
         for (int r = 0; r < splits; ++r) {
             had |= load_cluster(cluster_addr(smem_u32(&found), r)) != 0;
             late |= load_cluster(cluster_addr(smem_u32(&gave_up), r)) != 0;
         }
         for (int i = threadIdx.x; i < 2 * vecs * share; i += kAttnThreads) {
-            const int in = rank * share + i % share, which = i / share % 2, c = i / share / 2 * 8;
+            const int in = low + i % share, which = i / share % 2, c = i / share / 2 * 8;
             float z[8] = {};
             for (int r = 0; r < splits; ++r) {
                 const uint32_t from = cluster_addr(smem_u32(part_at(base_ptr, which, c, in)), r);
@@ -442,11 +446,11 @@ int injected_stall(int role) {
     return fault_injected(names[role][0]) ? kStallCopy : fault_injected(names[role][1]) ? kStallSoftmax : 0;
 }
 
-// CTAs that share a tile of keys: more while there are fewer than four units to an SM.
+// CTAs that may share a tile of keys: more while they all find place at one time, or nearly.
 int key_splits(const AttnCall& c) {
-    const int64_t units = tile_slots(c.seq, kTile) * c.kv_heads;
+    const int64_t units = tile_slots(c.seq, kTile) * c.kv_heads, most = (c.seq.rows + kStep - 1) / kStep * (c.heads / c.kv_heads);
     int splits = 1;
-    while (splits < 8 && units * splits < 4 * sm_count()) splits *= 2;
+    while (splits < 8 && units * splits < 2 * sm_count() && most >= 2 * splits * kFewBlocks) splits *= 2;
     return splits;
 }
 
