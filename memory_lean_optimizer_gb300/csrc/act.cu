@@ -27,59 +27,110 @@ constexpr int kActThreads = 256;
 constexpr int kBlock = 32, kPer = 16;      // elements that share an exponent; elements to a thread
 constexpr uint32_t kNoExponent = 255;      // of a block with an infinity or a NaN
 
-// Sixteen elements from p, the first `n` of them there (the rest zero).  kVec: p is 16-byte aligned.
-template <bool kVec>
-__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&f)[kPer]) {
-    if (kVec && n >= kPer) {
-        const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// A thread's sixteen elements, at `off` of a matrix, the first `n` of them there (the rest zero).  kVec: 16-byte aligned.
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ void put(uint16_t* to, float x) { *to = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ void put(float* to, float x) { *to = x; }
+__device__ __forceinline__ void load16_wide(const uint16_t* p, float (&f)[kPer]) {
+    unpack8(reinterpret_cast<const uint4*>(p)[0], f);
+    unpack8(reinterpret_cast<const uint4*>(p)[1], f + 8);
+}
+__device__ __forceinline__ void load16_wide(const float* p, float (&f)[kPer]) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] = i < n ? bf16_to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = reinterpret_cast<const float4*>(p)[i];
+        f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
     }
 }
-template <bool kVec>
-__device__ __forceinline__ void load16(const float* p, int n, float (&f)[kPer]) {
-    if (kVec && n >= kPer) {
+__device__ __forceinline__ void store16_wide(uint16_t* p, const float (&f)[kPer]) {
+    uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 a = reinterpret_cast<const float4*>(p)[i];
-            f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
+    for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void store16_wide(float* p, const float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+
+// Rows off 16 bytes: sixteen single elements a thread would be 32 places far apart for every access of a warp.  Instead half a warp
+// takes a thread's sixteen elements, next to each other, and they are turned round in 2 KiB of shared memory of the warp's own (fp32;
+// 16-byte pieces of thread t at their number XOR t / 2 mod 4, so that neither side meets a bank twice).
+// 5003 x 2047 fp32: packed in PACKODD us (single elements 21), the gated activation SWODD (65), its gradients SWBODD (133).
+struct Turn {
+    float* smem;     // 512 floats of the warp
+    int lane;
+    __device__ __forceinline__ float* piece(int thread, int q) const { return smem + 16 * thread + 4 * (q ^ (thread >> 1 & 3)); }
+    template <class T>
+    __device__ __forceinline__ void load(const T* base, int64_t off, int n, float (&f)[kPer]) const {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int of = 2 * k + (lane >> 4), e = lane & 15;
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, off, of);
+            const int have = __shfl_sync(0xFFFFFFFFu, n, of);
+            piece(of, e >> 2)[e & 3] = e < have ? value(base[at + e]) : 0.0f;
         }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 a = *reinterpret_cast<const float4*>(piece(lane, q));
+            f[4 * q] = a.x, f[4 * q + 1] = a.y, f[4 * q + 2] = a.z, f[4 * q + 3] = a.w;
+        }
+        __syncwarp();
+    }
+    template <class T>
+    __device__ __forceinline__ void store(T* base, int64_t off, int n, const float (&f)[kPer]) const {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<float4*>(piece(lane, q)) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int of = 2 * k + (lane >> 4), e = lane & 15;
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, off, of);
+            const int have = __shfl_sync(0xFFFFFFFFu, n, of);
+            if (e < have) put(base + at + e, piece(of, e >> 2)[e & 3]);
+        }
+        __syncwarp();
+    }
+};
+// All threads of a warp call these together.
+template <bool kVec, class T>
+__device__ __forceinline__ void load16(const Turn& turn, const T* base, int64_t off, int n, float (&f)[kPer]) {
+    if (!kVec) {
+        turn.load(base, off, n, f);
+    } else if (n == kPer) {
+        load16_wide(base + off, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) f[i] = i < n ? p[i] : 0.0f;
+        for (int i = 0; i < kPer; ++i) f[i] = i < n ? value(base[off + i]) : 0.0f;
     }
 }
-template <bool kVec>
-__device__ __forceinline__ void store16(uint16_t* p, int n, const float (&f)[kPer]) {
-    if (kVec && n >= kPer) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+template <bool kVec, class T>
+__device__ __forceinline__ void store16(const Turn& turn, T* base, int64_t off, int n, const float (&f)[kPer]) {
+    if (!kVec) {
+        turn.store(base, off, n, f);
+    } else if (n == kPer) {
+        store16_wide(base + off, f);
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (i < n) p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+            if (i < n) put(base + off + i, f[i]);
     }
 }
 template <bool kVec>
-__device__ __forceinline__ void store16(float* p, int n, const float (&f)[kPer]) {
-    if (kVec && n >= kPer) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (i < n) p[i] = f[i];
-    }
+__device__ __forceinline__ Turn turn_of() {
+    __shared__ float4 smem[kVec ? 1 : kActThreads * kPer / 4];
+    return {reinterpret_cast<float*>(smem) + (kVec ? 0 : threadIdx.x / 32 * 512), (int)(threadIdx.x & 31)};
 }
 
 // Codes of this thread's half of a block and the block's exponent.  Both threads of a block call it together.
@@ -161,15 +212,18 @@ struct ActArgs {
     int32_t cols;
 };
 
-// Where a thread's sixteen elements are; false past the last (both threads of a block alike).
+// Where a thread's sixteen elements are; past the last row (both threads of a block alike) there are none.
 struct Place {
-    uint32_t row;
+    int64_t row;
     int col, n;              // first column, how many are there
+    bool live;
     __device__ __forceinline__ Place(const ActArgs& p) {
         const uint64_t i = (uint64_t)blockIdx.x * kActThreads + threadIdx.x;
-        row = (uint32_t)(i < 0xFFFFFFFFull ? (uint32_t)i / p.per_row : i / p.per_row);
-        col = (int)(i - (uint64_t)row * p.per_row) * kPer;
-        n = min(max(p.cols - col, 0), kPer);
+        const uint32_t r = i < 0xFFFFFFFFull ? (uint32_t)i / p.per_row : (uint32_t)(i / p.per_row);
+        col = (int)(i - (uint64_t)r * p.per_row) * kPer;
+        live = r < p.rows;
+        row = live ? r : 0;
+        n = live ? min(max(p.cols - col, 0), kPer) : 0;
     }
 };
 __device__ __forceinline__ uint4* code_at(const ActArgs& p, int64_t row, int col) {
@@ -178,67 +232,69 @@ __device__ __forceinline__ uint4* code_at(const ActArgs& p, int64_t row, int col
 
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kActThreads) k_act_pack(const ActArgs p) {
+    const Turn turn = turn_of<kVec>();
     pdl_sync();
     const Place at(p);
     float f[kPer];
-    const bool live = at.row < p.rows;
-    load16<kVec>(static_cast<const T*>(p.in) + (live ? at.row * p.ld_in + at.col : 0), live ? at.n : 0, f);
+    load16<kVec>(turn, static_cast<const T*>(p.in), at.row * p.ld_in + at.col, at.n, f);
     uint4 c;
     const uint32_t e = encode(f, c);
-    if (!live) return;
+    if (!at.live) return;
     *code_at(p, at.row, at.col) = c;
     if (at.col % kBlock == 0) p.exponents[at.row * p.lde + at.col / kBlock] = (uint8_t)e;
 }
 
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kActThreads) k_act_unpack(const ActArgs p) {
+    const Turn turn = turn_of<kVec>();
     pdl_sync();
     const Place at(p);
-    if (at.row >= p.rows) return;
+    if (kVec && !at.live) return;
     float f[kPer];
-    decode(*code_at(p, at.row, at.col), p.exponents[at.row * p.lde + at.col / kBlock], f);
-    store16<kVec>(static_cast<T*>(p.out) + at.row * p.ld_out + at.col, at.n, f);
+    decode(*code_at(p, at.row, at.live ? at.col : 0), p.exponents[at.row * p.lde + (at.live ? at.col / kBlock : 0)], f);
+    store16<kVec>(turn, static_cast<T*>(p.out), at.row * p.ld_out + at.col, at.n, f);
 }
 
 // Rows 2r and 2r + 1 of the codes are the gate and the up part of row r.
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kActThreads) k_swiglu_forward(const ActArgs p) {
+    const Turn turn = turn_of<kVec>();
     pdl_sync();
     const Place at(p);
     float g[kPer], u[kPer];
-    const bool live = at.row < p.rows;
-    const T* const x = static_cast<const T*>(p.in) + (live ? at.row * p.ld_in + at.col : 0);
-    load16<kVec>(x, live ? at.n : 0, g);
-    load16<kVec>(x + p.cols, live ? at.n : 0, u);
+    const int64_t from = at.row * p.ld_in + at.col;
+    load16<kVec>(turn, static_cast<const T*>(p.in), from, at.n, g);
+    load16<kVec>(turn, static_cast<const T*>(p.in), from + p.cols, at.n, u);
     if (p.codes) {
         uint4 cg, cu;
         const uint32_t eg = encode(g, cg), eu = encode(u, cu);
-        if (live) {
-            *code_at(p, 2 * (int64_t)at.row, at.col) = cg;
-            *code_at(p, 2 * (int64_t)at.row + 1, at.col) = cu;
+        if (at.live) {
+            *code_at(p, 2 * at.row, at.col) = cg;
+            *code_at(p, 2 * at.row + 1, at.col) = cu;
             if (at.col % kBlock == 0) {
-                uint8_t* const e = p.exponents + 2 * (int64_t)at.row * p.lde + at.col / kBlock;
+                uint8_t* const e = p.exponents + 2 * at.row * p.lde + at.col / kBlock;
                 e[0] = (uint8_t)eg;
                 e[p.lde] = (uint8_t)eu;
             }
         }
     }
-    if (!live) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) g[i] = g[i] * sigmoid<T>(g[i]) * u[i];
-    store16<kVec>(static_cast<T*>(p.out) + at.row * p.ld_out + at.col, at.n, g);
+    store16<kVec>(turn, static_cast<T*>(p.out), at.row * p.ld_out + at.col, at.n, g);
 }
 
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kActThreads) k_swiglu_backward(const ActArgs p) {
+    const Turn turn = turn_of<kVec>();
     pdl_sync();
     const Place at(p);
-    if (at.row >= p.rows) return;
+    if (kVec && !at.live) return;
     float g[kPer], u[kPer], d[kPer];
-    const uint4 cg = *code_at(p, 2 * (int64_t)at.row, at.col), cu = *code_at(p, 2 * (int64_t)at.row + 1, at.col);
-    const uint8_t* const e = p.exponents + 2 * (int64_t)at.row * p.lde + at.col / kBlock;
+    const int col = at.live ? at.col : 0;
+    const uint4 cg = *code_at(p, 2 * at.row, col), cu = *code_at(p, 2 * at.row + 1, col);
+    const uint8_t* const e = p.exponents + 2 * at.row * p.lde + col / kBlock;
     const uint32_t eg = e[0], eu = e[p.lde];
-    load16<kVec>(static_cast<const T*>(p.in) + at.row * p.ld_in + at.col, at.n, d);
+    load16<kVec>(turn, static_cast<const T*>(p.in), at.row * p.ld_in + at.col, at.n, d);
     decode(cg, eg, g);
     decode(cu, eu, u);
     float h[kPer];
@@ -249,10 +305,10 @@ __global__ void __launch_bounds__(kActThreads) k_swiglu_backward(const ActArgs p
         g[i] = b * fmaf(a, 1.0f - s, s);
         u[i] = d[i] * a;
     }
-    T* const out = static_cast<T*>(p.out) + at.row * p.ld_out + at.col;
-    store16<kVec>(out, at.n, g);
-    store16<kVec>(out + p.cols, at.n, u);
-    if (p.h) store16<kVec>(static_cast<T*>(p.h) + at.row * p.ldh + at.col, at.n, h);
+    const int64_t to = at.row * p.ld_out + at.col;
+    store16<kVec>(turn, static_cast<T*>(p.out), to, at.n, g);
+    store16<kVec>(turn, static_cast<T*>(p.out), to + p.cols, at.n, u);
+    if (p.h) store16<kVec>(turn, static_cast<T*>(p.h), at.row * p.ldh + at.col, at.n, h);
 }
 
 bool vectors(const void* p, int64_t ld, size_t elem) { return is_aligned(p, 16) && (size_t)ld * elem % 16 == 0; }

@@ -130,6 +130,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found, copied;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // before anything of the stream is needed
+    const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
+                   sums_done = ready + 16, drained = sums_done + 8;
+    if (threadIdx.x == 0) {
+        gave_up = found = copied = 0;
+        mbar_init(a_full, kRole == kKeys ? 1 : 8);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(x_done + 8 * i, 1);
+            mbar_init(ready + 8 * i, 8);
+        }
+        mbar_init(sums_done, 1);
+        mbar_init(drained, 1);
+        mbar_init_fence();
+        if (kRole == kKeys) {
+            tma_prefetch_map(&map_a0);
+            tma_prefetch_map(&map_a1);
+        }
+        tma_prefetch_map(&map_b0);
+        tma_prefetch_map(&map_b1);
+    }
     pdl_sync();
     const int heads = kRole == kQueries ? p.heads : p.kv_heads;
     const int rank = kRole == kKeys && p.splits > 1 ? (int)cluster_rank() : 0;
@@ -166,23 +190,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
     const uint32_t stages = base + (kRole == kKeys ? 2 * kTileBytes : 0);   // stage: B0, B1
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
-    const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
-                   sums_done = ready + 16, drained = sums_done + 8;
-    if (threadIdx.x == 0) {
-        gave_up = found = copied = 0;
-        mbar_init(a_full, kRole == kKeys ? 1 : 8);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(x_done + 8 * i, 1);
-            mbar_init(ready + 8 * i, 8);
-        }
-        mbar_init(sums_done, 1);
-        mbar_init(drained, 1);
-        mbar_init_fence();
-    }
     if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
     tc_fence_before();
     __syncthreads();
@@ -371,6 +378,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         const int which = kRole == kKeys ? t : 0;
         const HeadRows& o = which ? p.out1 : p.out0;
         uint16_t* const to = static_cast<uint16_t*>(o.p) + head * o.head + row * o.row;
+        const bool sectors = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
         const float f = !ok ? __builtin_nanf("") : which ? 1.0f : p.scale;
         const uint32_t sum_at = tmem + lanes + 256 + 128 * which;
 #pragma unroll 1
@@ -387,9 +395,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                     *part_at(base_ptr, which, q + k, in) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
             } else if (live) {
                 if (which && *static_cast<volatile int*>(&found)) add_cleared(p, tile, head, row, q, z);
-#pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                    if (q + k < p.dim) store8(to + q + k, z[k], z[k + 1], z[k + 2], z[k + 3], z[k + 4], z[k + 5], z[k + 6], z[k + 7]);
+                store16(to + q, z, p.dim - q, sectors);
+                store16(to + q + 16, z + 16, p.dim - q - 16, sectors);
             }
             __syncwarp();
         }

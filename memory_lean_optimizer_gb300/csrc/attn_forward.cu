@@ -47,24 +47,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found[2], copied[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_sync();
-    const int head = (int)(blockIdx.x % (unsigned)p.heads);
-    // later tiles see more keys: they come first
-    const Tile tile = find_tile<2 * kTile>(p.seq, p.slots - 1 - blockIdx.x / (unsigned)p.heads);
-    if (tile.first >= tile.end) return;
-    uint16_t* const out = p.out + head * p.hso;
-    float* const lse = p.lse + (int64_t)head * p.seq.rows;
-    if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
-        const int rows = (int)min((int64_t)(2 * kTile), tile.end - tile.first), vecs = p.dim / 8;
-        for (int i = threadIdx.x; i < rows * vecs; i += kAttnThreads)
-            *reinterpret_cast<uint4*>(out + (tile.first + i / vecs) * p.ldo + i % vecs * 8) = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < rows; i += kAttnThreads) lse[tile.first + i] = 0.0f;
-        return;
-    }
-
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
-    const uint32_t q_tile = base, k_tile = base + 2 * kTileBytes, v_tile = k_tile + kStages * kTileBytes;
+    // before anything of the stream is needed
     const uint32_t q_full = smem_u32(bars), k_full = q_full + 16, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages,
                    v_empty = v_full + 8 * kStages, s_done = v_empty + 8 * kStages, p_ready = s_done + 16, o_done = p_ready + 16,
                    drained = o_done + 16;
@@ -85,7 +68,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
         }
         mbar_init(drained, 1);
         mbar_init_fence();
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
     }
+    pdl_sync();
+    const int head = (int)(blockIdx.x % (unsigned)p.heads);
+    // later tiles see more keys: they come first
+    const Tile tile = find_tile<2 * kTile>(p.seq, p.slots - 1 - blockIdx.x / (unsigned)p.heads);
+    if (tile.first >= tile.end) return;
+    uint16_t* const out = p.out + head * p.hso;
+    float* const lse = p.lse + (int64_t)head * p.seq.rows;
+    if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
+        const int rows = (int)min((int64_t)(2 * kTile), tile.end - tile.first), vecs = p.dim / 8;
+        for (int i = threadIdx.x; i < rows * vecs; i += kAttnThreads)
+            *reinterpret_cast<uint4*>(out + (tile.first + i / vecs) * p.ldo + i % vecs * 8) = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < rows; i += kAttnThreads) lse[tile.first + i] = 0.0f;
+        return;
+    }
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
+    const uint32_t q_tile = base, k_tile = base + 2 * kTileBytes, v_tile = k_tile + kStages * kTileBytes;
     if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
     tc_fence_before();
     __syncthreads();
@@ -202,9 +206,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             float top[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                top[q] = __uint_as_float(x[q][0]);
+                top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
 #pragma unroll
-                for (int k = 1; k < 32; ++k) top[q] = fmaxf(top[q], __uint_as_float(x[q][k]));
+                for (int k = 2; k < 32; k += 2) top[q] = max3(top[q], __uint_as_float(x[q][k]), __uint_as_float(x[q][k + 1]));
             }
             const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grow = now > m + kSlack;
@@ -266,6 +270,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             tc_fence_after();
             const int64_t row = tile.first + t * kTile + in;
             const bool live = row < tile.end;
+            uint16_t* const to = out + row * p.ldo;
+            const bool sectors = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
             const float inv = ok ? 1.0f / sum : __builtin_nanf("");
             if (live) lse[row] = ok ? (m + log2f(sum)) * kLn2 : __builtin_nanf("");
             // blocks whose values were cleared: the first tile's own (seen by both), the second's own
@@ -284,11 +290,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                         if (had0) add_non_finite(y, v, p.ldv, tile.first, min(tile.first + kTile, row + 1), q, p.dim);
                         if (had1) add_non_finite(y, v, p.ldv, tile.first + kTile, row + 1, q, p.dim);
                     }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        if (q + k < p.dim)
-                            *reinterpret_cast<uint4*>(out + row * p.ldo + q + k) = make_uint4(
-                                pack_bf16(y[k], y[k + 1]), pack_bf16(y[k + 2], y[k + 3]), pack_bf16(y[k + 4], y[k + 5]), pack_bf16(y[k + 6], y[k + 7]));
+                    store16(to + q, y, p.dim - q, sectors);
+                    store16(to + q + 16, y + 16, p.dim - q - 16, sectors);
                 }
                 __syncwarp();
             }

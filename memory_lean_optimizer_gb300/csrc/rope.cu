@@ -34,6 +34,7 @@ struct RopeArgs {
     const uint64_t* turns;
     int64_t rows;
     int32_t dim, rotary, tokens;   // tokens to a CTA
+    uint32_t per_head;             // 2^32 / units of a head, rounded up, where that finds the head of every unit; or 0
     float factor;
     bool inverse;
 };
@@ -101,11 +102,14 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs p) {
     constexpr int kStep = !kInterleaved ? V : V > 1 ? V / 2 : 1;      // pairs to a unit
     const int turning = half / kStep, units = turning + (p.dim - p.rotary) / V;
     const int all = (p.t[0].heads + p.t[1].heads) * units;
-    for (int token = 0; token < n; ++token) {
-        const float2* const cs = table + token * half;
-        for (int i = threadIdx.x; i < all; i += kRopeThreads) {
-            int head = i / units;
-            const int u = i - head * units;
+    int token = 0, rest = (int)threadIdx.x;                  // unit `rest` of that token
+    for (;;) {
+        while (rest >= all) rest -= all, ++token;
+        if (token >= n) break;
+        {
+            const float2* const cs = table + token * half;
+            int head = p.per_head ? (int)__umulhi((uint32_t)rest, p.per_head) : rest / units;
+            const int u = rest - head * units;
             const bool second = head >= p.t[0].heads;
             const RopeTensor& t = second ? p.t[1] : p.t[0];
             if (second) head -= p.t[0].heads;
@@ -144,12 +148,16 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs p) {
                 store<T, V>(y + c + half, b);
             }
         }
+        rest += kRopeThreads;
     }
 }
 
 template <class T, int V, bool kInterleaved>
 int rope_v(RopeArgs& a, cudaStream_t s) {
     a.tokens = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, a.rows / ((int64_t)sm_count() * 8)));
+    const uint64_t units = a.rotary / 2 / (!kInterleaved ? V : V > 1 ? V / 2 : 1) + (a.dim - a.rotary) / V;
+    // x ceil(2^32 / u) / 2^32 has the quotient x / u as its whole part while x u < 2^32
+    a.per_head = units > 1 && (uint64_t)(a.t[0].heads + a.t[1].heads) * units * units < (1ull << 32) ? (uint32_t)(((1ull << 32) + units - 1) / units) : 0;
     const int64_t grid = (a.rows + a.tokens - 1) / a.tokens;
     const size_t smem = (size_t)a.tokens * (a.rotary / 2) * sizeof(float2);
     return check_cuda(launch_after(k_rope<T, V, kInterleaved>, (unsigned)grid, kRopeThreads, smem, 1, s, a), "rotary launch");
@@ -217,7 +225,7 @@ extern "C" int rope_apply(const void* q, int64_t q_row, int64_t q_head, void* q_
     if (rotary && (!positions || !turns)) return set_error(OPTIM_EINVAL, "positions or turns is NULL");
     if (!is_aligned(positions, 8) || !is_aligned(turns, 8)) return set_error(OPTIM_EALIGN, "positions or turns not 8-byte aligned");
     RopeArgs a{{{q, q_out, q_row, qo_row, q_head, qo_head, (int32_t)q_heads}, {k, k_out, k_row, ko_row, k_head, ko_head, (int32_t)k_heads}},
-               positions, turns, rows, (int32_t)dim, (int32_t)rotary, 0, factor, inverse != 0};
+               positions, turns, rows, (int32_t)dim, (int32_t)rotary, 0, 0, factor, inverse != 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return type == OPTIM_BF16 ? rope_t<uint16_t>(a, interleaved != 0, s) : rope_t<float>(a, interleaved != 0, s);
 }

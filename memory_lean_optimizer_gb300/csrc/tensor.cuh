@@ -102,8 +102,13 @@ __device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
 // (*gave_up, a shared word of each CTA that is raised in both of a pair, so that neither works on alone);
 // false: it did not complete.
 constexpr uint64_t kWaitNs = 4000000000ull;
+// (Reading the timer takes as long as many a wait lasts: it begins after a while.)
 template <int kCta>
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
+    if (__builtin_expect(mbar_try<kCta>(bar, parity), 1)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try<kCta>(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
 #pragma unroll 1
@@ -116,14 +121,6 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
             return false;
         }
     }
-}
-// Reading the timer takes as long as many a wait lasts: it begins after a while.
-template <int kCta>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t ns) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-        if (mbar_try<kCta>(bar, parity)) return true;
-    return mbar_wait_long<kCta>(bar, parity, gave_up, ns);
 }
 // The same after a wait has given up, for what is in flight.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
