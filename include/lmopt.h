@@ -30,7 +30,8 @@
  *    GPU is disturbed).  =stall_<stats|grad|hidden|weight>_<copy|peer|free> lets the bounded waits
  *    inside that product kernel of the cross entropy run out after a tenth of a second: its first
  *    cluster stops copying (one of its CTAs) or keeps its accumulators, and every wait behind that
- *    ends by its limit; =stall_attention[_dq|_dkv]_<copy|softmax> does so in the first CTA of an attention kernel.
+ *    ends by its limit; =stall_attention[_dq|_dkv]_<copy|softmax> does so in an
+ *    attention kernel, for the first sequence's first tile of head 0.
  */
 #ifndef LMOPT_H
 #define LMOPT_H

@@ -18,7 +18,23 @@ from torch.autograd.function import once_differentiable
 
 from . import lmopt
 from .engine import _stream_ptr
-from .head import _on_stream, _rows, _type
+from .head import _rows, _type, layer_norm
+
+def _on_stream(fn):
+    """Runs a call's copies, allocations and kernels on its `stream` argument (None: the current stream)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for a in (*args, *kw.values()):        # their memory is not given away before the stream is done with it
+            for t in a.tensors() if isinstance(a, (PackedActivation, RotaryPlan)) else (a,):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+        return out
+    return call
+
 
 ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.h, act_pack_i8)
 
@@ -220,6 +236,9 @@ class RotaryPlan:
         turns = [round(Fraction(f) / (2 * _PI) * 2 ** 64) % 2 ** 64 for f in freq]
         self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device=device)
 
+    def tensors(self):
+        return (self.turns,)
+
 
 def _rope(q, k, positions, plan, inverse, names):
     q, k = _heads(q, names[0]), _heads(k, names[1])
@@ -289,7 +308,10 @@ class PackedActivation:
         if (codes.dtype is not torch.int8 or codes.shape != (rows, blocks * ACT_BLOCK) or not codes.is_contiguous() or
                 exponents.dtype is not torch.uint8 or exponents.shape != (rows, blocks) or not exponents.is_contiguous()):
             raise ValueError(f"codes and exponents do not fit {list(shape)}")
-        self.codes, self.exponents, self.shape, self.dtype = codes, exponents, shape, dtype
+        self.codes, self.exponents, self.shape, self.dtype = codes, exponents, torch.Size(shape), dtype
+
+    def tensors(self):
+        return self.codes, self.exponents
 
 
 def _new_packed(like: torch.Tensor, rows: int, cols: int, shape, dtype):
@@ -323,29 +345,14 @@ def pack_activation(x: torch.Tensor) -> PackedActivation:
     return p
 
 
-def _unpack(p: PackedActivation) -> torch.Tensor:
+@_on_stream
+def unpack_activation(p: PackedActivation) -> torch.Tensor:
+    """The values that a packed activation stands for, in its shape and type."""
     at = _packed_at(p)
     shape = p.shape
     x = torch.empty(shape, dtype=p.dtype, device=p.codes.device)
     lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.codes.shape[0], shape[-1], _type(x, "x"), _stream_ptr(None))
     return x
-
-
-def _on_stream_packed(fn, *args, packed: PackedActivation, stream, **kw):
-    """fn with the packed activation's tensors kept for `stream`."""
-    if stream is None:
-        return fn(*args, **kw)
-    with torch.cuda.stream(stream):
-        out = fn(*args, **kw)
-    for t in (packed.codes, packed.exponents, *args, *kw.values()):
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
-    return out
-
-
-def unpack_activation(p: PackedActivation, stream=None) -> torch.Tensor:
-    """The values that a packed activation stands for, in its shape and type."""
-    return _on_stream_packed(_unpack, p, packed=p, stream=stream)
 
 
 @_on_stream
@@ -364,10 +371,15 @@ def swiglu_forward(gate_up: torch.Tensor, keep: bool = True):
     return h, packed
 
 
-def _swiglu_backward(dh, packed, need_h):
+@_on_stream
+def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = False):
+    """(d_gate_up, h) from the gradient of h and what swiglu_forward kept: the gradients at the gate and up values that
+    the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
     at = _packed_at(packed)
-    *lead, two, cols = packed.shape
-    if two != 2 or dh.shape != (*lead, cols) or dh.dtype is not packed.dtype:
+    if len(packed.shape) < 2 or packed.shape[-2] != 2:
+        raise ValueError(f"a packed {list(packed.shape)} is not a gate and up pair")
+    *lead, _, cols = packed.shape
+    if dh.shape != (*lead, cols) or dh.dtype is not packed.dtype:
         raise ValueError(f"dh must be {packed.dtype} {[*lead, cols]} for a packed {list(packed.shape)}")
     d = _rows(dh, "dh")
     rows, device = d.shape[0], d.device
@@ -376,12 +388,6 @@ def _swiglu_backward(dh, packed, need_h):
     lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), *at, d_gate_up.data_ptr(), 2 * cols, h.data_ptr() if need_h else None,
                               cols, rows, cols, _type(d, "dh"), _stream_ptr(None))
     return d_gate_up, h
-
-
-def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = False, stream=None):
-    """(d_gate_up, h) from the gradient of h and what swiglu_forward kept: the gradients at the gate and up values that
-    the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
-    return _on_stream_packed(_swiglu_backward, dh, packed, need_h, packed=packed, stream=stream)
 
 
 class _SwiGLU(torch.autograd.Function):
@@ -439,3 +445,34 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch
     if not torch.is_grad_enabled():
         return torch.nn.functional.linear(swiglu_forward(torch.nn.functional.linear(x, w_in), keep=False)[0], w_out)
     return _GatedMLP.apply(x, w_in, w_out)
+
+
+class TransformerBlock(torch.nn.Module):
+    """x + attention(norm x), then x + mlp(norm x), over packed tokens [tokens, dim] in bf16: grouped heads with rotary
+    positions, a gated MLP that keeps its activations in 8 bits.  Both output matrices start at zero, so that the block starts as the
+    identity."""
+
+    def __init__(self, dim: int, heads: int, kv_heads: int | None = None, hidden: int | None = None, rotary: RotaryPlan | None = None,
+                 eps: float = 1e-5, device="cuda"):
+        super().__init__()
+        kv_heads = heads if kv_heads is None else kv_heads
+        if dim % heads or dim // heads % 8 or dim // heads > 128 or heads % kv_heads:
+            raise ValueError(f"width {dim} does not make {heads} heads of a multiple of 8, up to 128, that share {kv_heads}")
+        hidden = 4 * dim if hidden is None else hidden
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        self.heads, self.kv_heads, self.head_dim, self.eps = heads, kv_heads, dim // heads, eps
+        self.rotary = rotary or RotaryPlan(self.head_dim, device=device)
+        new = lambda rows, cols: torch.nn.Parameter(torch.randn(rows, cols, **bf16) * cols ** -0.5)
+        self.norm1, self.norm2 = torch.nn.Parameter(torch.ones(dim, **bf16)), torch.nn.Parameter(torch.ones(dim, **bf16))
+        self.qkv = new((heads + 2 * kv_heads) * self.head_dim, dim)
+        self.proj = torch.nn.Parameter(torch.zeros(dim, dim, **bf16))
+        self.w_in = new(2 * hidden, dim)
+        self.w_out = torch.nn.Parameter(torch.zeros(dim, hidden, **bf16))
+
+    def forward(self, x: torch.Tensor, positions: torch.Tensor, cu_seqlens: torch.Tensor | None = None) -> torch.Tensor:
+        h, kv = self.heads, self.kv_heads
+        qkv = torch.nn.functional.linear(layer_norm(x, self.norm1, None, self.eps), self.qkv).view(x.shape[0], h + 2 * kv, self.head_dim)
+        q, k = rotary(qkv[:, :h], qkv[:, h:h + kv], positions, self.rotary)
+        y = attention(q, k, qkv[:, h + kv:], cu_seqlens)
+        x = x + torch.nn.functional.linear(y.flatten(1), self.proj)
+        return x + gated_mlp(layer_norm(x, self.norm2, None, self.eps), self.w_in, self.w_out)

@@ -96,7 +96,7 @@ struct BackwardArgs {
     const uint16_t* d_out;              // kKeys: for what is taken out of masked blocks
     int64_t lddo, hsdo;
     uint64_t wait_ns;
-    int32_t stall;
+    int32_t stall;                      // tests of the waits' limit: what the first sequence's first tile of head 0 withholds (Stall), or 0
 };
 enum Stall { kStallCopy = 1, kStallSoftmax = 2 };
 
@@ -197,10 +197,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
+    const int stall = head == 0 && rank == 0 && tile.segment == 1 && tile.first == tile.start ? p.stall : 0;
+
     if (warp < 4) {
         regs_down<88>();
         if (warp == 0 && elect_lane()) {
-            const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
+            const int stop = stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const uint32_t boxes = p.dim > 64 ? 2 : 1;
             if (kRole == kKeys) {
                 mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !(blockIdx.x == 0 && p.stall == kStallSoftmax)) mbar_arrive(ready + 8 * (i & 1));
+            if (lane == 0 && stall != kStallSoftmax) mbar_arrive(ready + 8 * (i & 1));
         }
         ok = ok && wait(sums_done, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -453,11 +455,13 @@ int injected_stall(int role) {
     return fault_injected(names[role][0]) ? kStallCopy : fault_injected(names[role][1]) ? kStallSoftmax : 0;
 }
 
-// CTAs that may share a tile of keys: more while they all find place at one time, or nearly.
+// CTAs that may share a tile of keys: more while all of them find place at one time.  (A cluster waits for as many free SMs as it
+// has CTAs, those of little use among them: 8192 tokens in 16 sequences, 4 / 2 heads of 64, 164 units, 21 us with one CTA,
+// 34 with two, 50 with eight; 1024 tokens, 16 / 2 heads of 128, 22 units, 175 us with one, 41 with four.)
 int key_splits(const AttnCall& c) {
     const int64_t units = tile_slots(c.seq, kTile) * c.kv_heads, most = (c.seq.rows + kStep - 1) / kStep * (c.heads / c.kv_heads);
     int splits = 1;
-    while (splits < 8 && units * splits < 2 * sm_count() && most >= 2 * splits * kFewBlocks) splits *= 2;
+    while (splits < 8 && 2 * units * splits <= sm_count() && most >= 2 * splits * kFewBlocks) splits *= 2;
     return splits;
 }
 

@@ -34,7 +34,7 @@ struct ForwardArgs {
     const uint16_t* v;
     int64_t ldv, hsv;
     uint64_t wait_ns;
-    int32_t stall;                 // tests of the waits' limit: the first CTA withholds (Stall)
+    int32_t stall;                 // tests of the waits' limit: what the first sequence's first tile of head 0 withholds (Stall), or 0
 };
 enum Stall { kStallCopy = 1, kStallSoftmax = 2 };
 
@@ -102,10 +102,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
     const int n0 = before + 1, n1 = left > kTile ? before + 2 : 0;              // blocks that the tiles see
     const int blocks = max(n0, n1);
 
+    const int stall = head == 0 && tile.segment == 1 && tile.first == tile.start ? p.stall : 0;
+
     if (warp < 4) {
         regs_down<72>();
         if (warp == 0 && elect_lane()) {
-            const int stop = blockIdx.x == 0 && p.stall == kStallCopy ? 0 : 0x7FFFFFFF;
+            const int stop = stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const int kv = head / p.group;
             const uint32_t boxes = p.dim > 64 ? 2 : 1;
             for (int t = 0; t < (n1 ? 2 : 1); ++t) {
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !(blockIdx.x == 0 && p.stall == kStallSoftmax)) mbar_arrive(p_ready + 8 * t);
+            if (lane == 0 && stall != kStallSoftmax) mbar_arrive(p_ready + 8 * t);
         }
         if (n) {
             if (ok) ok = wait(o_done + 8 * t, (n - 1) & 1);

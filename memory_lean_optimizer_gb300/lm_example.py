@@ -1,8 +1,8 @@
 """A small language model trained with the memory-lean tail and optimizer, as they are used together:
 
-    python -m memory_lean_optimizer_gb300.lm_example [--steps 60] [--vocab 8192] [--states u8|fp32]
+    python -m memory_lean_optimizer_gb300.lm_example [--steps 60] [--vocab 8192] [--states u8|fp32] [--blocks 2]
 
-An embedding feeds ``head.LMTail`` (layer norm, output matrix, cross entropy without logits); every
+An embedding feeds (through transformer blocks, if asked for: ``block.TransformerBlock`` over the packed tokens) ``head.LMTail`` (layer norm, output matrix, cross entropy without logits); every
 parameter is bf16 with a Kahan residual and is stepped by AdamW with 8-bit (or fp32) moments from its
 gradient hook during the backward pass (``hooks.attach_fused_adamw``), so that neither the logits nor
 the gradients of the whole model nor fp32 moments exist at any time.  The data are synthetic: each
@@ -14,17 +14,28 @@ import argparse
 
 import torch
 
-from . import head, hooks
+from . import block, head, hooks
 
 
 class TinyLM(torch.nn.Module):
-    def __init__(self, vocab: int, dim: int):
+    def __init__(self, vocab: int, dim: int, blocks: int = 0):
         super().__init__()
         self.embed = torch.nn.Embedding(vocab, dim, device="cuda", dtype=torch.bfloat16)
         self.tail = head.LMTail(dim, vocab)
+        heads = max(dim // 64, 1)
+        self.blocks = torch.nn.ModuleList(block.TransformerBlock(dim, heads, max(heads // 2, 1)) for _ in range(blocks))
 
     def forward(self, tokens: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
-        return self.tail(self.embed(tokens), target)
+        x = self.embed(tokens)
+        if self.blocks:                        # tokens [rows, length] as sequences side by side
+            rows, length = tokens.shape
+            x = x.flatten(0, 1)
+            positions = torch.arange(length, device=x.device).repeat(rows)
+            borders = torch.arange(rows + 1, device=x.device, dtype=torch.int32) * length
+            for b in self.blocks:
+                x = b(x, positions, borders)
+            x = x.view(rows, length, -1)
+        return self.tail(x, target)
 
 
 def batch(vocab: int, rows: int, length: int, gen: torch.Generator):
@@ -36,11 +47,11 @@ def batch(vocab: int, rows: int, length: int, gen: torch.Generator):
 
 
 def train(steps: int = 60, vocab: int = 8192, dim: int = 256, rows: int = 16, length: int = 512, states: str = "u8",
-          lr: float = 5e-3, seed: int = 0, log=None) -> list[float]:
+          lr: float = 5e-3, seed: int = 0, log=None, blocks: int = 0) -> list[float]:
     """Trains the model; returns the loss of every step."""
     torch.manual_seed(seed)
     gen = torch.Generator(device="cuda").manual_seed(seed)
-    model = TinyLM(vocab, dim)
+    model = TinyLM(vocab, dim, blocks)
     stepper = hooks.attach_fused_adamw(list(model.parameters()), 2, dict(lr=lr, beta2=0.99, weight_decay=0.01), states=states)
     losses = []
     for step in range(steps):
@@ -58,9 +69,10 @@ def main() -> None:
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--vocab", type=int, default=8192)
     ap.add_argument("--states", choices=("u8", "fp32"), default="u8")
+    ap.add_argument("--blocks", type=int, default=0)
     args = ap.parse_args()
     torch.cuda.reset_peak_memory_stats()
-    losses = train(steps=args.steps, vocab=args.vocab, states=args.states, log=print)
+    losses = train(steps=args.steps, vocab=args.vocab, states=args.states, log=print, blocks=args.blocks)
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f}; peak memory {torch.cuda.max_memory_allocated() / 2 ** 20:.0f} MiB "
           f"(fp32 logits and their gradient alone: {2 * 16 * 512 * args.vocab * 4 / 2 ** 20:.0f} MiB)")
 
