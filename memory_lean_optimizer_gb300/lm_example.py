@@ -2,8 +2,8 @@
 
     python -m memory_lean_optimizer_gb300.lm_example [--steps 60] [--vocab 8192] [--states u8|fp32] [--blocks 2]
 
-An embedding feeds (through transformer blocks, if asked for: ``block.TransformerBlock`` over the packed tokens) ``head.LMTail`` (layer norm, output matrix, cross entropy without logits); every
-parameter is bf16 with a Kahan residual and is stepped by AdamW with 8-bit (or fp32) moments from its
+An embedding feeds ``head.LMTail`` (layer norm, output matrix, cross entropy without logits), through
+transformer blocks over the packed tokens if asked for (``block.TransformerBlock``); every parameter is bf16 with a Kahan residual and is stepped by AdamW with 8-bit (or fp32) moments from its
 gradient hook during the backward pass (``hooks.attach_fused_adamw``), so that neither the logits nor
 the gradients of the whole model nor fp32 moments exist at any time.  The data are synthetic: each
 token follows from the one before it, and a part of the positions carries no target.
@@ -22,8 +22,9 @@ class TinyLM(torch.nn.Module):
         super().__init__()
         self.embed = torch.nn.Embedding(vocab, dim, device="cuda", dtype=torch.bfloat16)
         self.tail = head.LMTail(dim, vocab)
-        heads = max(dim // 64, 1)
-        self.blocks = torch.nn.ModuleList(block.TransformerBlock(dim, heads, max(heads // 2, 1)) for _ in range(blocks))
+        heads = next(h for h in range(max(dim // 64, 1), 0, -1) if dim % h == 0)
+        kv_heads = heads // 2 if heads % 2 == 0 else heads
+        self.blocks = torch.nn.ModuleList(block.TransformerBlock(dim, heads, kv_heads) for _ in range(blocks))
 
     def forward(self, tokens: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
         x = self.embed(tokens)
