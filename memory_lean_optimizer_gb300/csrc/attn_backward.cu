@@ -90,7 +90,7 @@ struct BackwardArgs {
     int32_t heads, kv_heads, group, dim;
     int32_t splits;                     // kKeys: CTAs (a cluster) that share a tile's blocks
     float scale;
-    const RowBlock* rows;
+    RowBlock* rows;
     HeadRows a0, a1;                    // kQueries: Q, dO
     HeadRows out0, out1;                // dq; or dk, dv
     const uint16_t* d_out;              // kKeys: for what is taken out of masked blocks
@@ -126,13 +126,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                                                                    const BackwardArgs p) {
     constexpr int kStages = stages_of(kRole);
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 2];
+    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 3];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found, copied;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // before anything of the stream is needed
     const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
-                   sums_done = ready + 16, drained = sums_done + 8;
+                   sums_done = ready + 16, drained = sums_done + 8, halves_ready = drained + 8;
     if (threadIdx.x == 0) {
         gave_up = found = copied = 0;
         mbar_init(a_full, kRole == kKeys ? 1 : 8);
@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         mbar_init(sums_done, 1);
         mbar_init(drained, 1);
+        mbar_init(halves_ready, 4);
         mbar_init_fence();
         if (kRole == kKeys) {
             tma_prefetch_map(&map_a0);
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         for (int i = threadIdx.x; rank == 0 && i < rows * vecs; i += kAttnThreads) {
             const int64_t row = tile.first + i / vecs;
             const int c = i % vecs * 8;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out0.p) + head * p.out0.head + row * p.out0.row + c) = make_uint4(0, 0, 0, 0);
+            if (p.out0.p) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out0.p) + head * p.out0.head + row * p.out0.row + c) = make_uint4(0, 0, 0, 0);
             if (kRole == kKeys)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out1.p) + head * p.out1.head + row * p.out1.row + c) = make_uint4(0, 0, 0, 0);
         }
@@ -270,6 +271,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
 #pragma unroll
                 for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
                     mma_ts(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, i == 0 && j == 0);
+                if (kRole == kQueries) {
+#pragma unroll
+                    for (int j = 0; j < kStep / 16; ++j)     // what dS's rounding left
+                        mma_ts(tmem + 256, a + 144 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, false);
+                }
                 mma_commit<1>(empty + 8 * stage);
                 if (++stage == kStages) stage = 0;
             }
@@ -308,7 +314,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             const RowBlock& b = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
             if (row < tile.end) my_lse = b.lse[in % kStep], my_delta = b.delta[in % kStep];
         }
-        const F2 my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
+        F2 excess[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};                       // sum of dS
+        const F2 minus1 = f2(-1.0f, -1.0f), my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
         int at = first_block % per_head;                                       // the block's place in its head
         bool ok = true;
         uint32_t stage = 0, phase = 0;
@@ -330,10 +337,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             tmem_wait(x);
             tmem_wait(y);
             const RowBlock* const rb = reinterpret_cast<const RowBlock*>(base_ptr + (row_stages - base)) + stage;
-            uint32_t pw[16], dw[16];
+            uint32_t pw[16], dw[16];      // p, and for queries what the rounding of dS left
             // the columns that the row sees: from .. to - 1 (tests of them only where some are masked: they cost as much as the rest)
             const int from = kRole == kQueries ? 0 : (int)max(row - first, (int64_t)0) - 32 * t;
             const int to = (int)min((kRole == kQueries ? row + 1 : tile.end) - first, (int64_t)kStep) - 32 * t;
+            // a row that sees one key: p is 1 and dS 0 (or NaN), whatever the two products' roundings say
+            const bool only = kRole == kQueries && row == tile.start;
+            const int one = (int)max(tile.start - first, (int64_t)-1) - 32 * t;
             auto weights = [&](auto some) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
@@ -352,15 +362,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                         if constexpr (decltype(some)::value) {                 // 0 whatever was multiplied
                             if (e < from || e >= to) a = u = 0.0f;
                             if (e + 1 < from || e + 1 >= to) b = w = 0.0f;
+                            if (kRole == kQueries ? only : e == one) u *= 0.0f;
+                            if (kRole == kQueries ? only : e + 1 == one) w *= 0.0f;
                         }
-                        pw[e / 2] = pack_bf16(a, b);
                         dw[e / 2] = pack_bf16(u, w);
+                        if (kRole == kKeys) {
+                            pw[e / 2] = pack_bf16(a, b);
+                        } else {
+                            excess[h] = add2(excess[h], f2(u, w));
+                            split2(fma2(f2(__uint_as_float(dw[e / 2] << 16), __uint_as_float(dw[e / 2] & 0xFFFF0000u)), minus1, f2(u, w)), a, b);
+                            pw[e / 2] = pack_bf16(a, b);
+                        }
                     }
                 }
             };
             if (masked) weights(std::true_type{});
             else weights(std::false_type{});
-            if (kRole == kKeys) tmem_store16(x_at, pw);
+            tmem_store16(kRole == kKeys ? x_at : x_at + 144, pw);
             tmem_store16(x_at + 128, dw);
             tmem_store_wait();
             if (masked && in < kStep) {      // rows of masked places are not multiplied, not even by 0
@@ -375,6 +393,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         ok = ok && wait(sums_done, 0);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
+        if (kRole == kQueries) {
+            // sum_j p_ij dP_ij is delta_i, and sum_j dS_ij = 0 with it: what is left of the sum is how far off the rounding of out made
+            // delta.  The keys' gradients take the better one.
+            float a, b;
+            split2(add2(excess[0], excess[1]), a, b);
+            float* const halves = reinterpret_cast<float*>(base_ptr);          // over the operands, which are done with
+            if (t == 1) {
+                halves[in] = a + b;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(halves_ready);
+            } else {
+                const bool both = wait(halves_ready, 0) && ok;
+                RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
+                if (row < tile.end) to.delta[in % kStep] = both ? my_delta - (a + b + halves[in]) : __builtin_nanf("");
+                __syncwarp();
+            }
+        }
         // the first four warps take half of dq or dk out, the others the other half or dv
         const bool live = row < tile.end;
         const int which = kRole == kKeys ? t : 0;
@@ -395,7 +430,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
                     *part_at(base_ptr, which, q + k, in) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
-            } else if (live) {
+            } else if (live && o.p) {
                 if (which && *static_cast<volatile int*>(&found)) add_cleared(p, tile, head, row, q, z);
                 store16(to + q, z, p.dim - q, sectors);
                 store16(to + q + 16, z + 16, p.dim - q - 16, sectors);
@@ -483,7 +518,7 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
     a.heads = (int)c.heads, a.kv_heads = (int)c.kv_heads, a.group = (int)(c.heads / c.kv_heads), a.dim = (int)c.dim;
     a.splits = queries ? 1 : key_splits(c);
     a.scale = c.scale;
-    a.rows = static_cast<const RowBlock*>(c.workspace);
+    a.rows = static_cast<RowBlock*>(c.workspace);
     a.a0 = operands[0], a.a1 = operands[1];
     a.out0 = queries ? c.dq : c.dk, a.out1 = c.dv;
     a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
@@ -511,8 +546,8 @@ int launch_attn_backward(const AttnCall& c, cudaStream_t s) {
     // heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and
     // tests of the number of steps between the products cost more than products
     const HeadRows keys[4] = {c.k, c.v, c.q, c.d_out}, queries[4] = {c.q, c.d_out, c.k, c.v};
+    if (!rc) rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);   // delta too
     if (!rc && c.dk.p) rc = c.dim <= 64 ? launch_role<kKeys, 4>(c, keys, s) : launch_role<kKeys, 8>(c, keys, s);
-    if (!rc && c.dq.p) rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);
     return rc;
 }
 

@@ -33,7 +33,8 @@ def test_a_wait_that_runs_out_gives_nan_and_returns(kernel, what, dim, lengths, 
         if not kernel and i == 1:
             x = x.t()[:, :, None]
             bad = x.isnan()
-        reached = {"": (0, 1), "_dq": (0,), "_dkv": (1, 2)}[kernel]
+        # the queries' kernel forms the deltas that the keys' gradients take
+        reached = {"": (0, 1), "_dq": (0, 1), "_dkv": (1, 2)}[kernel]
         assert bool(bad.any()) == (i in reached)
         if i in reached:           # whole rows of the tile, of its head alone
             assert not bad[tile:].any() and not bad[:, 1:].any() and bool(bad[:tile, 0].any())
