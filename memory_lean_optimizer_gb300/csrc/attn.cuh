@@ -25,7 +25,7 @@ struct Sequences {
         if (i == 0) return 0;
         if (i == n + 2) return rows;
         if (!cu) return (int64_t)(i - 1) * (rows / n);
-        return min(max((int64_t)cu[i - 1], (int64_t)0), rows);
+        return min(max((int64_t)__ldg(cu + i - 1), (int64_t)0), rows);
     }
 };
 // bf16 [rows][heads][dim], strides in elements.
@@ -143,30 +143,30 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
 
 // Zeroes the infinities and NaN of a tile in shared memory, thread `i` in row i, for a product with weights of which
 // some are masked: 0 times those is NaN.  True if there was any (then the thread's stores are made visible to the tensor cores).
-// Rows lie 128 bytes apart, so the threads of a warp start at different banks.
+// Rows lie 128 bytes apart, so the threads of a warp start at different banks.  (Eight loads at a time: one by one, each with its test, a
+// row of 128 elements took 1900 cycles, more than the softmax that it ends.)
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {      // an exponent of ones and the bit below it make a carry into the sign's place
+    return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
 template <int kRows>
 __device__ __forceinline__ bool clear_non_finite(char* tile, int dim, int i) {
     bool any = false;
     for (int box = 0; box < (dim > 64 ? 2 : 1); ++box) {
         char* const row = tile + box * kRows * 128 + i * 128;
+        uint4 v[8];
+        uint32_t bad = 0;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            uint4* const at = reinterpret_cast<uint4*>(row + ((q + i) & 7) * 16);
-            const uint4 v = *at;
-            // an exponent of ones and the bit below it make a carry into the sign's place
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t bad = 0;
+        for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const uint4*>(row + ((q + i) & 7) * 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-            if (bad) {
-                any = true;
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t b = ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                    o[k] = w[k] & ~((b >> 15) * 0xFFFFu);
-                }
-                *at = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int q = 0; q < 8; ++q) bad |= non_finite(v[q].x) | non_finite(v[q].y) | non_finite(v[q].z) | non_finite(v[q].w);
+        if (bad) {
+            any = true;
+            auto finite = [](uint32_t w) { return w & ~((non_finite(w) >> 15) * 0xFFFFu); };
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+                uint4* const at = reinterpret_cast<uint4*>(row + q * 16);
+                const uint4 x = *at;
+                *at = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
             }
         }
     }

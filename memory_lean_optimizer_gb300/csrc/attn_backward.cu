@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         tma_prefetch_map(&map_b0);
         tma_prefetch_map(&map_b1);
     }
+    if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
+    tc_fence_before();
     pdl_sync();
     const int heads = kRole == kQueries ? p.heads : p.kv_heads;
     const int rank = kRole == kKeys && p.splits > 1 ? (int)cluster_rank() : 0;
@@ -163,7 +165,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     // the tiles with the most work first: the last queries, the first keys
     const int64_t slot = unit / (unsigned)heads;
     const Tile tile = find_tile<kTile>(p.seq, kRole == kQueries ? p.slots - 1 - slot : slot);
-    if (tile.first >= tile.end) return;
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
+    auto leave = [&]() {
+        if (warp == 2) tmem_free<1>(tmem, 512);
+    };
+    if (tile.first >= tile.end) return leave();
     if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
         const int rows = (int)min((int64_t)kTile, tile.end - tile.first), vecs = p.dim / 8;
         for (int i = threadIdx.x; rank == 0 && i < rows * vecs; i += kAttnThreads) {
@@ -173,7 +180,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             if (kRole == kKeys)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out1.p) + head * p.out1.head + row * p.out1.row + c) = make_uint4(0, 0, 0, 0);
         }
-        return;
+        return leave();
     }
 
     // Streamed blocks: for queries those of the keys up to the tile's last row, for keys those of the queries from the tile's first row
@@ -184,18 +191,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const int all_blocks = per_head * (kRole == kQueries ? 1 : p.group);
     // CTAs of the cluster that take part: each has a start and an end of its own that cost as much as several blocks
     const int splits = kRole == kKeys ? min(p.splits, max(1, all_blocks / kFewBlocks)) : 1;
-    if (rank >= splits) return;
+    if (rank >= splits) return leave();
     const int first_block = (int)((int64_t)all_blocks * rank / splits), blocks = (int)((int64_t)all_blocks * (rank + 1) / splits) - first_block;
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
     const uint32_t stages = base + (kRole == kKeys ? 2 * kTileBytes : 0);   // stage: B0, B1
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
-    if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
     const int stall = head == 0 && rank == 0 && tile.segment == 1 && tile.first == tile.start ? p.stall : 0;
@@ -295,17 +297,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             // Q (four warps) and dO (the others) into tensor memory, two elements a column
             const HeadRows& from = t ? p.a1 : p.a0;
             const uint16_t* const x = static_cast<const uint16_t*>(from.p) + head * from.head + row * from.row;
-#pragma unroll 1
-            for (int h = 0; h < (p.dim > 64 ? 2 : 1); ++h) {
-                uint32_t w[32];
+            uint32_t w[kSteps / 4][32];
+#pragma unroll
+            for (int h = 0; h < kSteps / 4; ++h)
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const bool there = row < tile.end && 64 * h + 2 * k < p.dim;
                     const uint4 v = there ? *reinterpret_cast<const uint4*>(x + 64 * h + 2 * k) : make_uint4(0, 0, 0, 0);
-                    w[k] = v.x, w[k + 1] = v.y, w[k + 2] = v.z, w[k + 3] = v.w;
+                    w[h][k] = v.x, w[h][k + 1] = v.y, w[h][k + 2] = v.z, w[h][k + 3] = v.w;
                 }
-                tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, w);
-            }
+#pragma unroll
+            for (int h = 0; h < kSteps / 4; ++h) tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, w[h]);
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
@@ -322,11 +324,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         for (int i = 0; i < blocks; ++i, stage = stage == kStages - 1 ? 0 : stage + 1, phase ^= stage == 0 ? 1u : 0u) {
             const int64_t first = stream_first + (int64_t)at * kStep;          // the block's first row
             if (++at == per_head) at = 0;
-            // keys behind the row's own, queries before it, or rows behind the sequence
-            const bool masked = kRole == kQueries ? first + kStep > tile.first : first < tile.first + kTile || first + kStep > tile.end;
+            // keys behind a row of the tile, queries before one, or rows behind the sequence: in the block, and among the warp's own
+            const bool partly = kRole == kQueries ? first + kStep > tile.first : first < tile.first + kTile || first + kStep > tile.end;
+            const int64_t top = tile.first + 32 * (warp & 3), left = first + 32 * t;
+            const bool masked = kRole == kQueries ? left + 31 > top : left < top + 31 || left + 32 > tile.end;
             ok = wait(x_done + 8 * (i & 1), i / 2 & 1);
             // what the copies brought is read here too
-            if (ok && (kRole == kKeys || masked)) ok = wait(full + 8 * stage, phase);
+            if (ok && (kRole == kKeys || partly)) ok = wait(full + 8 * stage, phase);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             tmem_store16(kRole == kKeys ? x_at : x_at + 144, pw);
             tmem_store16(x_at + 128, dw);
             tmem_store_wait();
-            if (masked && in < kStep) {      // rows of masked places are not multiplied, not even by 0
+            if (partly && in < kStep) {      // rows of masked places are not multiplied, not even by 0
                 char* const b = base_ptr + (stages - base) + stage * 2 * kStepBytes;
                 if (t == 0) clear_non_finite<kStep>(b, p.dim, in);
                 else if (kRole == kKeys && clear_non_finite<kStep>(b + kStepBytes, p.dim, in)) found = 1;

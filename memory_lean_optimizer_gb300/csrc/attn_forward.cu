@@ -72,11 +72,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
         tma_prefetch_map(&map_k);
         tma_prefetch_map(&map_v);
     }
+    if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
+    tc_fence_before();
     pdl_sync();
     const int head = (int)(blockIdx.x % (unsigned)p.heads);
     // later tiles see more keys: they come first
-    const Tile tile = find_tile<2 * kTile>(p.seq, p.slots - 1 - blockIdx.x / (unsigned)p.heads);
-    if (tile.first >= tile.end) return;
+    const Tile tile = find_tile<2 * kTile>(p.seq, p.slots - 1 - blockIdx.x / (unsigned)p.heads);   // a barrier of the CTA too
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    if (tile.first >= tile.end) {
+        if (warp == 2) tmem_free<1>(tmem, 512);
+        return;
+    }
     uint16_t* const out = p.out + head * p.hso;
     float* const lse = p.lse + (int64_t)head * p.seq.rows;
     if (tile.segment == 0 || tile.segment == p.seq.n + 1) {   // rows of no sequence
@@ -84,17 +91,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
         for (int i = threadIdx.x; i < rows * vecs; i += kAttnThreads)
             *reinterpret_cast<uint4*>(out + (tile.first + i / vecs) * p.ldo + i % vecs * 8) = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; i < rows; i += kAttnThreads) lse[tile.first + i] = 0.0f;
+        if (warp == 2) tmem_free<1>(tmem, 512);
         return;
     }
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
     const uint32_t q_tile = base, k_tile = base + 2 * kTileBytes, v_tile = k_tile + kStages * kTileBytes;
-    if (warp == 2) tmem_alloc<1>(smem_u32(&tmem_base), 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base;
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
     const int left = (int)min(tile.end - tile.first, (int64_t)(2 * kTile));     // rows of the two tiles
@@ -200,10 +203,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             for (int q = 0; q < 4; ++q) tmem_wait(x[q]);
             if (j == n - 1) {      // the tile's own block: keys behind the row
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4; ++q) {
+                    if (q < (warp & 3)) continue;
+                    const int seen = q == (warp & 3) ? lane : -1;
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (32 * q + k > in) x[q][k] = 0xFF800000u;
+                        if (k > seen) x[q][k] = 0xFF800000u;
+                }
             }
             float top[4];
 #pragma unroll
@@ -278,22 +284,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             if (live) lse[row] = ok ? (m + log2f(sum)) * kLn2 : __builtin_nanf("");
             // blocks whose values were cleared: the first tile's own (seen by both), the second's own
             const bool had0 = *static_cast<volatile int*>(&found[0]) != 0, had1 = t && *static_cast<volatile int*>(&found[1]) != 0;
-#pragma unroll 1
-            for (int q = 0; q < p.dim; q += 32) {
-                uint32_t o[32];
-                tmem_load32(o_at + q, o);
-                tmem_wait(o);
-                if (live) {
-                    float y[32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
-                    if (had0 || had1) {
-                        const uint16_t* const v = p.v + (int64_t)(head / p.group) * p.hsv;
-                        if (had0) add_non_finite(y, v, p.ldv, tile.first, min(tile.first + kTile, row + 1), q, p.dim);
-                        if (had1) add_non_finite(y, v, p.ldv, tile.first + kTile, row + 1, q, p.dim);
+            for (int h = 0; h < kSteps / 4; ++h) {
+                uint32_t o[2][32];
+                tmem_load32(o_at + 64 * h, o[0]);
+                tmem_load32(o_at + 64 * h + 32, o[1]);
+                tmem_wait(o[0]);
+                tmem_wait(o[1]);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int q = 64 * h + 32 * i;
+                        float y[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[i][k]) * inv;
+                        if (had0 || had1) {
+                            const uint16_t* const v = p.v + (int64_t)(head / p.group) * p.hsv;
+                            if (had0) add_non_finite(y, v, p.ldv, tile.first, min(tile.first + kTile, row + 1), q, p.dim);
+                            if (had1) add_non_finite(y, v, p.ldv, tile.first + kTile, row + 1, q, p.dim);
+                        }
+                        store16(to + q, y, p.dim - q, sectors);
+                        store16(to + q + 16, y + 16, p.dim - q - 16, sectors);
                     }
-                    store16(to + q, y, p.dim - q, sectors);
-                    store16(to + q + 16, y + 16, p.dim - q - 16, sectors);
                 }
                 __syncwarp();
             }
