@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             float top[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
+                top[q] = __uint_as_float(x[q][0]);
 #pragma unroll
-                for (int k = 2; k < 32; k += 2) top[q] = max3(top[q], __uint_as_float(x[q][k]), __uint_as_float(x[q][k + 1]));
+                for (int k = 1; k < 32; ++k) top[q] = fmaxf(top[q], __uint_as_float(x[q][k]));
             }
             const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grow = now > m + kSlack;
