@@ -357,3 +357,59 @@ def test_long():
         r = es + es.amax(1, keepdim=True) + 8 * U
         mag = p @ v[:, 0].double().abs()
         assert within(out[rows, h], p @ v[:, 0].double(), 1.25 * ((p * (B + 2 * r)) @ v[:, 0].double().abs() + n * 2 * U * mag))
+
+
+@pytest.mark.parametrize("count", [300, 700, 3000])
+def test_more_sequences_than_threads(count):
+    """Tiles are looked up in one round of borders for as many sequences as a CTA has threads (256 and 384), in several for more."""
+    from memory_lean_optimizer_gb300 import block
+    g = torch.Generator().manual_seed(count)
+    lengths = torch.randint(0, 6, (count,), generator=g)
+    lengths[count // 3], lengths[-2] = 200, 130
+    n = int(lengths.sum())
+    q, k, v, do = inputs(n + 9, 2, 1, 32)
+    cu = torch.cat((torch.zeros(1, dtype=torch.int64), lengths.cumsum(0))).to(torch.int32).cuda()
+    out, lse = block.attention_forward(q, k, v, cu)
+    got = (out, lse.t()[..., None], *block.attention_backward(do, q, k, v, out, lse, cu))
+    # the same sequences one by one, in a few places
+    at = cu.tolist()
+    for i in (0, 1, count // 3, count // 2, count - 2, count - 1):
+        s = slice(at[i], at[i + 1])
+        if at[i] == at[i + 1]:
+            continue
+        o, l = block.attention_forward(q[s], k[s], v[s])
+        alone = (o, l.t()[..., None], *block.attention_backward(do[s], q[s], k[s], v[s], o, l))
+        assert all(torch.equal(a[s], b) for a, b in zip(got, alone)), i
+    assert not any(t[n:].any() for t in got)
+    # and all of them against one batch of sequences of three
+    if count == 700:
+        three = torch.arange(0, n // 3 * 3 + 1, 3, dtype=torch.int32, device="cuda")
+        m = n // 3 * 3
+        a = block.attention_forward(q[:m], k[:m], v[:m], three)[0]
+        b = block.attention_forward(*(t[:m].view(m // 3, 3, -1, 32) for t in (q, k, v)))[0]
+        assert torch.equal(a, b.flatten(0, 1))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, among them the cross entropy's products, which use tensor memory too: each as by itself."""
+    from memory_lean_optimizer_gb300 import block, head
+    sets = [inputs(600 + 100 * i, 8, 2, 64, seed=i) for i in range(2)]
+    h, w = torch.randn(300, 256, device="cuda").to(BF), torch.randn(5000, 256, device="cuda").to(BF)
+    t = torch.randint(5000, (300,), device="cuda")
+
+    def work(i):
+        q, k, v, do = sets[i]
+        out, lse = block.attention_forward(q, k, v)
+        return (out, lse, *block.attention_backward(do, q, k, v, out, lse), *head.xent_forward(h, w, t))
+    want = [work(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
