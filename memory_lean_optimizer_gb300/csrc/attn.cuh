@@ -93,10 +93,8 @@ inline int make_head_map(CUtensorMap* map, const void* base, int64_t rows, int64
     if (rows == 1) ld = heads * dim;
     const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const CUresult r = encode_bf16_map(fn, map, 3, base, dims, strides, box);
     if (r != CUDA_SUCCESS)
         return set_error(OPTIM_ECUDA, "tensor map of %lld x %lld heads of %lld: error %d", (long long)rows, (long long)heads, (long long)dim, (int)r);
     return OPTIM_OK;

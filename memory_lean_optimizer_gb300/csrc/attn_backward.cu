@@ -22,27 +22,18 @@ namespace {
 constexpr int kTile = 128, kStep = 64;           // rows of a CTA's tile and of a streamed block
 constexpr int kAttnThreads = 384;                // warp 0 copies, warp 1 multiplies, warp 2 holds tensor memory; 4-11: p and dS
 constexpr uint32_t kTileBytes = kTile * 256, kStepBytes = kStep * 256;
-// Stages of a pair of blocks; a tile of queries is in tensor memory and leaves its place to more of them.
-__host__ __device__ constexpr int stages_of(int role) { return role == 0 ? 6 : 4; }
+constexpr int kStages = 4;                       // of a pair of streamed blocks
 constexpr int kFewBlocks = 12;
-constexpr size_t kSmem = 6 * 2 * kStepBytes + 4 * kStep * 8 + 1024;
+// Tiles of the CTA's own rows in shared memory: Q, dO and out (which go into tensor memory, or into delta), or K and V.
+__host__ __device__ constexpr int own_tiles(int role) { return role == 0 ? 3 : 2; }
+__host__ __device__ constexpr size_t smem_of(int role) {
+    return own_tiles(role) * kTileBytes + kStages * (2 * kStepBytes + (role == 0 ? 0 : kStep * 8)) + 1024;
+}
 
 // The rows' -lse (times log2 e) and -delta, by blocks of 64 rows of a sequence: 64 of one, 64 of the other.  Blocks are numbered as tiles
 // of 64 (find_tile), `slots` a head; rows behind a sequence's end have -inf (p is 0) and 0.
 struct RowBlock {
     float lse[kStep], delta[kStep];
-};
-
-struct PrepArgs {
-    Sequences seq;
-    int64_t slots;
-    int32_t heads, dim;
-    const uint16_t* out;
-    int64_t ldo, hso;
-    const uint16_t* d_out;
-    int64_t lddo, hsdo;
-    const float* lse;
-    RowBlock* rows;
 };
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
@@ -56,32 +47,6 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
     return s;
 }
 
-// A block of 64 rows of one head to a CTA: four threads to a row.
-__global__ void __launch_bounds__(256) k_attn_rows(const PrepArgs p) {
-    pdl_sync();
-    const int head = (int)(blockIdx.x % (unsigned)p.heads);
-    const int64_t slot = blockIdx.x / (unsigned)p.heads;
-    const Tile tile = find_tile<kStep>(p.seq, slot);
-    if (tile.first >= tile.end || tile.segment == 0 || tile.segment == p.seq.n + 1) return;
-    const int in = threadIdx.x >> 2, part = threadIdx.x & 3;
-    const int64_t row = tile.first + in;
-    const bool live = row < tile.end;
-    float s = 0.0f;
-    if (live) {
-        const uint16_t* const o = p.out + row * p.ldo + head * p.hso;
-        const uint16_t* const g = p.d_out + row * p.lddo + head * p.hsdo;
-        for (int c = 8 * part; c < p.dim; c += 32)
-            s += dot8(*reinterpret_cast<const uint4*>(o + c), *reinterpret_cast<const uint4*>(g + c));
-    }
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-    if (part == 0) {
-        RowBlock& b = p.rows[head * p.slots + slot];
-        b.lse[in] = live ? p.lse[head * p.seq.rows + row] * -kLog2e : -INFINITY;
-        b.delta[in] = live ? -s : 0.0f;
-    }
-}
-
 enum { kQueries = 0, kKeys = 1 };
 
 struct BackwardArgs {
@@ -91,7 +56,7 @@ struct BackwardArgs {
     int32_t splits;                     // kKeys: CTAs (a cluster) that share a tile's blocks
     float scale;
     RowBlock* rows;
-    HeadRows a0, a1;                    // kQueries: Q, dO
+    const float* lse;                   // kQueries
     HeadRows out0, out1;                // dq; or dk, dv
     const uint16_t* d_out;              // kKeys: for what is taken out of masked blocks
     int64_t lddo, hsdo;
@@ -119,23 +84,24 @@ __device__ __forceinline__ float4* part_at(char* base, int which, int c, int row
     return reinterpret_cast<float4*>(base + which * (kTile * 512)) + (c / 4) * kTile + row;
 }
 
-// maps: the tile's operands (a0, a1), the streamed ones (b0, b1): Q, dO, K, V for queries, K, V, Q, dO for keys
+// maps: the tile's operands (a0, a1), the streamed ones (b0, b1): Q, dO, K, V for queries (and out), K, V, Q, dO for keys
 template <int kRole, int kSteps>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
                                                                    const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
-                                                                   const BackwardArgs p) {
-    constexpr int kStages = stages_of(kRole);
+                                                                   const __grid_constant__ CUtensorMap map_out, const BackwardArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 3];
+    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 5];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found, copied;
+    __shared__ float tile_delta[kRole == kQueries ? kTile : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // before anything of the stream is needed
     const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
-                   sums_done = ready + 16, drained = sums_done + 8, halves_ready = drained + 8;
+                   sums_done = ready + 16, drained = sums_done + 8, halves_ready = drained + 8, delta_ready = halves_ready + 8, tile_full = delta_ready + 8;
     if (threadIdx.x == 0) {
         gave_up = found = copied = 0;
-        mbar_init(a_full, kRole == kKeys ? 1 : 8);
+        mbar_init(a_full, 8);
+        mbar_init(tile_full, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
@@ -147,11 +113,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         mbar_init(sums_done, 1);
         mbar_init(drained, 1);
         mbar_init(halves_ready, 4);
+        mbar_init(delta_ready, 4);
         mbar_init_fence();
-        if (kRole == kKeys) {
-            tma_prefetch_map(&map_a0);
-            tma_prefetch_map(&map_a1);
-        }
+        tma_prefetch_map(&map_a0);
+        tma_prefetch_map(&map_a1);
+        if (kRole == kQueries) tma_prefetch_map(&map_out);
         tma_prefetch_map(&map_b0);
         tma_prefetch_map(&map_b1);
     }
@@ -196,7 +162,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     char* const base_ptr = reinterpret_cast<char*>(smem_raw) + (base - smem_u32(smem_raw));
-    const uint32_t stages = base + (kRole == kKeys ? 2 * kTileBytes : 0);   // stage: B0, B1
+    const uint32_t stages = base + own_tiles(kRole) * kTileBytes;      // stage: B0, B1
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
@@ -207,11 +173,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         if (warp == 0 && elect_lane()) {
             const int stop = stall == kStallCopy ? 0 : 0x7FFFFFFF;
             const uint32_t boxes = p.dim > 64 ? 2 : 1;
-            if (kRole == kKeys) {
-                mbar_expect_tx(a_full, 2 * boxes * kTile * 128);
-                load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, a_full);
-                load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, a_full);
-            }
+            mbar_expect_tx(tile_full, own_tiles(kRole) * boxes * kTile * 128);
+            load_rows<kTile>(base, &map_a0, p.dim, head, tile.first, tile_full);
+            load_rows<kTile>(base + kTileBytes, &map_a1, p.dim, head, tile.first, tile_full);
+            if (kRole == kQueries) load_rows<kTile>(base + 2 * kTileBytes, &map_out, p.dim, head, tile.first, tile_full);
             int issued = 0, in = first_block % per_head;
             int of = kRole == kQueries ? head / p.group : head * p.group + first_block / per_head;     // head of the streamed operands
             const int64_t row_slot = kRole == kKeys ? (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep : 0;
@@ -238,7 +203,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             constexpr uint32_t desc_x = mma_desc(128, kStep, false, false), desc_sum = mma_desc(128, kSteps * 16, false, true);
             constexpr uint32_t up = desc_upper(1024);
             const uint32_t a_lo = desc_lower(base, 8192), b_lo = desc_lower(stages, kStep * 128);
-            bool ok = wait(a_full, 0);
+            bool ok = wait(kRole == kKeys ? tile_full : a_full, 0);
             tc_fence_after();
             uint32_t next = 0, parity = 0, stage = 0;       // of the block whose scores, and whose sums, come next
             auto scores = [&](int i) {
@@ -294,27 +259,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         const F2 c2 = f2(c, c);
         float my_lse = 0.0f, my_delta = 0.0f;
         if (kRole == kQueries) {
-            // Q (four warps) and dO (the others) into tensor memory, two elements a column
-            const HeadRows& from = t ? p.a1 : p.a0;
-            const uint16_t* const x = static_cast<const uint16_t*>(from.p) + head * from.head + row * from.row;
-            uint32_t w[kSteps / 4][32];
+            // Q (four warps) and dO (the others) into tensor memory, two elements a column; delta from out as it was rounded.  (Rows come in by
+            // copies: a lane's own row read from memory takes a line of every lane for each 16 bytes, 3 us a tile.)
+            wait(tile_full, 0);
+            const char* const mine = base_ptr + t * kTileBytes + in * 128;
+            float s[4] = {};
 #pragma unroll
-            for (int h = 0; h < kSteps / 4; ++h)
+            for (int h = 0; h < kSteps / 4; ++h) {
+                uint32_t r[32];
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const bool there = row < tile.end && 64 * h + 2 * k < p.dim;
-                    const uint4 v = there ? *reinterpret_cast<const uint4*>(x + 64 * h + 2 * k) : make_uint4(0, 0, 0, 0);
-                    w[h][k] = v.x, w[h][k + 1] = v.y, w[h][k + 2] = v.z, w[h][k + 3] = v.w;
+                for (int k = 0; k < 8; ++k) {
+                    const int at = h * kTile * 128 + (k ^ (in & 7)) * 16;      // of the eighth elements from 64 h + 8 k on
+                    const uint4 v = *reinterpret_cast<const uint4*>(mine + at);
+                    r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                    if (t == 1) s[k & 3] += dot8(*reinterpret_cast<const uint4*>(mine + kTileBytes + at), v);
                 }
-#pragma unroll
-            for (int h = 0; h < kSteps / 4; ++h) tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, w[h]);
+                tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, r);
+            }
+            my_delta = -((s[0] + s[1]) + (s[2] + s[3]));
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(a_full);
-            // tiles of 128 start at a block of 64
-            const RowBlock& b = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
-            if (row < tile.end) my_lse = b.lse[in % kStep], my_delta = b.delta[in % kStep];
+            my_lse = row < tile.end ? p.lse[head * p.seq.rows + row] * -kLog2e : -INFINITY;
+            if (t == 1) {
+                tile_delta[in] = my_delta;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(delta_ready);
+            } else {
+                wait(delta_ready, 0);
+                my_delta = tile_delta[in];
+            }
         }
         F2 excess[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};                       // sum of dS
         const F2 minus1 = f2(-1.0f, -1.0f), my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
@@ -409,8 +384,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (lane == 0) mbar_arrive(halves_ready);
             } else {
                 const bool both = wait(halves_ready, 0) && ok;
+                // tiles of 128 start at a block of 64
                 RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
-                if (row < tile.end) to.delta[in % kStep] = both ? my_delta - (a + b + halves[in]) : __builtin_nanf("");
+                if (tile.first + in / kStep * kStep < tile.end) {
+                    to.lse[in % kStep] = my_lse;
+                    to.delta[in % kStep] = row >= tile.end ? 0.0f : both ? my_delta - (a + b + halves[in]) : __builtin_nanf("");
+                }
                 __syncwarp();
             }
         }
@@ -480,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         if (warp == 0 && elect_lane()) {
             const int n = copied;
-            if (kRole == kKeys) mbar_drain(a_full, 0);
+            mbar_drain(tile_full, 0);
             for (int i = max(0, n - kStages); i < n; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1);
         }
         __syncthreads();
@@ -507,14 +486,15 @@ int key_splits(const AttnCall& c) {
 template <int kRole, int kSteps>
 int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s) {
     const bool queries = kRole == kQueries;
-    CUtensorMap map[4];
-    for (int i = 0; i < 4; ++i) {
-        const HeadRows& t = operands[i];
-        const int rc = make_head_map(&map[i], t.p, c.seq.rows, (i < 2) == queries ? c.heads : c.kv_heads, c.dim, t.row, t.head, i < 2 ? kTile : kStep);
+    CUtensorMap map[5] = {};
+    for (int i = 0; i < (queries ? 5 : 4); ++i) {
+        const HeadRows& t = i < 4 ? operands[i] : c.out;
+        const bool own = i < 2 || i == 4;
+        const int rc = make_head_map(&map[i], t.p, c.seq.rows, own == queries ? c.heads : c.kv_heads, c.dim, t.row, t.head, own ? kTile : kStep);
         if (rc) return rc;
     }
     static std::atomic<uint64_t> allowed{0};
-    const int rc = allow_smem(k_attn_backward<kRole, kSteps>, (int)kSmem, allowed);
+    const int rc = allow_smem(k_attn_backward<kRole, kSteps>, (int)smem_of(kRole), allowed);
     if (rc) return rc;
     BackwardArgs a{};
     a.seq = c.seq;
@@ -523,13 +503,13 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
     a.splits = queries ? 1 : key_splits(c);
     a.scale = c.scale;
     a.rows = static_cast<RowBlock*>(c.workspace);
-    a.a0 = operands[0], a.a1 = operands[1];
+    a.lse = c.lse;
     a.out0 = queries ? c.dq : c.dk, a.out1 = c.dv;
     a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
     a.stall = faults_injected() ? injected_stall(kRole) : 0;
     a.wait_ns = a.stall ? kWaitNs / 40 : kWaitNs;
-    return check_cuda(launch_after(k_attn_backward<kRole, kSteps>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads) * a.splits), kAttnThreads, kSmem, a.splits, s,
-                                   map[0], map[1], map[2], map[3], a),
+    return check_cuda(launch_after(k_attn_backward<kRole, kSteps>, (unsigned)(a.slots * (queries ? c.heads : c.kv_heads) * a.splits), kAttnThreads, smem_of(kRole), a.splits, s,
+                                   map[0], map[1], map[2], map[3], map[4], a),
                       "attention backward launch");
 }
 
@@ -538,19 +518,10 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
 size_t attn_workspace_bytes(const AttnCall& c) { return (size_t)tile_slots(c.seq, kStep) * c.heads * sizeof(RowBlock); }
 
 int launch_attn_backward(const AttnCall& c, cudaStream_t s) {
-    PrepArgs a{};
-    a.seq = c.seq;
-    a.slots = tile_slots(c.seq, kStep);
-    a.heads = (int)c.heads, a.dim = (int)c.dim;
-    a.out = static_cast<const uint16_t*>(c.out.p), a.ldo = c.out.row, a.hso = c.out.head;
-    a.d_out = static_cast<const uint16_t*>(c.d_out.p), a.lddo = c.d_out.row, a.hsdo = c.d_out.head;
-    a.lse = c.lse;
-    a.rows = static_cast<RowBlock*>(c.workspace);
-    int rc = check_cuda(launch_after(k_attn_rows, (unsigned)(a.slots * c.heads), 256, 0, 1, s, a), "attention backward launch");
     // heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and
     // tests of the number of steps between the products cost more than products
     const HeadRows keys[4] = {c.k, c.v, c.q, c.d_out}, queries[4] = {c.q, c.d_out, c.k, c.v};
-    if (!rc) rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);   // delta too
+    int rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);   // delta too
     if (!rc && c.dk.p) rc = c.dim <= 64 ? launch_role<kKeys, 4>(c, keys, s) : launch_role<kKeys, 8>(c, keys, s);
     return rc;
 }

@@ -22,4 +22,22 @@ inline EncodeFn encode_fn() {
     return fn;
 }
 
+// Encodes a map of bf16 in boxes of 64 elements (128 bytes, swizzled).  A thread whose first CUDA call this is has no context yet (one
+// of autograd's, say): the runtime makes it current.
+inline CUresult encode_bf16_map(EncodeFn fn, CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                                const cuuint32_t* box) {
+    static constexpr cuuint32_t one[3] = {1, 1, 1};
+    auto encode = [&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        int device = 0;
+        if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = encode();
+    }
+    return r;
+}
+
 }  // namespace lmo

@@ -860,10 +860,8 @@ int make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int
     EncodeFn fn = encode_fn();
     if (!fn) return set_error(OPTIM_ECUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const CUresult r = encode_bf16_map(fn, map, 2, base, dims, strides, box);
     if (r != CUDA_SUCCESS) return set_error(OPTIM_ECUDA, "tensor map of a %lld x %lld matrix: error %d", (long long)rows, (long long)cols, (int)r);
     return OPTIM_OK;
 }

@@ -413,3 +413,33 @@ def test_two_streams_at_once():
     for i in range(2):
         for run in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
+
+
+def test_first_calls_of_a_thread():
+    """In a thread that has made no CUDA call yet (nothing to allocate either: the allocator has the memory)."""
+    import threading
+    from memory_lean_optimizer_gb300 import block, head
+    q, k, v, do = inputs(200, 4, 2, 64)
+    h, w, t = q.flatten(1), torch.randn(3000, 256, device="cuda").to(BF), torch.randint(3000, (200,), device="cuda")
+    want = block.attention_forward(q, k, v)
+    grads = block.attention_backward(do, q, k, v, *want)
+    loss = head.xent_forward(h, w, t)
+    x = head.xent_backward(h, w, t, loss[1], torch.ones_like(loss[0]))
+    del grads
+    grads = block.attention_backward(do, q, k, v, *want)
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: block.attention_forward(q, k, v), want), (lambda: block.attention_backward(do, q, k, v, *want), grads),
+                      (lambda: head.xent_forward(h, w, t), loss), (lambda: head.xent_backward(h, w, t, loss[1], torch.ones_like(loss[0])), x),
+                      (lambda: (block.unpack_activation(block.pack_activation(q)),), (block.unpack_activation(block.pack_activation(q)),))):
+        got, error = [], []
+
+        def run():
+            try:
+                got.extend(call())
+            except Exception as e:      # a thread's exceptions stay in it
+                error.append(e)
+        thread = threading.Thread(target=run)
+        thread.start()
+        thread.join()
+        torch.cuda.synchronize()
+        assert not error and all(torch.equal(a, b) for a, b in zip(got, ref)), error
