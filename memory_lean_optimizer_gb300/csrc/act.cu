@@ -23,7 +23,7 @@
 namespace lmo {
 namespace {
 
-constexpr int kActThreads = 256;
+constexpr int kActThreads = 128;
 constexpr int kBlock = 32, kPer = 16;      // elements that share an exponent; elements to a thread
 constexpr uint32_t kNoExponent = 255;      // of a block with an infinity or a NaN
 
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kActThreads) k_swiglu_forward(const ActArgs p)
 }
 
 template <class T, bool kVec>
-__global__ void __launch_bounds__(kActThreads) k_swiglu_backward(const ActArgs p) {
+__global__ void __launch_bounds__(kActThreads, 10) k_swiglu_backward(const ActArgs p) {
     const Turn turn = turn_of<kVec>();
     pdl_sync();
     const Place at(p);

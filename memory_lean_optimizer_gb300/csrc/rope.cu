@@ -74,7 +74,7 @@ __device__ __forceinline__ void store(T* p, const Piece<T, V>& r) {
 }
 
 // A head is cut into units: first those that turn (two pieces of V elements half the rotated part
-// apart, or one piece of V / 2 neighbouring pairs), then pieces that are copied (nothing to do in place).
+// apart, or one piece of V / 2 neighbouring pairs), then pieces that are copied.
 template <class T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs p) {
     extern __shared__ float2 table[];      // [tokens][rotary / 2]: cosine and sine, times the factor
@@ -102,53 +102,65 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs p) {
     constexpr int kStep = !kInterleaved ? V : V > 1 ? V / 2 : 1;      // pairs to a unit
     const int turning = half / kStep, units = turning + (p.dim - p.rotary) / V;
     const int all = (p.t[0].heads + p.t[1].heads) * units;
-    int token = 0, rest = (int)threadIdx.x;                  // unit `rest` of that token
+    constexpr bool kSingles = kInterleaved && V == 1;                 // pairs that are not aligned to pairs
+    struct Unit {
+        const T* x;
+        T* y;
+        int pair;              // its first pair of the table, or -1: copied
+        bool live;
+        Piece<T, V> a, b;
+    };
+    // two units at a time, so that one's loads do not wait for the other's stores
+    int token = 0, rest = (int)threadIdx.x;                           // unit `rest` of that token
     for (;;) {
-        while (rest >= all) rest -= all, ++token;
-        if (token >= n) break;
-        {
-            const float2* const cs = table + token * half;
+        Unit unit[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            Unit& w = unit[j];
+            while (rest >= all) rest -= all, ++token;
+            w.live = token < n;
             int head = p.per_head ? (int)__umulhi((uint32_t)rest, p.per_head) : rest / units;
             const int u = rest - head * units;
             const bool second = head >= p.t[0].heads;
             const RopeTensor& t = second ? p.t[1] : p.t[0];
             if (second) head -= p.t[0].heads;
-            const T* const x = static_cast<const T*>(t.x) + (first + token) * t.ldx + head * t.hsx;
-            T* const y = static_cast<T*>(t.y) + (first + token) * t.ldy + head * t.hsy;
-            if (u >= turning) {
-                const int c = p.rotary + (u - turning) * V;
-                store<T, V>(y + c, load<T, V>(x + c));
-            } else if (kInterleaved && V == 1) {
-                const float2 r = cs[u];
-                const float f = value(x[2 * u]), g = value(x[2 * u + 1]);
-                put(y[2 * u], fmaf(f, r.x, -(g * r.y)));
-                put(y[2 * u + 1], fmaf(g, r.x, f * r.y));
-            } else if (kInterleaved) {
-                const int c = u * V;
-                Piece<T, V> a = load<T, V>(x + c);
-#pragma unroll
-                for (int k = 0; k + 1 < V; k += 2) {
-                    const float2 r = cs[c / 2 + k / 2];
-                    const float f = value(a.e[k]), g = value(a.e[k + 1]);
-                    put(a.e[k], fmaf(f, r.x, -(g * r.y)));
-                    put(a.e[k + 1], fmaf(g, r.x, f * r.y));
-                }
-                store<T, V>(y + c, a);
-            } else {
-                const int c = u * V;
-                Piece<T, V> a = load<T, V>(x + c), b = load<T, V>(x + c + half);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float2 r = cs[c + k];
-                    const float f = value(a.e[k]), g = value(b.e[k]);
-                    put(a.e[k], fmaf(f, r.x, -(g * r.y)));
-                    put(b.e[k], fmaf(g, r.x, f * r.y));
-                }
-                store<T, V>(y + c, a);
-                store<T, V>(y + c + half, b);
+            const int c = u >= turning ? p.rotary + (u - turning) * V : kSingles ? 2 * u : u * V;
+            w.x = static_cast<const T*>(t.x) + (first + token) * t.ldx + head * t.hsx + c;
+            w.y = static_cast<T*>(t.y) + (first + token) * t.ldy + head * t.hsy + c;
+            w.pair = u >= turning ? -1 : token * half + u * kStep;
+            if (w.live) {
+                w.a = load<T, V>(w.x);
+                if (w.pair >= 0 && (kSingles || !kInterleaved)) w.b = load<T, V>(w.x + (kSingles ? 1 : half));
             }
+            rest += kRopeThreads;
         }
-        rest += kRopeThreads;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            Unit& w = unit[j];
+            if (!w.live) return;
+            if (w.pair >= 0) {
+                const float2* const cs = table + w.pair;
+                if (kInterleaved && !kSingles) {
+#pragma unroll
+                    for (int k = 0; k + 1 < V; k += 2) {
+                        const float2 r = cs[k / 2];
+                        const float f = value(w.a.e[k]), g = value(w.a.e[k + 1]);
+                        put(w.a.e[k], fmaf(f, r.x, -(g * r.y)));
+                        put(w.a.e[k + 1], fmaf(g, r.x, f * r.y));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const float2 r = cs[k];
+                        const float f = value(w.a.e[k]), g = value(w.b.e[k]);
+                        put(w.a.e[k], fmaf(f, r.x, -(g * r.y)));
+                        put(w.b.e[k], fmaf(g, r.x, f * r.y));
+                    }
+                    store<T, V>(w.y + (kSingles ? 1 : half), w.b);
+                }
+            }
+            store<T, V>(w.y, w.a);
+        }
     }
 }
 
