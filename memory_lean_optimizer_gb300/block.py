@@ -196,6 +196,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: tor
 
 # ---------------------------------------------------------------------------------- rotary positions
 _PI = Fraction(3141592653589793238462643383279502884197169399375105820974944592307816406286208998, 10 ** 81)
+_TURN_BITS = 256
+_TURNS_PER_RADIAN = round(2 ** _TURN_BITS / (2 * _PI))
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -233,7 +235,11 @@ class RotaryPlan:
                  factor: float = 1.0, original_length: int | None = None, device="cuda"):
         freq, self.factor = rotary_frequencies(rotary_dim, base, scaling, factor, original_length)
         self.rotary_dim, self.interleaved = rotary_dim, interleaved
-        turns = [round(Fraction(f) / (2 * _PI) * 2 ** 64) % 2 ** 64 for f in freq]
+        turns = []
+        for f in freq:
+            num, den = f.as_integer_ratio()            # den is a power of two: the quotient is a shift
+            shift = den.bit_length() - 1 + _TURN_BITS - 64
+            turns.append((num * _TURNS_PER_RADIAN + (1 << shift - 1) >> shift) % 2 ** 64)
         self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device=device)
 
     def tensors(self):

@@ -3,15 +3,27 @@
 //   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i   (i: of all heads that share j)
 // Scores are formed again.  Two product kernels, one for dq (a tile of queries, the keys stream by) and one for dk and
 // dv (a tile of keys, the queries of the group's heads stream by): every sum has one owner and one order, at the
-// price of forming p and dS twice (7 products, not 5); adding dq up from the tiles of keys would need atomics, whose order changes
+// price of forming p and dS twice (8 products, not 5); adding dq up from the tiles of keys would need atomics, whose order changes
 // results, or a buffer of fp32.
 //
-// Both are one kernel in two roles.  A CTA holds two operands of 128 rows (Q and dO, or K and V) and streams pairs of
-// blocks of 64 rows of the other two.  X = A0 B0' and Y = A1 B1' go into one of two pairs of accumulators (64 columns each), four warps
-// turn them into p and dS, in bf16, in place (the tensor cores want both operands of one type), and those are the A operands, from tensor
-// memory, of the sums' products (with B0 and B1 read along their rows).  For keys X and Y are the transposed
+// Both are one kernel in two roles.  A CTA holds two operands of 128 rows (Q and dO, in tensor memory, or K and V, in shared memory) and
+// streams pairs of blocks of 64 rows of the other two.  X = A0 B0' and Y = A1 B1' go into one of two pairs of accumulators (64 columns
+// each), eight warps turn them into p and dS, in bf16, in place (the tensor cores want both operands of one type), and those are the A
+// operands, from tensor memory, of the sums' products (with B0 and B1 read along their rows).  For keys X and Y are the transposed
 // scores: nothing is ever transposed through shared memory.  Blocks of 64 so that two pairs and the two sums fit in the 512
-// columns; while four warps work on one pair the tensor cores fill the other.
+// columns; while the warps work on one pair the tensor cores fill the other.
+//
+// What bf16 costs.  dq, dk and dv are rounded once (1.65e-3 in the 2-norm); p and dS once before (as much again in dk and dv).  delta from out as
+// the forward pass rounded it would add 1.2e-3 to dq and dk: instead dq's kernel sums its dS (sum_j dS_ij = 0 with the true delta), and the keys'
+// kernel takes delta without that excess; dq itself, which cannot, takes dS in two bf16 parts (a product more).  Against 64 bits
+// all three are within 2.4e-3; with dS in one part and that delta 2.6e-3.
+//
+// Many rows: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: dq 1.23 ms, dk and dv 1.25 ms, together 8 products of
+// 0.55e12 operations at 1.77 PFLOP/s (a library product in a burst: 1.93).  128 x 64 scores from shared memory take 48 cycles for 16 elements of
+// the head where 32 would do (128 bytes a cycle); Q and dO in tensor memory free dq's of it.  A lone CTA takes 7 us from its start to its end, of
+// which two blocks are 1.3: texts of 1 to 2035 tokens (11287 rows, 12 / 3 heads of 80) take 203 us, of which the products are 58.
+// What the warps' part cost before: tests of masked places in every block (one set of instructions in two), operands read row by row
+// from memory (a line a lane, 3 us a tile), a wait that reads the timer (half of the waits last less).
 #include <type_traits>
 
 #include "attn.cuh"
@@ -258,10 +270,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         const float c = p.scale * kLog2e;
         const F2 c2 = f2(c, c);
         float my_lse = 0.0f, my_delta = 0.0f;
+        bool ok = true;
         if (kRole == kQueries) {
             // Q (four warps) and dO (the others) into tensor memory, two elements a column; delta from out as it was rounded.  (Rows come in by
             // copies: a lane's own row read from memory takes a line of every lane for each 16 bytes, 3 us a tile.)
-            wait(tile_full, 0);
+            ok = wait(tile_full, 0);
             const char* const mine = base_ptr + t * kTileBytes + in * 128;
             float s[4] = {};
 #pragma unroll
@@ -287,16 +300,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(delta_ready);
             } else {
-                wait(delta_ready, 0);
+                ok = wait(delta_ready, 0) && ok;
                 my_delta = tile_delta[in];
             }
         }
         F2 excess[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};                       // sum of dS
         const F2 minus1 = f2(-1.0f, -1.0f), my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
         int at = first_block % per_head;                                       // the block's place in its head
-        bool ok = true;
+        ok = __all_sync(0xFFFFFFFFu, ok);
         uint32_t stage = 0, phase = 0;
-        for (int i = 0; i < blocks; ++i, stage = stage == kStages - 1 ? 0 : stage + 1, phase ^= stage == 0 ? 1u : 0u) {
+        for (int i = 0; ok && i < blocks; ++i, stage = stage == kStages - 1 ? 0 : stage + 1, phase ^= stage == 0 ? 1u : 0u) {
             const int64_t first = stream_first + (int64_t)at * kStep;          // the block's first row
             if (++at == per_head) at = 0;
             // keys behind a row of the tile, queries before one, or rows behind the sequence: in the block, and among the warp's own
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             __syncwarp();
             if (lane == 0 && stall != kStallSoftmax) mbar_arrive(ready + 8 * (i & 1));
         }
-        ok = ok && wait(sums_done, 0);
+        ok = ok && wait(sums_done, 0) && *static_cast<volatile int*>(&gave_up) == 0;     // whoever gave up
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (kRole == kQueries) {

@@ -11,6 +11,14 @@
 //
 // m follows the running maximum only when that has grown by 8 (p then stays below 2^8, far from any limit of fp32 or
 // bf16): the outputs in tensor memory are rescaled a few times a row, not once a block.
+//
+// Heads of 128: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: 0.65 ms (1.69 PFLOP/s; a library product in a
+// burst 1.93); 32768: 2.69 ms (1.63).  Heads of 64 take 0.62 ms: the products would be done in half of that, but a tile's
+// scores wait for its softmax (1300 cycles of a warp, 512 of them exponentials at a quarter of a warp a cycle) and the softmax for them.  P apart
+// from the scores, so that the next scores need not wait, does not help (642 us): the softmax of both tiles at one time takes twice as long.
+// Short sequences: a tile's chain of steps (the tile looked up 0.7 us, copies and scores 1.3, softmax 1.5, product 0.4, output 0.9).  64
+// sequences of 512, 8 heads of 128: 89 us.  CTAs that take over units that have not started, so that one's end lies beside the next one's
+// beginning, gained nothing there and lost 3 % of the long ones.
 #include "attn.cuh"
 
 namespace lmo {
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             if (lane == 0 && stall != kStallSoftmax) mbar_arrive(p_ready + 8 * t);
         }
         if (n) {
-            if (ok) ok = wait(o_done + 8 * t, (n - 1) & 1);
+            ok = ok && wait(o_done + 8 * t, (n - 1) & 1) && *static_cast<volatile int*>(&gave_up) == 0;     // whoever gave up
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
             const int64_t row = tile.first + t * kTile + in;

