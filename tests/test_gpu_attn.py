@@ -443,3 +443,35 @@ def test_first_calls_of_a_thread():
         thread.join()
         torch.cuda.synchronize()
         assert not error and all(torch.equal(a, b) for a, b in zip(got, ref)), error
+
+
+def test_gradients_of_broadcast_inputs_and_of_one_sequence():
+    """A key head shown to several, a gradient that is one number everywhere, no borders: autograd sums what was shared."""
+    from memory_lean_optimizer_gb300 import block
+    q, k, v, _ = inputs(190, 4, 1, 64)
+    a, b, c = (t.clone().requires_grad_() for t in (q, k, v))
+    y = block.attention(a, b.expand(190, 2, 64), c.expand(190, 2, 64))
+    y.sum().backward()                                  # the gradient of y is one expanded element
+    out, lse = block.attention_forward(q, k.expand(190, 2, 64), v.expand(190, 2, 64))
+    dq, dk, dv = block.attention_backward(torch.ones_like(q), q, k.expand(190, 2, 64), v.expand(190, 2, 64), out, lse)
+    assert torch.equal(a.grad, dq) and torch.equal(b.grad, dk.sum(1, keepdim=True)) and torch.equal(c.grad, dv.sum(1, keepdim=True))
+    # two heads that share a key head outright: the same sums, one rounding less
+    y = block.attention(a, b, c)
+    got = torch.autograd.grad(y, (b, c), torch.ones_like(y))
+    for one, two in zip(got, (dk, dv)):
+        # each of the two was rounded, and their sum, and this one
+        assert bool(((one.double() - two.double().sum(1, keepdim=True)).abs() <= 2 * B * two.double().abs().sum(1, keepdim=True) + 2 ** -20).all())
+    with pytest.raises(RuntimeError):
+        g, = torch.autograd.grad(block.attention(a, b, c).float().pow(2).sum(), a, create_graph=True)
+        g.sum().backward()
+
+
+def test_nothing_finite():
+    """A training run that has blown up: every call still returns, and says so."""
+    from memory_lean_optimizer_gb300 import block
+    for bad in (float("nan"), float("inf")):
+        q, k, v, do = (torch.full_like(t, bad) for t in inputs(3000, 4, 2, 128))
+        out, lse = block.attention_forward(q, k, v)
+        got = block.attention_backward(do, q, k, v, out, lse)
+        torch.cuda.synchronize()
+        assert not out.isfinite().any() and not any(t.isfinite().any() for t in got[:1])
