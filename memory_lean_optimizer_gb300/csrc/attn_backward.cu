@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             const char* const mine = base_ptr + t * kTileBytes + in * 128;
             float s[4] = {};
 #pragma unroll
-            for (int h = 0; h < kSteps / 4; ++h) {
+            for (int h = 0; h < (kSteps + 3) / 4; ++h) {
                 uint32_t r[32];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -531,11 +531,9 @@ int launch_role(const AttnCall& c, const HeadRows (&operands)[4], cudaStream_t s
 size_t attn_workspace_bytes(const AttnCall& c) { return (size_t)tile_slots(c.seq, kStep) * c.heads * sizeof(RowBlock); }
 
 int launch_attn_backward(const AttnCall& c, cudaStream_t s) {
-    // heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and
-    // tests of the number of steps between the products cost more than products
     const HeadRows keys[4] = {c.k, c.v, c.q, c.d_out}, queries[4] = {c.q, c.d_out, c.k, c.v};
-    int rc = c.dim <= 64 ? launch_role<kQueries, 4>(c, queries, s) : launch_role<kQueries, 8>(c, queries, s);   // delta too
-    if (!rc && c.dk.p) rc = c.dim <= 64 ? launch_role<kKeys, 4>(c, keys, s) : launch_role<kKeys, 8>(c, keys, s);
+    int rc = with_steps(c.dim, [&](auto steps) { return launch_role<kQueries, decltype(steps)::value>(c, queries, s); });   // delta too
+    if (!rc && c.dk.p) rc = with_steps(c.dim, [&](auto steps) { return launch_role<kKeys, decltype(steps)::value>(c, keys, s); });
     return rc;
 }
 

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             // blocks whose values were cleared: the first tile's own (seen by both), the second's own
             const bool had0 = *static_cast<volatile int*>(&found[0]) != 0, had1 = t && *static_cast<volatile int*>(&found[1]) != 0;
 #pragma unroll
-            for (int h = 0; h < kSteps / 4; ++h) {
+            for (int h = 0; h < (kSteps + 3) / 4; ++h) {
                 uint32_t o[2][32];
                 tmem_load32(o_at + 64 * h, o[0]);
                 tmem_load32(o_at + 64 * h + 32, o[1]);
@@ -365,8 +365,8 @@ static int launch_steps(const AttnCall& c, cudaStream_t s) {
     return check_cuda(launch_after(k_attn_forward<kSteps>, (unsigned)(a.slots * c.heads), kAttnThreads, kSmem, 1, s, q, k, v, a), "attention launch");
 }
 
-// Heads of up to 64 elements in four steps of 16, longer ones in eight: what lies past a head's end is zero, and tests of the
-// number of steps between the products cost more than products.
-int launch_attn_forward(const AttnCall& c, cudaStream_t s) { return c.dim <= 64 ? launch_steps<4>(c, s) : launch_steps<8>(c, s); }
+int launch_attn_forward(const AttnCall& c, cudaStream_t s) {
+    return with_steps(c.dim, [&](auto steps) { return launch_steps<decltype(steps)::value>(c, s); });
+}
 
 }  // namespace lmo
