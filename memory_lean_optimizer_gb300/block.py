@@ -17,23 +17,22 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import lmopt
-from .engine import _stream_ptr
 from .head import _rows, _type, layer_norm
 
-def _on_stream(fn):
-    """Runs a call's copies, allocations and kernels on its `stream` argument (None: the current stream)."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            out = fn(*args, **kw)
-        for a in (*args, *kw.values()):        # their memory is not given away before the stream is done with it
-            for t in a.tensors() if isinstance(a, (PackedActivation, RotaryPlan)) else (a,):
-                if isinstance(t, torch.Tensor) and t.is_cuda:
-                    t.record_stream(stream)
-        return out
-    return call
+
+def _on_stream(stream, fn, *args):
+    """A call's copies, allocations and kernels on a stream that is not the current one."""
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    for a in args:                             # their memory is not given away before the stream is done with it
+        for t in a.tensors() if isinstance(a, (PackedActivation, RotaryPlan)) else (a,):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+    return out
+
+
+def _stream() -> int:
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.h, act_pack_i8)
@@ -42,14 +41,6 @@ ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.
 def _on_gpu(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU")
-
-
-def _heads(t: torch.Tensor, name: str) -> torch.Tensor:
-    """t [tokens, heads, dim] with the elements of a head next to each other: t itself, or a copy."""
-    _on_gpu(t, name)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
-    return t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
 
 
 # ----------------------------------------------------------------------------------------- attention
@@ -126,26 +117,29 @@ def _attn_bytes(packed: bool, sequences: int, rows: int, heads: int, kv_heads: i
     return lmopt.attn_workspace(256 if packed else None, sequences, rows, heads, kv_heads, dim)
 
 
-@_on_stream
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
-                      scale: float | None = None):
+                      scale: float | None = None, *, stream=None):
     """(out, lse): every query attends to the keys of its sequence up to its own, softmax(scale q k) v with scale
     dim^-1/2 by default.  q [tokens, heads, dim], k and v [tokens, kv_heads, dim] bf16 (dim a multiple of 8 up to 128, heads a multiple of
     kv_heads), sequence i rows cu_seqlens[i] to cu_seqlens[i + 1] - 1 (int32, on the device; None: one sequence), or all with
     a batch dimension before, sequences of one length.  lse, fp32 [heads, tokens], is the log of the softmax's
     denominator.  Rows of no sequence are 0 in both."""
+    if stream is not None:
+        return _on_stream(stream, attention_forward, q, k, v, cu_seqlens, scale)
     reads, shape, _, sides, args = _attn_args(q, k, v, cu_seqlens, scale)
     out, out_side = _new_side(shape, reads[0])
     lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=out.device)
-    lmopt.attn_forward(*sides, out_side, lse.data_ptr(), *args, _stream_ptr(None))
+    lmopt.attn_forward(*sides, out_side, lse.data_ptr(), *args, _stream())
     return out.view(q.shape) if q.dim() == 4 else out, lse
 
 
-@_on_stream
 def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
-                       cu_seqlens: torch.Tensor | None = None, scale: float | None = None, need_q: bool = True, need_kv: bool = True):
+                       cu_seqlens: torch.Tensor | None = None, scale: float | None = None, need_q: bool = True, need_kv: bool = True, *,
+                       stream=None):
     """(dq, dk, dv) from the gradient of out and what the forward call was given and returned; None for those that are not
     needed (dk and dv go together).  Rows of no sequence get 0."""
+    if stream is not None:
+        return _on_stream(stream, attention_backward, d_out, q, k, v, out, lse, cu_seqlens, scale, need_q, need_kv)
     if d_out.shape != q.shape or out.shape != q.shape:
         raise ValueError(f"d_out and out must be {list(q.shape)}")
     batched = q.dim() == 4
@@ -166,7 +160,7 @@ def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     nbytes = _attn_bytes(borders is not None, sequences, rows, heads, kv_heads, dim)
     work = torch.empty(nbytes, dtype=torch.uint8, device=out.device)
     lmopt.attn_backward(do_side, *sides, out_side, lse.data_ptr(), dq_side, dk_side, dv_side, *args, work.data_ptr(), nbytes,
-                        _stream_ptr(None))
+                        _stream())
     if batched:
         dq, dk, dv = (None if t is None else t.view(s) for t, s in ((dq, q.shape), (dk, k.shape), (dv, v.shape)))
     return dq, dk, dv
@@ -246,43 +240,54 @@ class RotaryPlan:
         return (self.turns,)
 
 
-def _rope(q, k, positions, plan, inverse, names):
-    q, k = _heads(q, names[0]), _heads(k, names[1])
+def _rope_side(t, name):
+    """t [tokens, heads, dim] and a new tensor like it: (t or a copy, the new one, what a call takes of both)."""
+    _on_gpu(t, name)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
+    shape = t.shape
+    _, heads, dim = shape
+    row, head, one = t.stride()
+    if one != 1 and dim != 1:
+        t = t.contiguous()
+        row, head = heads * dim, dim
+    o = torch.empty(shape, dtype=t.dtype, device=t.device)
+    return t, o, (t.data_ptr(), row, head, o.data_ptr(), heads * dim, dim, heads)
+
+
+def _rope(q, k, positions, plan, inverse, q_name, k_name):
+    dtype = _type(q, q_name)
+    q, q_out, q_side = _rope_side(q, q_name)
+    k, k_out, k_side = _rope_side(k, k_name)
     rows, _, dim = q.shape
-    if k.shape[0] != rows or k.shape[2] != dim or k.dtype != q.dtype:
-        raise ValueError(f"{names[0]} and {names[1]} must have the same tokens, head size and type")
-    dtype, device = _type(q, names[0]), q.device
+    if k.shape[0] != rows or k.shape[2] != dim or k.dtype is not q.dtype:
+        raise ValueError(f"{q_name} and {k_name} must have the same tokens, head size and type")
     if plan.rotary_dim > dim:
         raise ValueError(f"{plan.rotary_dim} rotated elements in heads of {dim}")
     if positions.dtype is not torch.int64 or positions.shape != (rows,) or positions.get_device() != q.get_device():
-        raise ValueError(f"positions must be int64 [{rows}] on {device}")
+        raise ValueError(f"positions must be int64 [{rows}] on {q.device}")
     if plan.turns.get_device() != q.get_device():
         raise ValueError("the plan is on another device")
     if not positions.is_contiguous():
         positions = positions.contiguous()
-    out, sides = [], []
-    for t in (q, k):
-        shape = t.shape
-        o = torch.empty(shape, dtype=t.dtype, device=device)
-        out.append(o)
-        row, head, _ = t.stride()
-        sides.append((t.data_ptr(), row, head, o.data_ptr(), shape[1] * dim, dim, shape[1]))
-    lmopt.rope_apply(*sides, positions.data_ptr(), plan.turns.data_ptr(), rows, dim, plan.rotary_dim, plan.factor,
-                     plan.interleaved, inverse, dtype, _stream_ptr(None))
-    return out[0], out[1]
+    lmopt.rope_apply(q_side, k_side, positions.data_ptr(), plan.turns.data_ptr(), rows, dim, plan.rotary_dim, plan.factor,
+                     plan.interleaved, inverse, dtype, _stream())
+    return q_out, k_out
 
 
-@_on_stream
-def rotary_forward(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan):
+def rotary_forward(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan, *, stream=None):
     """(q, k) turned by their tokens' positions.  q [tokens, heads, dim], k [tokens, kv_heads, dim] (bf16 or fp32, any strides;
     kv_heads may be 0), positions int64 [tokens], of any size.  New tensors."""
-    return _rope(q, k, positions, plan, False, ("q", "k"))
+    if stream is not None:
+        return _on_stream(stream, rotary_forward, q, k, positions, plan)
+    return _rope(q, k, positions, plan, False, "q", "k")
 
 
-@_on_stream
-def rotary_backward(dq: torch.Tensor, dk: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan):
+def rotary_backward(dq: torch.Tensor, dk: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan, *, stream=None):
     """Gradients of rotary_forward's inputs from those of its outputs."""
-    return _rope(dq, dk, positions, plan, True, ("dq", "dk"))
+    if stream is not None:
+        return _on_stream(stream, rotary_backward, dq, dk, positions, plan)
+    return _rope(dq, dk, positions, plan, True, "dq", "dk")
 
 
 class _Rotary(torch.autograd.Function):
@@ -331,68 +336,83 @@ def _new_packed(like: torch.Tensor, rows: int, cols: int, shape, dtype):
 
 
 def _packed_at(p: PackedActivation):
-    """What a call takes of a packed activation."""
-    _on_gpu(p.codes, "the packed activation")
-    _on_gpu(p.exponents, "the packed activation")
-    return p.codes.data_ptr(), p.codes.shape[1], p.exponents.data_ptr(), p.exponents.shape[1]
+    """(what a call takes of a packed activation, its rows)"""
+    codes, exponents = p.codes, p.exponents
+    _on_gpu(codes, "the packed activation")
+    _on_gpu(exponents, "the packed activation")
+    rows, width = codes.shape
+    return (codes.data_ptr(), width, exponents.data_ptr(), width // ACT_BLOCK), rows
 
 
-@_on_stream
-def pack_activation(x: torch.Tensor) -> PackedActivation:
+def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t as a matrix of its last dimension's rows."""
+    if t.dim() == 2 and t.is_contiguous():
+        _on_gpu(t, name)
+        return t
+    return _rows(t, name)
+
+
+def pack_activation(x: torch.Tensor, *, stream=None) -> PackedActivation:
     """x (bf16 or fp32) in 8 bits: off by at most half a step, 2^-7 of the largest magnitude among its block of 32
     elements of the last dimension.  A block with an infinity or a NaN comes back as NaN."""
+    if stream is not None:
+        return _on_stream(stream, pack_activation, x)
     dtype = _type(x, "x")
-    m = _rows(x, "x")
+    m = _matrix(x, "x")
     rows, cols = m.shape
     if cols == 0:
         raise ValueError("x needs at least one element in a row")
     p, at = _new_packed(m, rows, cols, x.shape, x.dtype)
-    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), *at, rows, cols, dtype, _stream_ptr(None))
+    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), *at, rows, cols, dtype, _stream())
     return p
 
 
-@_on_stream
-def unpack_activation(p: PackedActivation) -> torch.Tensor:
+def unpack_activation(p: PackedActivation, *, stream=None) -> torch.Tensor:
     """The values that a packed activation stands for, in its shape and type."""
-    at = _packed_at(p)
+    if stream is not None:
+        return _on_stream(stream, unpack_activation, p)
+    at, rows = _packed_at(p)
     shape = p.shape
     x = torch.empty(shape, dtype=p.dtype, device=p.codes.device)
-    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.codes.shape[0], shape[-1], _type(x, "x"), _stream_ptr(None))
+    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], rows, shape[-1], _type(x, "x"), _stream())
     return x
 
 
-@_on_stream
-def swiglu_forward(gate_up: torch.Tensor, keep: bool = True):
+def swiglu_forward(gate_up: torch.Tensor, keep: bool = True, *, stream=None):
     """(h, packed): h = g sigmoid(g) u of gate_up [..., 2 n], g its first and u its last n elements, and both in 8
     bits ([..., 2, n]; None if keep is false) for swiglu_backward."""
+    if stream is not None:
+        return _on_stream(stream, swiglu_forward, gate_up, keep)
     dtype = _type(gate_up, "gate_up")
-    m = _rows(gate_up, "gate_up")
-    rows, cols = m.shape[0], m.shape[1] // 2
-    if m.shape[1] != 2 * cols or cols == 0:
-        raise ValueError(f"gate_up's last dimension must be even and not 0, not {m.shape[1]}")
+    m = _matrix(gate_up, "gate_up")
+    rows, width = m.shape
+    cols = width // 2
+    if width != 2 * cols or cols == 0:
+        raise ValueError(f"gate_up's last dimension must be even and not 0, not {width}")
     lead, device = gate_up.shape[:-1], m.device
     h = torch.empty((*lead, cols), dtype=gate_up.dtype, device=device)
     packed, at = _new_packed(m, 2 * rows, cols, torch.Size((*lead, 2, cols)), gate_up.dtype) if keep else (None, (None, 0, None, 0))
-    lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, *at, rows, cols, dtype, _stream_ptr(None))
+    lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, *at, rows, cols, dtype, _stream())
     return h, packed
 
 
-@_on_stream
-def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = False):
+def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = False, *, stream=None):
     """(d_gate_up, h) from the gradient of h and what swiglu_forward kept: the gradients at the gate and up values that
     the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
-    at = _packed_at(packed)
+    if stream is not None:
+        return _on_stream(stream, swiglu_backward, dh, packed, need_h)
+    at, _ = _packed_at(packed)
     if len(packed.shape) < 2 or packed.shape[-2] != 2:
         raise ValueError(f"a packed {list(packed.shape)} is not a gate and up pair")
     *lead, _, cols = packed.shape
     if dh.shape != (*lead, cols) or dh.dtype is not packed.dtype:
         raise ValueError(f"dh must be {packed.dtype} {[*lead, cols]} for a packed {list(packed.shape)}")
-    d = _rows(dh, "dh")
+    d = _matrix(dh, "dh")
     rows, device = d.shape[0], d.device
     d_gate_up = torch.empty((*lead, 2 * cols), dtype=packed.dtype, device=device)
     h = torch.empty((*lead, cols), dtype=packed.dtype, device=device) if need_h else None
     lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), *at, d_gate_up.data_ptr(), 2 * cols, h.data_ptr() if need_h else None,
-                              cols, rows, cols, _type(d, "dh"), _stream_ptr(None))
+                              cols, rows, cols, _type(d, "dh"), _stream())
     return d_gate_up, h
 
 
@@ -462,7 +482,7 @@ class TransformerBlock(torch.nn.Module):
                  eps: float = 1e-5, device="cuda"):
         super().__init__()
         kv_heads = heads if kv_heads is None else kv_heads
-        if dim % heads or dim // heads % 8 or dim // heads > 128 or heads % kv_heads:
+        if heads < 1 or kv_heads < 1 or dim < 1 or dim % heads or dim // heads % 8 or dim // heads > 128 or heads % kv_heads:
             raise ValueError(f"width {dim} does not make {heads} heads of a multiple of 8, up to 128, that share {kv_heads}")
         hidden = 4 * dim if hidden is None else hidden
         bf16 = dict(dtype=torch.bfloat16, device=device)
