@@ -1,11 +1,14 @@
 """The inside of a transformer block's training step over liblmopt.so: causal attention over packed sequences with
 grouped heads, rotary positions, and activations kept in 8 bits between the forward and the backward pass,
-alone and in the gated activation that reads them.  With ``head`` (norm, loss) and the optimizer groups they are a memory-lean training step.
+alone and in the gated activation that reads them.  With ``head`` (norm, loss) and the optimizer groups they are a
+memory-lean training step.
 
 The ``*_forward`` / ``*_backward`` functions and ``pack_activation`` / ``unpack_activation`` are the library calls on
 tensors; each takes ``stream`` (a torch stream the caller has ordered after its inputs; default: the
 current one).  ``attention``, ``rotary``, ``swiglu``, ``gated_mlp`` are the same with autograd and run on
 the current stream.  PyTorch supplies device memory, streams, the graph and plain matrix products.
+All of them can be captured into a CUDA graph.  With autograd, capture the forward and the backward pass together, and let no
+eager autograd graph of the same leaves live on at that time: its gradient accumulators belong to its own stream.
 """
 from __future__ import annotations
 

@@ -145,3 +145,10 @@ def test_tensors_are_checked():
             call()
     with pytest.raises(TypeError):
         block.pack_activation(torch.zeros(4, 64, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(128, 0, None), (128, 2, 0), (0, 1, None), (128, -2, None), (128, 2, -1), (24, 6, 6), (512, 2, 2)])
+def test_blocks_that_do_not_divide_are_refused(dim, heads, kv_heads):
+    from memory_lean_optimizer_gb300 import block
+    with pytest.raises(ValueError):
+        block.TransformerBlock(dim, heads, kv_heads, device="cpu")

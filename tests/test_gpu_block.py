@@ -157,3 +157,47 @@ def test_example_model_gradients():
     assert abs(float(loss.detach()) - float(ref.detach())) < 2.0 ** -5
     for k, v in model.named_parameters():
         assert float((v.grad.double() - p[k].grad).norm()) <= 2.0 ** -4 * float(p[k].grad.norm()), k
+
+
+def test_block_of_no_tokens():
+    b = make()
+    x = torch.zeros(0, 128, device="cuda", dtype=BF).requires_grad_()
+    pos = torch.zeros(0, dtype=torch.int64, device="cuda")
+    for cu in (None, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")):
+        y = b(x, pos, cu)
+        assert y.shape == (0, 128)
+        g = torch.autograd.grad(y, [x, *b.parameters()], torch.zeros_like(y))
+        assert all(not t.any() for t in g)
+
+
+def test_operators_with_their_gradients_in_a_graph():
+    """Rotary, attention and the gated activation with autograd, captured and replayed with other inputs and borders: bit for bit
+    what they give outside a graph.  (No eager autograd graph of the same leaves is alive at the capture.)"""
+    from memory_lean_optimizer_gb300 import block
+    torch.manual_seed(5)
+    plan = block.RotaryPlan(64)
+    x = torch.randn(150, 8 * 64, device="cuda").to(BF).requires_grad_()
+    pos = torch.arange(150, device="cuda")
+    cu = torch.tensor([0, 90, 150], dtype=torch.int32, device="cuda")
+    dy = torch.randn(150, 2 * 64, device="cuda").to(BF)
+
+    def step():
+        qkv = x.view(150, 8, 64)
+        q, k = block.rotary(qkv[:, :4], qkv[:, 4:6], pos, plan)
+        y = block.swiglu(block.attention(q, k, qkv[:, 6:], cu).flatten(1))
+        return y.detach(), torch.autograd.grad(y, x, dy)[0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    with torch.no_grad():
+        x.copy_(torch.randn(150, 8 * 64, device="cuda").to(BF))
+    cu.copy_(torch.tensor([0, 20, 140], dtype=torch.int32))
+    pos.copy_(torch.randperm(150))
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
