@@ -21,7 +21,7 @@
 // Many rows: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: dq 1.23 ms, dk and dv 1.25 ms, together 8 products of
 // 0.55e12 operations at 1.77 PFLOP/s (a library product in a burst: 1.93).  128 x 64 scores from shared memory take 48 cycles for 16 elements of
 // the head where 32 would do (128 bytes a cycle); Q and dO in tensor memory free dq's of it.  A lone CTA takes 7 us from its start to its end, of
-// which two blocks are 1.3: texts of 1 to 2035 tokens (11287 rows, 12 / 3 heads of 80) take 187 us, of which the products are 45.
+// which two blocks are 1.3: texts of 1 to 2035 tokens (11287 rows, 12 / 3 heads of 80) take 187 us, of which the products are 36.
 // What the warps' part cost before: tests of masked places in every block (one set of instructions in two), operands read row by row
 // from memory (a line a lane, 3 us a tile), a wait that reads the timer (half of the waits last less).
 #include <type_traits>

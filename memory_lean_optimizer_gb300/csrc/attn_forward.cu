@@ -5,17 +5,20 @@
 // A CTA takes 256 rows of one head as two tiles of 128, which share the keys' and values' blocks of 128 rows
 // in shared memory.  Scores and outputs are accumulators in tensor memory (2 x 128 and 2 x 128 columns, all 512); a
 // thread of a tile's four softmax warps holds one row's 128 scores, so that maxima and sums need no other
-// thread.  P goes back, in bf16, into the first half of its scores' columns and is the A operand of P V from there.
-// The tensor cores work in the order P0 V, Q0 K', P1 V, Q1 K' (K' the next block): while they serve one tile, the other's
-// softmax runs.  P in bf16: the tensor cores want both operands of one type; the sum is of the fp32 values.
+// thread.  P goes back, in bf16, into the first half of its scores' columns (heads of up to 64: into columns of its own)
+// and is the A operand of P V from there.
+// The tensor cores work in the order P0 V, Q0 K', P1 V, Q1 K' (K' the next block; heads of up to 64: Q0 K', Q1 K', P0 V, P1 V): while they
+// serve one tile, the other's softmax runs.  P in bf16: the tensor cores want both operands of one type; the sum is of the fp32 values.
 //
 // m follows the running maximum only when that has grown by 8 (p then stays below 2^8, far from any limit of fp32 or
 // bf16): the outputs in tensor memory are rescaled a few times a row, not once a block.
 //
 // Heads of 128: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: 0.65 ms (1.69 PFLOP/s; a library product in a
-// burst 1.93); 32768: 2.69 ms (1.63).  Heads of 64 take 0.62 ms: the products would be done in half of that, but a tile's
-// scores wait for its softmax (1300 cycles of a warp, 512 of them exponentials at a quarter of a warp a cycle) and the softmax for them.  P apart
-// from the scores, so that the next scores need not wait, does not help (642 us): the softmax of both tiles at one time takes twice as long.
+// burst 1.93); 32768: 2.69 ms (1.63).
+// Heads of up to 64 have room for P beside its scores, so that the next scores are there when a softmax ends (kApart).  16384 tokens in one sequence
+// 540 us (P over its scores: 557), in sequences of 1024 81 us (97), of 256 64 us (67).  What bounds them is the softmax: two warps share a
+// scheduler, and the pair of tiles takes 2500 cycles a block of keys where its arithmetic alone takes 1450 (1024 of them exponentials, a quarter of
+// a warp a cycle), with its waits and arrivals 1700 to 1950, and the products 1024.  A warp of its own for each tile's products gained nothing (561).
 // Short sequences: a tile's chain of steps (the tile looked up 0.7 us, copies and scores 1.3, softmax 1.5, product 0.4, output 0.9).  64
 // sequences of 512, 8 heads of 128: 89 us.  CTAs that take over units that have not started, so that one's end lies beside the next one's
 // beginning, gained nothing there and lost 3 % of the long ones.
@@ -51,14 +54,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                                                                const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v, const ForwardArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[2 + 4 * kStages + 6 + 1];
+    constexpr bool kApart = kSteps <= 4;           // P beside its scores: 2 x 128 columns of scores, 2 x 64 of P, 2 x 64 of outputs
+    constexpr uint32_t kP = kApart ? 256 : 0, kO = kApart ? 384 : 256, kTileP = kApart ? 64 : 128, kTileO = kApart ? 64 : 128;
+    __shared__ uint64_t bars[2 + 4 * kStages + 8 + 1];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found[2], copied[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // before anything of the stream is needed
     const uint32_t q_full = smem_u32(bars), k_full = q_full + 16, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages,
                    v_empty = v_full + 8 * kStages, s_done = v_empty + 8 * kStages, p_ready = s_done + 16, o_done = p_ready + 16,
-                   drained = o_done + 16;
+                   s_free = o_done + 16, drained = s_free + 16;
     if (threadIdx.x == 0) {
         gave_up = 0;
         found[0] = found[1] = copied[0] = copied[1] = 0;
@@ -67,6 +72,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             mbar_init(s_done + 8 * i, 1);
             mbar_init(p_ready + 8 * i, 4);
             mbar_init(o_done + 8 * i, 1);
+            mbar_init(s_free + 8 * i, 4);
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(k_full + 8 * i, 1);
@@ -171,6 +177,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                 const int stage = j % kStages, next = (j + 1) % kStages;
                 ok = wait(v_full + 8 * stage, j / kStages & 1);
                 if (ok && j + 1 < blocks) ok = wait(k_full + 8 * next, (j + 1) / kStages & 1);
+                if (kApart && j + 1 < blocks) {
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (j + 1 >= (t ? n1 : n0)) continue;
+                        ok = wait(s_free + 8 * t, j & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(t, j + 1);
+                    }
+                    if (!ok) break;
+                    mma_commit<1>(k_empty + 8 * next);
+                }
                 for (int t = 0; ok && t < 2; ++t) {
                     const int n = t ? n1 : n0;
                     if (j >= n) continue;
@@ -179,13 +196,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < kTile / 16; ++i)
-                        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8, v_lo + stage * (kTileBytes >> 4) + i * 128, up, desc_o, i == 0 && j == 0);
+                        mma_ts(tmem + kO + t * kTileO, tmem + kP + t * kTileP + i * 8, v_lo + stage * (kTileBytes >> 4) + i * 128, up, desc_o, i == 0 && j == 0);
                     mma_commit<1>(o_done + 8 * t);
-                    if (j + 1 < n) scores(t, j + 1);      // into the columns of P, behind the product that reads it
+                    if (!kApart && j + 1 < n) scores(t, j + 1);      // into the columns of P, behind the product that reads it
                 }
                 if (!ok) break;
                 mma_commit<1>(v_empty + 8 * stage);
-                if (j + 1 < blocks) mma_commit<1>(k_empty + 8 * next);
+                if (!kApart && j + 1 < blocks) mma_commit<1>(k_empty + 8 * next);
             }
         }
         __syncwarp();
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
         regs_up<216>();
         const int t = (warp >> 2) - 1, n = t ? n1 : n0;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+        const uint32_t s_at = tmem + lanes + t * 128, p_at = tmem + lanes + kP + t * kTileP, o_at = tmem + lanes + kO + t * kTileO;
         const int in = 32 * (warp & 3) + lane;                                  // this thread's row of the tile
         const float c = p.scale * kLog2e;
         const F2 c2 = f2(c, c);
@@ -209,6 +226,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             for (int q = 0; q < 4; ++q) tmem_load32(s_at + 32 * q, x[q]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_wait(x[q]);
+            if (kApart) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + 8 * t);
+            }
             if (j == n - 1) {      // the tile's own block: keys behind the row
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -228,16 +250,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
             }
             const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grow = now > m + kSlack;
+            if (kApart && j > 0) {      // the product that reads the last P
+                ok = wait(o_done + 8 * t, (j - 1) & 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
             if (j == 0) {
                 m = now;
             } else if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float f = grow ? exp2_approx(m - now) : 1.0f;
                 if (grow) m = now;
                 sum *= f;
-                ok = wait(o_done + 8 * t, (j - 1) & 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
+                if (!kApart) {
+                    ok = wait(o_done + 8 * t, (j - 1) & 1);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
 #pragma unroll 1
                 for (int q = 0; q < p.dim; q += 32) {
                     uint32_t o[32];
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_forward(const __grid_c
                         part[k / 2 & 3] = add2(part[k / 2 & 3], f2(a, b));
                         w[16 * q + k / 2] = pack_bf16(a, b);
                     }
-                tmem_store32(s_at + 32 * h, w);
+                tmem_store32(p_at + 32 * h, w);
             }
             tmem_store_wait();
             float a, b;
