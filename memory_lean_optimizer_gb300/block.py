@@ -314,37 +314,56 @@ def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, plan: Rota
 # ------------------------------------------------------------------------- activations kept in 8 bits
 class PackedActivation:
     """An activation in 8 bits: int8 codes of rows of its last dimension, a uint8 exponent per 32 of them (the last block of a
-    row is filled up with zeros), value = code * 2^(exponent - 133); the shape and type it was packed from."""
-    __slots__ = ("codes", "exponents", "shape", "dtype")
+    row is filled up with zeros), value = code * 2^(exponent - 133); the shape and type it was packed from.  Codes and
+    exponents lie in one piece of memory, `data`; made from codes and exponents, it copies them there."""
+    __slots__ = ("data", "rows", "width", "shape", "dtype")
 
     def __init__(self, codes: torch.Tensor, exponents: torch.Tensor, shape: torch.Size, dtype: torch.dtype):
-        rows, blocks = math.prod(shape[:-1]), -(-shape[-1] // ACT_BLOCK)
-        if (codes.dtype is not torch.int8 or codes.shape != (rows, blocks * ACT_BLOCK) or not codes.is_contiguous() or
-                exponents.dtype is not torch.uint8 or exponents.shape != (rows, blocks) or not exponents.is_contiguous()):
+        self._lay_out(shape, dtype)
+        if (codes.dtype is not torch.int8 or codes.shape != (self.rows, self.width) or codes.device != exponents.device or
+                exponents.dtype is not torch.uint8 or exponents.shape != (self.rows, self.width // ACT_BLOCK)):
             raise ValueError(f"codes and exponents do not fit {list(shape)}")
-        self.codes, self.exponents, self.shape, self.dtype = codes, exponents, torch.Size(shape), dtype
+        self.data = torch.cat((codes.reshape(-1).view(torch.uint8), exponents.reshape(-1)))
+
+    def _lay_out(self, shape, dtype):
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.rows, self.width = math.prod(shape[:-1]), -(-shape[-1] // ACT_BLOCK) * ACT_BLOCK
+
+    @classmethod
+    def _of(cls, data, shape, dtype):
+        p = cls.__new__(cls)
+        p._lay_out(shape, dtype)
+        p.data = data
+        return p
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self.data[:self.rows * self.width].view(torch.int8).view(self.rows, self.width)
+
+    @property
+    def exponents(self) -> torch.Tensor:
+        return self.data[self.rows * self.width:].view(self.rows, self.width // ACT_BLOCK)
 
     def tensors(self):
-        return self.codes, self.exponents
+        return (self.data,)
 
 
 def _new_packed(like: torch.Tensor, rows: int, cols: int, shape, dtype):
     """A PackedActivation of new memory, and what a call takes of it."""
     blocks = -(-cols // ACT_BLOCK)
+    width = blocks * ACT_BLOCK
     p = PackedActivation.__new__(PackedActivation)
-    p.codes = torch.empty((rows, blocks * ACT_BLOCK), dtype=torch.int8, device=like.device)
-    p.exponents = torch.empty((rows, blocks), dtype=torch.uint8, device=like.device)
-    p.shape, p.dtype = shape, dtype
-    return p, (p.codes.data_ptr(), blocks * ACT_BLOCK, p.exponents.data_ptr(), blocks)
+    p.data = torch.empty(rows * (width + blocks), dtype=torch.uint8, device=like.device)
+    p.rows, p.width, p.shape, p.dtype = rows, width, shape, dtype
+    at = p.data.data_ptr()
+    return p, (at, width, at + rows * width, blocks)
 
 
 def _packed_at(p: PackedActivation):
-    """(what a call takes of a packed activation, its rows)"""
-    codes, exponents = p.codes, p.exponents
-    _on_gpu(codes, "the packed activation")
-    _on_gpu(exponents, "the packed activation")
-    rows, width = codes.shape
-    return (codes.data_ptr(), width, exponents.data_ptr(), width // ACT_BLOCK), rows
+    """What a call takes of a packed activation."""
+    _on_gpu(p.data, "the packed activation")
+    at, width = p.data.data_ptr(), p.width
+    return at, width, at + p.rows * width, width // ACT_BLOCK
 
 
 def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -374,10 +393,10 @@ def unpack_activation(p: PackedActivation, *, stream=None) -> torch.Tensor:
     """The values that a packed activation stands for, in its shape and type."""
     if stream is not None:
         return _on_stream(stream, unpack_activation, p)
-    at, rows = _packed_at(p)
+    at = _packed_at(p)
     shape = p.shape
-    x = torch.empty(shape, dtype=p.dtype, device=p.codes.device)
-    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], rows, shape[-1], _type(x, "x"), _stream())
+    x = torch.empty(shape, dtype=p.dtype, device=p.data.device)
+    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.rows, shape[-1], _type(x, "x"), _stream())
     return x
 
 
@@ -404,7 +423,7 @@ def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = F
     the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
     if stream is not None:
         return _on_stream(stream, swiglu_backward, dh, packed, need_h)
-    at, _ = _packed_at(packed)
+    at = _packed_at(packed)
     if len(packed.shape) < 2 or packed.shape[-2] != 2:
         raise ValueError(f"a packed {list(packed.shape)} is not a gate and up pair")
     *lead, _, cols = packed.shape
@@ -423,14 +442,14 @@ class _SwiGLU(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate_up):
         h, packed = swiglu_forward(gate_up)
-        ctx.save_for_backward(packed.codes, packed.exponents)
+        ctx.save_for_backward(packed.data)
         ctx.kept = packed.shape, packed.dtype
         return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
-        return swiglu_backward(dh, PackedActivation(*ctx.saved_tensors, *ctx.kept))[0]
+        return swiglu_backward(dh, PackedActivation._of(*ctx.saved_tensors, *ctx.kept))[0]
 
 
 def swiglu(gate_up: torch.Tensor) -> torch.Tensor:
@@ -445,22 +464,22 @@ class _GatedMLP(torch.autograd.Function):
     def forward(ctx, x, w_in, w_out):
         h, kept = swiglu_forward(torch.nn.functional.linear(x, w_in))
         x8 = pack_activation(x) if ctx.needs_input_grad[1] else None
-        ctx.save_for_backward(w_in, w_out, kept.codes, kept.exponents, *((x8.codes, x8.exponents) if x8 else ()))
+        ctx.save_for_backward(w_in, w_out, kept.data, x8.data if x8 else None)
         ctx.kept, ctx.x = (kept.shape, kept.dtype), (x.shape, x.dtype)
         return torch.nn.functional.linear(h, w_out)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        w_in, w_out, codes, exponents, *x8 = ctx.saved_tensors
+        w_in, w_out, kept, x8 = ctx.saved_tensors
         need_x, need_in, need_out = ctx.needs_input_grad
-        d_gate_up, h = swiglu_backward(dy @ w_out, PackedActivation(codes, exponents, *ctx.kept), need_h=need_out)
+        d_gate_up, h = swiglu_backward(dy @ w_out, PackedActivation._of(kept, *ctx.kept), need_h=need_out)
         dx = d_in = d_out = None
         if need_out:
             d_out = dy.flatten(0, -2).t() @ h.flatten(0, -2)
             del h
         if need_in:
-            d_in = d_gate_up.flatten(0, -2).t() @ unpack_activation(PackedActivation(*x8, *ctx.x)).flatten(0, -2)
+            d_in = d_gate_up.flatten(0, -2).t() @ unpack_activation(PackedActivation._of(x8, *ctx.x)).flatten(0, -2)
         if need_x:
             dx = d_gate_up @ w_in
         return dx, d_in, d_out

@@ -222,3 +222,19 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     h, p = block.swiglu_forward(x)
     assert torch.equal(h2, h) and torch.equal(d2, block.swiglu_backward(dh, p)[0])
+
+
+def test_packed_from_codes_and_exponents():
+    """A packed activation made from another's codes and exponents (a saved one) is the same; empty ones too."""
+    from memory_lean_optimizer_gb300 import block
+    x = torch.randn(3, 5, 70, device="cuda").to(BF)
+    p = block.pack_activation(x)
+    q = block.PackedActivation(p.codes.cpu(), p.exponents.cpu(), (3, 5, 70), BF)
+    with pytest.raises(ValueError):
+        block.unpack_activation(q)                       # not on the GPU
+    q = block.PackedActivation(p.codes.clone(), p.exponents.t().contiguous().t(), p.shape, p.dtype)
+    assert torch.equal(block.unpack_activation(q), block.unpack_activation(p))
+    assert torch.equal(q.codes, p.codes) and torch.equal(q.exponents, p.exponents)
+    e = block.pack_activation(x[:0])
+    assert block.PackedActivation(e.codes, e.exponents, e.shape, e.dtype).data.numel() == 0
+    assert block.unpack_activation(e).shape == (0, 5, 70)
