@@ -34,25 +34,29 @@ def _on_stream(stream, fn, *args):
     return out
 
 
-def _stream() -> int:
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 ACT_BLOCK = 32        # elements of a row that share an exponent (include/lmopt.h, act_pack_i8)
 
 
-def _on_gpu(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+def _on_gpu(t: torch.Tensor, name: str) -> int:
+    """The current GPU, where t has to be."""
+    device = t.get_device()
+    if device < 0 or device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current GPU")
+    return device
 
 
 # ----------------------------------------------------------------------------------------- attention
-def _attn_side(t: torch.Tensor, name: str):
+def _attn_side(t: torch.Tensor, name: str, device: int):
     """t [tokens, heads, dim], bf16, as the kernels read it: heads on 16 bytes, rows and heads apart; t itself, or a copy.  (t,
     its shape, its pointer and strides)"""
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
-    _on_gpu(t, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current GPU")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
     shape = t.shape
@@ -81,7 +85,7 @@ def _flat(t: torch.Tensor, name: str) -> torch.Tensor:
 
 
 def _attn_args(q, k, v, cu_seqlens, scale):
-    """(tensors that the call reads, shape of q, shape of k, sides of q, k, v, the call's sizes) of [tokens, heads, dim] or, for
+    """(tensors that the call reads, shape of q, shape of k, sides of q, k, v, the call's sizes, the device) of [tokens, heads, dim] or, for
     sequences of one length, [batch, length, heads, dim]."""
     batch = 1
     if q.dim() == 4:
@@ -91,9 +95,12 @@ def _attn_args(q, k, v, cu_seqlens, scale):
             raise ValueError("q, k and v must have the same batch and length")
         batch = q.shape[0] or 1
         q, k, v = _flat(q, "q"), _flat(k, "k"), _flat(v, "v")
-    q, q_shape, q_side = _attn_side(q, "q")
-    k, k_shape, k_side = _attn_side(k, "k")
-    v, v_shape, v_side = _attn_side(v, "v")
+    if q.dtype is not torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, not {q.dtype}")
+    device = _on_gpu(q, "q")
+    q, q_shape, q_side = _attn_side(q, "q", device)
+    k, k_shape, k_side = _attn_side(k, "k", device)
+    v, v_shape, v_side = _attn_side(v, "v", device)
     rows, heads, dim = q_shape
     kv_heads = k_shape[1]
     if k_shape != v_shape or k_shape[0] != rows or k_shape[2] != dim:
@@ -104,7 +111,7 @@ def _attn_args(q, k, v, cu_seqlens, scale):
         raise ValueError(f"heads must have 8 to 128 elements, a multiple of 8, not {dim}")
     borders = None
     if cu_seqlens is not None:
-        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != q.get_device():
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.get_device() != device:
             raise ValueError(f"cu_seqlens must be int32 [sequences + 1] on {q.device}")
         if not cu_seqlens.is_contiguous():
             cu_seqlens = cu_seqlens.contiguous()
@@ -112,7 +119,7 @@ def _attn_args(q, k, v, cu_seqlens, scale):
     scale = dim ** -0.5 if scale is None else float(scale)
     if not (scale > 0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
-    return (q, k, v, cu_seqlens), q_shape, k_shape, (q_side, k_side, v_side), (borders, batch, rows, heads, kv_heads, dim, scale)
+    return (q, k, v, cu_seqlens), q_shape, k_shape, (q_side, k_side, v_side), (borders, batch, rows, heads, kv_heads, dim, scale), device
 
 
 @functools.lru_cache(maxsize=256)
@@ -129,10 +136,10 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     denominator.  Rows of no sequence are 0 in both."""
     if stream is not None:
         return _on_stream(stream, attention_forward, q, k, v, cu_seqlens, scale)
-    reads, shape, _, sides, args = _attn_args(q, k, v, cu_seqlens, scale)
+    reads, shape, _, sides, args, device = _attn_args(q, k, v, cu_seqlens, scale)
     out, out_side = _new_side(shape, reads[0])
     lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=out.device)
-    lmopt.attn_forward(*sides, out_side, lse.data_ptr(), *args, _stream())
+    lmopt.attn_forward(*sides, out_side, lse.data_ptr(), *args, _stream(device))
     return out.view(q.shape) if q.dim() == 4 else out, lse
 
 
@@ -146,10 +153,10 @@ def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     if d_out.shape != q.shape or out.shape != q.shape:
         raise ValueError(f"d_out and out must be {list(q.shape)}")
     batched = q.dim() == 4
-    reads, q_shape, k_shape, sides, args = _attn_args(q, k, v, cu_seqlens, scale)
-    d_out, _, do_side = _attn_side(_flat(d_out, "d_out") if batched else d_out, "d_out")
-    out, _, out_side = _attn_side(_flat(out, "out") if batched else out, "out")
-    if lse.dtype is not torch.float32 or lse.shape != (q_shape[1], q_shape[0]) or lse.get_device() != out.get_device():
+    reads, q_shape, k_shape, sides, args, device = _attn_args(q, k, v, cu_seqlens, scale)
+    d_out, _, do_side = _attn_side(_flat(d_out, "d_out") if batched else d_out, "d_out", device)
+    out, _, out_side = _attn_side(_flat(out, "out") if batched else out, "out", device)
+    if lse.dtype is not torch.float32 or lse.shape != (q_shape[1], q_shape[0]) or lse.get_device() != device:
         raise ValueError(f"lse must be float32 {[q_shape[1], q_shape[0]]} on {out.device}")
     if not lse.is_contiguous():
         lse = lse.contiguous()
@@ -163,7 +170,7 @@ def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     nbytes = _attn_bytes(borders is not None, sequences, rows, heads, kv_heads, dim)
     work = torch.empty(nbytes, dtype=torch.uint8, device=out.device)
     lmopt.attn_backward(do_side, *sides, out_side, lse.data_ptr(), dq_side, dk_side, dv_side, *args, work.data_ptr(), nbytes,
-                        _stream())
+                        _stream(device))
     if batched:
         dq, dk, dv = (None if t is None else t.view(s) for t, s in ((dq, q.shape), (dk, k.shape), (dv, v.shape)))
     return dq, dk, dv
@@ -245,7 +252,6 @@ class RotaryPlan:
 
 def _rope_side(t, name):
     """t [tokens, heads, dim] and a new tensor like it: (t or a copy, the new one, what a call takes of both)."""
-    _on_gpu(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim], not {list(t.shape)}")
     shape = t.shape
@@ -260,6 +266,9 @@ def _rope_side(t, name):
 
 def _rope(q, k, positions, plan, inverse, q_name, k_name):
     dtype = _type(q, q_name)
+    device = _on_gpu(q, q_name)
+    if k.get_device() != device:
+        raise ValueError(f"{k_name} must be on the current GPU")
     q, q_out, q_side = _rope_side(q, q_name)
     k, k_out, k_side = _rope_side(k, k_name)
     rows, _, dim = q.shape
@@ -267,14 +276,14 @@ def _rope(q, k, positions, plan, inverse, q_name, k_name):
         raise ValueError(f"{q_name} and {k_name} must have the same tokens, head size and type")
     if plan.rotary_dim > dim:
         raise ValueError(f"{plan.rotary_dim} rotated elements in heads of {dim}")
-    if positions.dtype is not torch.int64 or positions.shape != (rows,) or positions.get_device() != q.get_device():
+    if positions.dtype is not torch.int64 or positions.shape != (rows,) or positions.get_device() != device:
         raise ValueError(f"positions must be int64 [{rows}] on {q.device}")
-    if plan.turns.get_device() != q.get_device():
+    if plan.turns.get_device() != device:
         raise ValueError("the plan is on another device")
     if not positions.is_contiguous():
         positions = positions.contiguous()
     lmopt.rope_apply(q_side, k_side, positions.data_ptr(), plan.turns.data_ptr(), rows, dim, plan.rotary_dim, plan.factor,
-                     plan.interleaved, inverse, dtype, _stream())
+                     plan.interleaved, inverse, dtype, _stream(device))
     return q_out, k_out
 
 
@@ -360,18 +369,16 @@ def _new_packed(like: torch.Tensor, rows: int, cols: int, shape, dtype):
 
 
 def _packed_at(p: PackedActivation):
-    """What a call takes of a packed activation."""
-    _on_gpu(p.data, "the packed activation")
+    """(what a call takes of a packed activation, its device)"""
+    device = _on_gpu(p.data, "the packed activation")
     at, width = p.data.data_ptr(), p.width
-    return at, width, at + p.rows * width, width // ACT_BLOCK
+    return (at, width, at + p.rows * width, width // ACT_BLOCK), device
 
 
-def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
-    """t as a matrix of its last dimension's rows."""
-    if t.dim() == 2 and t.is_contiguous():
-        _on_gpu(t, name)
-        return t
-    return _rows(t, name)
+def _matrix(t: torch.Tensor, name: str):
+    """(t as a matrix of its last dimension's rows, its device)"""
+    device = _on_gpu(t, name)
+    return t if t.dim() == 2 and t.is_contiguous() else _rows(t, name), device
 
 
 def pack_activation(x: torch.Tensor, *, stream=None) -> PackedActivation:
@@ -380,12 +387,12 @@ def pack_activation(x: torch.Tensor, *, stream=None) -> PackedActivation:
     if stream is not None:
         return _on_stream(stream, pack_activation, x)
     dtype = _type(x, "x")
-    m = _matrix(x, "x")
+    m, device = _matrix(x, "x")
     rows, cols = m.shape
     if cols == 0:
         raise ValueError("x needs at least one element in a row")
     p, at = _new_packed(m, rows, cols, x.shape, x.dtype)
-    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), *at, rows, cols, dtype, _stream())
+    lmopt.act_pack_i8(m.data_ptr(), m.stride(0), *at, rows, cols, dtype, _stream(device))
     return p
 
 
@@ -393,10 +400,10 @@ def unpack_activation(p: PackedActivation, *, stream=None) -> torch.Tensor:
     """The values that a packed activation stands for, in its shape and type."""
     if stream is not None:
         return _on_stream(stream, unpack_activation, p)
-    at = _packed_at(p)
+    at, device = _packed_at(p)
     shape = p.shape
     x = torch.empty(shape, dtype=p.dtype, device=p.data.device)
-    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.rows, shape[-1], _type(x, "x"), _stream())
+    lmopt.act_unpack_i8(*at, x.data_ptr(), shape[-1], p.rows, shape[-1], _type(x, "x"), _stream(device))
     return x
 
 
@@ -406,15 +413,15 @@ def swiglu_forward(gate_up: torch.Tensor, keep: bool = True, *, stream=None):
     if stream is not None:
         return _on_stream(stream, swiglu_forward, gate_up, keep)
     dtype = _type(gate_up, "gate_up")
-    m = _matrix(gate_up, "gate_up")
+    m, device = _matrix(gate_up, "gate_up")
     rows, width = m.shape
     cols = width // 2
     if width != 2 * cols or cols == 0:
         raise ValueError(f"gate_up's last dimension must be even and not 0, not {width}")
-    lead, device = gate_up.shape[:-1], m.device
-    h = torch.empty((*lead, cols), dtype=gate_up.dtype, device=device)
+    lead = gate_up.shape[:-1]
+    h = torch.empty((*lead, cols), dtype=gate_up.dtype, device=m.device)
     packed, at = _new_packed(m, 2 * rows, cols, torch.Size((*lead, 2, cols)), gate_up.dtype) if keep else (None, (None, 0, None, 0))
-    lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, *at, rows, cols, dtype, _stream())
+    lmopt.act_swiglu_forward(m.data_ptr(), m.stride(0), h.data_ptr(), cols, *at, rows, cols, dtype, _stream(device))
     return h, packed
 
 
@@ -423,18 +430,18 @@ def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = F
     the codes stand for, and (need_h; else None) h of those values, for the next product's weight gradient."""
     if stream is not None:
         return _on_stream(stream, swiglu_backward, dh, packed, need_h)
-    at = _packed_at(packed)
+    at, device = _packed_at(packed)
     if len(packed.shape) < 2 or packed.shape[-2] != 2:
         raise ValueError(f"a packed {list(packed.shape)} is not a gate and up pair")
     *lead, _, cols = packed.shape
     if dh.shape != (*lead, cols) or dh.dtype is not packed.dtype:
         raise ValueError(f"dh must be {packed.dtype} {[*lead, cols]} for a packed {list(packed.shape)}")
-    d = _matrix(dh, "dh")
-    rows, device = d.shape[0], d.device
-    d_gate_up = torch.empty((*lead, 2 * cols), dtype=packed.dtype, device=device)
-    h = torch.empty((*lead, cols), dtype=packed.dtype, device=device) if need_h else None
+    d, _ = _matrix(dh, "dh")
+    rows = d.shape[0]
+    d_gate_up = torch.empty((*lead, 2 * cols), dtype=packed.dtype, device=d.device)
+    h = torch.empty((*lead, cols), dtype=packed.dtype, device=d.device) if need_h else None
     lmopt.act_swiglu_backward(d.data_ptr(), d.stride(0), *at, d_gate_up.data_ptr(), 2 * cols, h.data_ptr() if need_h else None,
-                              cols, rows, cols, _type(d, "dh"), _stream())
+                              cols, rows, cols, _type(d, "dh"), _stream(device))
     return d_gate_up, h
 
 
