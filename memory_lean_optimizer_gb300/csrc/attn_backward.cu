@@ -16,7 +16,10 @@
 // What bf16 costs.  dq, dk and dv are rounded once (1.65e-3 in the 2-norm); p and dS once before (as much again in dk and dv).  delta from out as
 // the forward pass rounded it would add 1.2e-3 to dq and dk: instead dq's kernel sums its dS (sum_j dS_ij = 0 with the true delta), and the keys'
 // kernel takes delta without that excess; dq itself, which cannot, takes dS in two bf16 parts (a product more).  Against 64 bits
-// all three are within 2.4e-3; with dS in one part and that delta 2.6e-3.
+// dk and dv are within 2.4e-3 and dq within 1.7e-3; dq with dS in one part and that delta, 2.6e-3.
+// Where queries see few keys out is not small beside the values it is a mean of, nor is its rounding in dq: a sequence's first 64 queries
+// take the excess out of dq too, dq -= excess sum_j p_ij k_j, for the first block's scores and keys are still there at the end of its first
+// tile (`exact`).  Sequences of 2 to 13 tokens: dq within 1.7e-3 (3.4e-3 before), for 0 to 5 us in 124 to 154 (sequences of 256, 1024).
 //
 // Many rows: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: dq 1.23 ms, dk and dv 1.25 ms, together 8 products of
 // 0.55e12 operations at 1.77 PFLOP/s (a library product in a burst: 1.93).  128 x 64 scores from shared memory take 48 cycles for 16 elements of
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         }
         mbar_init(sums_done, 1);
         mbar_init(drained, 1);
-        mbar_init(halves_ready, 4);
+        mbar_init(halves_ready, 8);
         mbar_init(delta_ready, 4);
         mbar_init_fence();
         tma_prefetch_map(&map_a0);
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
+    const bool exact = tile.first == tile.start;      // queries that see few keys (see above)
     const int stall = head == 0 && rank == 0 && tile.segment == 1 && tile.first == tile.start ? p.stall : 0;
 
     if (warp < 4) {
@@ -259,6 +263,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (++stage == kStages) stage = 0;
             }
             if (ok) mma_commit<1>(sums_done);
+            if (kRole == kQueries && exact && ok && wait(ready, 1)) {      // the sums' correction, over the first block's dS
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < kStep / 16; ++j) mma_ts(tmem + 256, tmem + 128 + (j >> 1) * 32 + (j & 1) * 8, b_lo + j * 128, up, desc_sum, false);
+                mma_commit<1>(sums_done);
+            }
         }
         __syncwarp();
     } else {
@@ -391,19 +401,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             float a, b;
             split2(add2(excess[0], excess[1]), a, b);
             float* const halves = reinterpret_cast<float*>(base_ptr);          // over the operands, which are done with
-            if (t == 1) {
-                halves[in] = a + b;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(halves_ready);
-            } else {
+            halves[kTile * t + in] = a + b;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(halves_ready);
+            if (t == 0 || exact) {
                 const bool both = wait(halves_ready, 0) && ok;
-                // tiles of 128 start at a block of 64
-                RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
-                if (tile.first + in / kStep * kStep < tile.end) {
-                    to.lse[in % kStep] = my_lse;
-                    to.delta[in % kStep] = row >= tile.end ? 0.0f : both ? my_delta - (a + b + halves[in]) : __builtin_nanf("");
+                const float off = halves[in] + halves[kTile + in];
+                if (t == 0) {
+                    // tiles of 128 start at a block of 64
+                    RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
+                    if (tile.first + in / kStep * kStep < tile.end) {
+                        to.lse[in % kStep] = my_lse;
+                        to.delta[in % kStep] = row >= tile.end ? 0.0f : both ? my_delta - off : __builtin_nanf("");
+                    }
                 }
+                ok = __all_sync(0xFFFFFFFFu, both);
+            }
+            if (exact && ok) {
+                // the first block's scores are still there (a sequence's first tile has two blocks at most), and its keys
+                const uint32_t x_at = tmem + lanes + 32 * t;
+                uint32_t x[32], w[16];
+                tmem_load32(x_at, x);
+                tmem_wait(x);
+                const int to = in < kStep ? in + 1 - 32 * t : 0;
+                const float e = -(halves[in] + halves[kTile + in]);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float y[2];
+                    split2(fma2(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, my_lse2), y[0], y[1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) y[i] = k + i < to ? e * exp2_approx(y[i]) : 0.0f;
+                    w[k / 2] = pack_bf16(y[0], y[1]);
+                }
+                tmem_store16(x_at + 128, w);
+                tmem_store_wait();
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(ready);
+                ok = wait(sums_done, 1) && *static_cast<volatile int*>(&gave_up) == 0;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                tc_fence_after();
             }
         }
         // the first four warps take half of dq or dk out, the others the other half or dv

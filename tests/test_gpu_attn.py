@@ -475,3 +475,26 @@ def test_nothing_finite():
         got = block.attention_backward(do, q, k, v, out, lse)
         torch.cuda.synchronize()
         assert not out.isfinite().any() and not any(t.isfinite().any() for t in got[:1])
+
+
+@pytest.mark.parametrize("lengths", [[2] * 20, [9], [6, 3, 8, 13, 2, 11] * 4, [64] * 4, [65, 100]], ids=["two", "nine", "few", "block", "tile"])
+def test_gradients_of_queries_that_see_few_keys(lengths):
+    """out's rounding, 2^-8 of a mean that is not small beside its values here, must not reach dq: in the 2-norm dq is off by its own rounding
+    (as the formula's, rounded) and by no more than 2^-11 beside it.  What is left: dS in two parts (2^-17), and the correction's
+    own rounding, 2^-8 of a correction of 2^-8 delta |sum p k|, which stays below 2^5 |dq| for these inputs."""
+    from memory_lean_optimizer_gb300 import block
+    rows = sum(lengths)
+    q, k, v, do = inputs(rows, 8, 2, 64)
+    cu = borders(lengths)
+    out, lse = block.attention_forward(q, k, v, cu)
+    dq = block.attention_backward(do, q, k, v, out, lse, cu)[0]
+    qd, kd, vd = (t.double().requires_grad_() for t in (q, k, v))
+    outs, at = [], 0
+    for n in lengths:
+        s = torch.einsum("ihd,jhd->hij", qd[at:at + n], kd[at:at + n].repeat_interleave(4, 1)) * 64 ** -0.5
+        s = s.masked_fill(~torch.ones(n, n, dtype=torch.bool, device="cuda").tril(), -math.inf)
+        outs.append(torch.einsum("hij,jhd->ihd", s.softmax(2), vd[at:at + n].repeat_interleave(4, 1)))
+        at += n
+    want = torch.autograd.grad(torch.cat(outs), qd, do.double())[0]
+    rounded = float((want.to(BF).double() - want).norm())
+    assert float((dq.double() - want).norm()) <= 1.02 * rounded + 2.0 ** -11 * float(want.norm())
