@@ -447,39 +447,40 @@ def swiglu_backward(dh: torch.Tensor, packed: PackedActivation, need_h: bool = F
 
 class _SwiGLU(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, gate_up):
-        h, packed = swiglu_forward(gate_up)
-        ctx.save_for_backward(packed.data)
-        ctx.kept = packed.shape, packed.dtype
+    def forward(ctx, gate_up, keep):
+        h, packed = swiglu_forward(gate_up, keep)
+        if keep:
+            ctx.save_for_backward(packed.data)
+            ctx.kept = packed.shape, packed.dtype
         return h
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
-        return swiglu_backward(dh, PackedActivation._of(*ctx.saved_tensors, *ctx.kept))[0]
+        return swiglu_backward(dh, PackedActivation._of(*ctx.saved_tensors, *ctx.kept))[0], None
 
 
 def swiglu(gate_up: torch.Tensor) -> torch.Tensor:
     """g sigmoid(g) u with autograd; for the backward pass g and u are kept in 8 bits."""
-    if torch.is_grad_enabled() and gate_up.requires_grad:
-        return _SwiGLU.apply(gate_up)
-    return swiglu_forward(gate_up, keep=False)[0]
+    # always through the Function, which refuses forward-mode tangents: they come without requires_grad, and without grad mode too
+    return _SwiGLU.apply(gate_up, torch.is_grad_enabled() and gate_up.requires_grad)
 
 
 class _GatedMLP(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_in, w_out):
-        h, kept = swiglu_forward(torch.nn.functional.linear(x, w_in))
-        x8 = pack_activation(x) if ctx.needs_input_grad[1] else None
-        ctx.save_for_backward(w_in, w_out, kept.data, x8.data if x8 else None)
-        ctx.kept, ctx.x = (kept.shape, kept.dtype), (x.shape, x.dtype)
+    def forward(ctx, x, w_in, w_out, keep):
+        h, kept = swiglu_forward(torch.nn.functional.linear(x, w_in), keep)
+        if keep:
+            x8 = pack_activation(x) if ctx.needs_input_grad[1] else None
+            ctx.save_for_backward(w_in, w_out, kept.data, x8.data if x8 else None)
+            ctx.kept, ctx.x = (kept.shape, kept.dtype), (x.shape, x.dtype)
         return torch.nn.functional.linear(h, w_out)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         w_in, w_out, kept, x8 = ctx.saved_tensors
-        need_x, need_in, need_out = ctx.needs_input_grad
+        need_x, need_in, need_out, _ = ctx.needs_input_grad
         d_gate_up, h = swiglu_backward(dy @ w_out, PackedActivation._of(kept, *ctx.kept), need_h=need_out)
         dx = d_in = d_out = None
         if need_out:
@@ -489,7 +490,7 @@ class _GatedMLP(torch.autograd.Function):
             d_in = d_gate_up.flatten(0, -2).t() @ unpack_activation(PackedActivation._of(x8, *ctx.x)).flatten(0, -2)
         if need_x:
             dx = d_gate_up @ w_in
-        return dx, d_in, d_out
+        return dx, d_in, d_out, None
 
 
 def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch.Tensor:
@@ -497,9 +498,7 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch
     the gate and up values in 8 bits (x for w_in's gradient; gate and up for everything else: h is formed again)."""
     if x.dim() < 2 or w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or x.shape[-1] != w_in.shape[1]:
         raise ValueError(f"x {list(x.shape)}, w_in {list(w_in.shape)} and w_out {list(w_out.shape)} do not fit")
-    if not torch.is_grad_enabled():
-        return torch.nn.functional.linear(swiglu_forward(torch.nn.functional.linear(x, w_in), keep=False)[0], w_out)
-    return _GatedMLP.apply(x, w_in, w_out)
+    return _GatedMLP.apply(x, w_in, w_out, torch.is_grad_enabled())
 
 
 class TransformerBlock(torch.nn.Module):
