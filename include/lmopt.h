@@ -538,8 +538,8 @@ int attn_workspace(const int32_t* cu_seqlens, int64_t sequences, int64_t rows, i
 /* Gradients of the above from d_out and what forward gave, bf16: with p_ij = exp(s_ij - lse_i), delta_i = d_out_i out_i and
  * dS_ij = p_ij (d_out_i v_j - delta_i): dq_i = scale sum_j dS_ij k_j, and, summed over the heads that share j, dk_j = scale
  * sum_i dS_ij q_i, dv_j = sum_i p_ij d_out_i.  dq NULL, or dk and dv NULL: not wanted.  p and dS are rounded to bf16 for their
- * products (dS in two parts for dq).  delta is formed from out, and made good by what dq's dS sum up to.  The order of dk's and dv's sums
- * depends on the sizes; two runs of one call agree bit for bit.  Rows of no sequence get 0.  Two enqueued kernels.  workspace: 256-byte aligned. */
+ * products (dS in two parts for dq of heads up to 80).  delta is formed from out, and what out's rounding makes of it is taken out of all three again, by
+ * what dq's dS sum up to.  The order of dk's and dv's sums depends on the sizes; two runs of one call agree bit for bit.  Rows of no sequence get 0.  Two enqueued kernels.  workspace: 256-byte aligned. */
 int attn_backward(const void* d_out, int64_t do_row, int64_t do_head, const void* q, int64_t q_row, int64_t q_head, const void* k,
                   int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head, const void* out, int64_t out_row,
                   int64_t out_head, const float* lse, void* dq, int64_t dq_row, int64_t dq_head, void* dk, int64_t dk_row, int64_t dk_head,

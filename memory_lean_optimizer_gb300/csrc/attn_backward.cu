@@ -3,7 +3,7 @@
 //   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i p_ij dO_i   (i: of all heads that share j)
 // Scores are formed again.  Two product kernels, one for dq (a tile of queries, the keys stream by) and one for dk and
 // dv (a tile of keys, the queries of the group's heads stream by): every sum has one owner and one order, at the
-// price of forming p and dS twice (8 products, not 5); adding dq up from the tiles of keys would need atomics, whose order changes
+// price of forming p and dS twice (7 products, not 5); adding dq up from the tiles of keys would need atomics, whose order changes
 // results, or a buffer of fp32.
 //
 // Both are one kernel in two roles.  A CTA holds two operands of 128 rows (Q and dO, in tensor memory, or K and V, in shared memory) and
@@ -13,18 +13,20 @@
 // scores: nothing is ever transposed through shared memory.  Blocks of 64 so that two pairs and the two sums fit in the 512
 // columns; while the warps work on one pair the tensor cores fill the other.
 //
-// What bf16 costs.  dq, dk and dv are rounded once (1.65e-3 in the 2-norm); p and dS once before (as much again in dk and dv).  delta from out as
-// the forward pass rounded it would add 1.2e-3 to dq and dk: instead dq's kernel sums its dS (sum_j dS_ij = 0 with the true delta), and the keys'
-// kernel takes delta without that excess; dq itself, which cannot, takes dS in two bf16 parts (a product more).  Against 64 bits
-// dk and dv are within 2.4e-3 and dq within 1.7e-3; dq with dS in one part and that delta, 2.6e-3.
-// Where queries see few keys out is not small beside the values it is a mean of, nor is its rounding in dq: a sequence's first 64 queries
-// take the excess out of dq too, dq -= excess sum_j p_ij k_j, for the first block's scores and keys are still there at the end of its first
-// tile (`exact`).  Sequences of 2 to 13 tokens: dq within 1.7e-3 (3.4e-3 before), for 0 to 5 us in 124 to 154 (sequences of 256, 1024).
+// What bf16 costs.  dq, dk and dv are rounded once at their end (1.65e-3 in the 2-norm), p and dS once before (as much again): within 2.4e-3 of 64
+// bits.  For heads up to 80 dq takes dS in two bf16 parts (a product more): 1.7e-3.
+// The rounding of out does not count: delta formed from out as it was rounded is off by some 2^-9 |dO||o|, and every dS of the row by p_ij times that.  In dq this
+// makes sum_j p_ij k_j times it, which is as large as a key where a row's weights lie on few keys, or where the keys have a mean, while dq itself may be small
+// (on 512 tokens it was 5e-3 of dq with sharp weights, 2e-1 with keys and values whose mean is four times their spread).  So dq's kernel sums its dS,
+// which the true delta would make 0: the keys' kernel takes delta without that excess, and dq is rid of the excess times sum_j p_ij k_j, which
+// is formed beside it (a product more).  Where dS is in one part, the excess is that of the rounded values: then dq, like the formula's, does not
+// change when a vector is added to all keys.  16384 tokens, 16 / 4 heads of 64, 80, 96, 128: dq 1042, 1173, 1126, 1268 us; without the product
+// and with dS in two parts 975, 1040, 1095, 1190.
 //
-// Many rows: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: dq 1.23 ms, dk and dv 1.25 ms, together 8 products of
-// 0.55e12 operations at 1.77 PFLOP/s (a library product in a burst: 1.93).  128 x 64 scores from shared memory take 48 cycles for 16 elements of
-// the head where 32 would do (128 bytes a cycle); Q and dO in tensor memory free dq's of it.  A lone CTA takes 7 us from its start to its end, of
-// which two blocks are 1.3: texts of 1 to 2035 tokens (11287 rows, 12 / 3 heads of 80) take 187 us, of which the products are 36.
+// Many rows: the tensor cores bound it, and their power.  16384 tokens, 16 / 4 heads of 128: dq 1.27 ms, dk and dv 1.33 ms, together 8 products of
+// 0.55e12 operations at 1.69 PFLOP/s (a library product in a burst: 1.93).  128 x 64 scores from shared memory take 48 cycles for 16 elements of
+// the head where 32 would do (128 bytes a cycle); operands in tensor memory free dq's of it.  A lone CTA takes 7 us from its start to its end, of
+// which two blocks are 1.3: texts of 1 to 2035 tokens (11287 rows, 12 / 3 heads of 80) take 194 us, of which the products are 41.
 // What the warps' part cost before: tests of masked places in every block (one set of instructions in two), operands read row by row
 // from memory (a line a lane, 3 us a tile), a wait that reads the timer (half of the waits last less).
 #include <type_traits>
@@ -63,6 +65,19 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 }
 
 enum { kQueries = 0, kKeys = 1 };
+
+// Columns of tensor memory (512).  X and Y: two blocks' scores each.  Keys: dk, dv.  Queries: the sums of dS K and of p K, and the tile's
+// operands Q and dO.  Heads over 80 have no room for a second X, which is then formed when the warps have read the one before, nor for what dS's
+// rounding left; over 96 none for dO, which is read from shared memory (48 cycles for 16 elements of a block instead of 32).  A head's 16 elements
+// take 8 columns as an operand, 16 as a sum.  (Heads of 96 with a second X and dO in shared memory: 16384 tokens, dq 1361 us.)
+template <int kRole, int kSteps>
+struct Columns {
+    static constexpr bool kWide = kRole == kQueries && kSteps > 5, kBoth = kRole == kQueries && kSteps <= 6;     // kBoth: Q and dO are here
+    static constexpr uint32_t kX = 0, kNextX = kWide ? 0 : 64, kY = kWide ? 64 : 128, kNextY = 64;
+    static constexpr uint32_t kSum = kWide ? 192 : 256, kDv = 384, kMean = kSum + (kSteps * 16 + 31) / 32 * 32;   // sums start at multiples of 32
+    static constexpr uint32_t kQ = kMean + kSteps * 16, kDo = kQ + kSteps * 8;
+    static_assert(kRole == kKeys || kQ + (kBoth ? 2 : 1) * kSteps * 8 <= 512, "tensor memory");
+};
 
 struct BackwardArgs {
     Sequences seq;
@@ -105,14 +120,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                                                                    const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1,
                                                                    const __grid_constant__ CUtensorMap map_out, const BackwardArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 5];
+    using At = Columns<kRole, kSteps>;
+    __shared__ uint64_t bars[1 + 2 * kStages + 4 + 6];
     __shared__ uint32_t tmem_base;
     __shared__ int gave_up, found, copied;
     __shared__ float tile_delta[kRole == kQueries ? kTile : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // before anything of the stream is needed
     const uint32_t a_full = smem_u32(bars), full = a_full + 8, empty = full + 8 * kStages, x_done = empty + 8 * kStages, ready = x_done + 16,
-                   sums_done = ready + 16, drained = sums_done + 8, halves_ready = drained + 8, delta_ready = halves_ready + 8, tile_full = delta_ready + 8;
+                   sums_done = ready + 16, drained = sums_done + 8, halves_ready = drained + 8, delta_ready = halves_ready + 8, tile_full = delta_ready + 8,
+                   x_free = tile_full + 8;
     if (threadIdx.x == 0) {
         gave_up = found = copied = 0;
         mbar_init(a_full, 8);
@@ -129,6 +146,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         mbar_init(drained, 1);
         mbar_init(halves_ready, 8);
         mbar_init(delta_ready, 4);
+        mbar_init(x_free, 8);
         mbar_init_fence();
         tma_prefetch_map(&map_a0);
         tma_prefetch_map(&map_a1);
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const int64_t slot = unit / (unsigned)heads;
     const Tile tile = find_tile<kTile>(p.seq, kRole == kQueries ? p.slots - 1 - slot : slot);
     tc_fence_after();
-    const uint32_t tmem = tmem_base;      // X: columns 0 and 64, Y: 128 and 192, sums: 256 and 384
+    const uint32_t tmem = tmem_base;
     auto leave = [&]() {
         if (warp == 2) tmem_free<1>(tmem, 512);
     };
@@ -181,7 +199,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
     const uint32_t row_stages = stages + kStages * 2 * kStepBytes;       // kKeys: RowBlock each
     auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait<1>(bar, parity, &gave_up, p.wait_ns); };
 
-    const bool exact = tile.first == tile.start;      // queries that see few keys (see above)
     const int stall = head == 0 && rank == 0 && tile.segment == 1 && tile.first == tile.start ? p.stall : 0;
 
     if (warp < 4) {
@@ -219,23 +236,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             constexpr uint32_t desc_x = mma_desc(128, kStep, false, false), desc_sum = mma_desc(128, kSteps * 16, false, true);
             constexpr uint32_t up = desc_upper(1024);
             const uint32_t a_lo = desc_lower(base, 8192), b_lo = desc_lower(stages, kStep * 128);
-            bool ok = wait(kRole == kKeys ? tile_full : a_full, 0);
+            bool ok = wait(tile_full, 0) && (kRole == kKeys || wait(a_full, 0));
             tc_fence_after();
             uint32_t next = 0, parity = 0, stage = 0;       // of the block whose scores, and whose sums, come next
             auto scores = [&](int i) {
                 ok = wait(full + 8 * next, parity);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t b = b_lo + next * (2 * kStepBytes >> 4), d = tmem + (i & 1) * kStep;
+                const uint32_t b0 = b_lo + next * (2 * kStepBytes >> 4), b1 = b0 + (kStepBytes >> 4);
+                const uint32_t x = tmem + At::kX + (i & 1) * At::kNextX, y = tmem + At::kY + (i & 1) * At::kNextY;
+                auto of_head = [](int j, int rows) { return (uint32_t)((j >> 2) * (rows * 8) + (j & 3) * 2); };   // 16 elements of a head
+                if (kRole == kKeys) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int j = 0; j < kSteps; ++j) mma_ss(x, a_lo + of_head(j, kTile), b0 + of_head(j, kStep), up, desc_x, j == 0);
+                }
 #pragma unroll
-                    for (int j = 0; j < kSteps; ++j)
-                        if (kRole == kQueries)
-                            mma_ts(d + h * 128, tmem + 384 + h * 64 + j * 8, b + h * (kStepBytes >> 4) + (j >> 2) * (kStep * 8) + (j & 3) * 2, up, desc_x, j == 0);
-                        else
-                            mma_ss(d + h * 128, a_lo + h * (kTileBytes >> 4) + (j >> 2) * (kTile * 8) + (j & 3) * 2,
-                                   b + h * (kStepBytes >> 4) + (j >> 2) * (kStep * 8) + (j & 3) * 2, up, desc_x, j == 0);
+                for (int j = 0; j < kSteps; ++j) {
+                    if (At::kBoth) mma_ts(y, tmem + At::kDo + j * 8, b1 + of_head(j, kStep), up, desc_x, j == 0);
+                    else mma_ss(y, a_lo + (kTileBytes >> 4) + of_head(j, kTile), b1 + of_head(j, kStep), up, desc_x, j == 0);
+                }
+                if (kRole == kQueries) {
+                    if (At::kWide && i > 0) {
+                        ok = wait(x_free, (i - 1) & 1);
+                        if (!ok) return;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) mma_ts(x, tmem + At::kQ + j * 8, b0 + of_head(j, kStep), up, desc_x, j == 0);
+                }
                 mma_commit<1>(x_done + 8 * (i & 1));
                 if (++next == kStages) next = 0, parity ^= 1u;
             };
@@ -245,30 +273,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                 if (ok) ok = wait(ready + 8 * (i & 1), i / 2 & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b = b_lo + stage * (2 * kStepBytes >> 4), a = tmem + (i & 1) * kStep;
-                if (kRole == kKeys) {
+                const uint32_t b = b_lo + stage * (2 * kStepBytes >> 4);
+                const uint32_t x = tmem + At::kX + (i & 1) * At::kNextX, y = tmem + At::kY + (i & 1) * At::kNextY;
+                auto add = [&](uint32_t sum, uint32_t a, uint32_t rows, bool first) {     // a's weights times 64 rows
 #pragma unroll
-                    for (int j = 0; j < kStep / 16; ++j)     // dv += p' dO
-                        mma_ts(tmem + 384, a + (j >> 1) * 32 + (j & 1) * 8, b + (kStepBytes >> 4) + j * 128, up, desc_sum, i == 0 && j == 0);
-                }
-#pragma unroll
-                for (int j = 0; j < kStep / 16; ++j)         // dq += dS K, dk += dS' Q
-                    mma_ts(tmem + 256, a + 128 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, i == 0 && j == 0);
+                    for (int j = 0; j < kStep / 16; ++j) mma_ts(sum, a + (j >> 1) * 32 + (j & 1) * 8, rows + j * 128, up, desc_sum, first && j == 0);
+                };
+                if (kRole == kKeys) add(tmem + At::kDv, x, b + (kStepBytes >> 4), i == 0);                   // dv += p' dO
+                add(tmem + At::kSum, y, b, i == 0);                                                         // dq += dS K, dk += dS' Q
                 if (kRole == kQueries) {
-#pragma unroll
-                    for (int j = 0; j < kStep / 16; ++j)     // what dS's rounding left
-                        mma_ts(tmem + 256, a + 144 + (j >> 1) * 32 + (j & 1) * 8, b + j * 128, up, desc_sum, false);
+                    if (!At::kWide) add(tmem + At::kSum, y + 16, b, false);                                  // what dS's rounding left
+                    add(tmem + At::kMean, At::kWide ? y + 16 : x, b, i == 0);                               // p K
                 }
                 mma_commit<1>(empty + 8 * stage);
                 if (++stage == kStages) stage = 0;
             }
             if (ok) mma_commit<1>(sums_done);
-            if (kRole == kQueries && exact && ok && wait(ready, 1)) {      // the sums' correction, over the first block's dS
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < kStep / 16; ++j) mma_ts(tmem + 256, tmem + 128 + (j >> 1) * 32 + (j & 1) * 8, b_lo + j * 128, up, desc_sum, false);
-                mma_commit<1>(sums_done);
-            }
         }
         __syncwarp();
     } else {
@@ -282,8 +302,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         float my_lse = 0.0f, my_delta = 0.0f;
         bool ok = true;
         if (kRole == kQueries) {
-            // Q (four warps) and dO (the others) into tensor memory, two elements a column; delta from out as it was rounded.  (Rows come in by
-            // copies: a lane's own row read from memory takes a line of every lane for each 16 bytes, 3 us a tile.)
+            // Q (four warps) and dO (the others, where it has room) into tensor memory, two elements a column; delta from out as it was rounded.
+            // (Rows come in by copies: a lane's own row read from memory takes a line of every lane for each 16 bytes, 3 us a tile.)
             ok = wait(tile_full, 0);
             const char* const mine = base_ptr + t * kTileBytes + in * 128;
             float s[4] = {};
@@ -297,7 +317,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                     r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
                     if (t == 1) s[k & 3] += dot8(*reinterpret_cast<const uint4*>(mine + kTileBytes + at), v);
                 }
-                tmem_store32(tmem + lanes + 384 + 64 * t + 32 * h, r);
+                const uint32_t to = tmem + lanes + (t ? At::kDo : At::kQ) + 32 * h;
+                if (t == 0 || At::kBoth) {
+                    if (h == 0 || kSteps == 8) tmem_store32(to, r);
+                    else if (kSteps == 6) tmem_store16(to, reinterpret_cast<const uint32_t(&)[16]>(r));
+                    else tmem_store8(to, reinterpret_cast<const uint32_t(&)[8]>(r));
+                }
             }
             my_delta = -((s[0] + s[1]) + (s[2] + s[3]));
             tmem_store_wait();
@@ -315,6 +340,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             }
         }
         F2 excess[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};                       // sum of dS
+        F2 rounded[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};                      // kWide: of dS as it is multiplied
         const F2 minus1 = f2(-1.0f, -1.0f), my_lse2 = f2(my_lse, my_lse), my_delta2 = f2(my_delta, my_delta);
         int at = first_block % per_head;                                       // the block's place in its head
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -332,14 +358,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t x_at = tmem + lanes + (i & 1) * kStep + 32 * t;
+            const uint32_t x_at = tmem + lanes + At::kX + (i & 1) * At::kNextX + 32 * t, y_at = tmem + lanes + At::kY + (i & 1) * At::kNextY + 32 * t;
             uint32_t x[32], y[32];
             tmem_load32(x_at, x);
-            tmem_load32(x_at + 128, y);
+            tmem_load32(y_at, y);
             tmem_wait(x);
             tmem_wait(y);
+            if (At::kWide) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_free);
+            }
             const RowBlock* const rb = reinterpret_cast<const RowBlock*>(base_ptr + (row_stages - base)) + stage;
-            uint32_t pw[16], dw[16];      // p, and for queries what the rounding of dS left
+            uint32_t pw[16], dw[16], left_w[16];      // p, dS, and (queries, not kWide) what the rounding of dS left
             // the columns that the row sees: from .. to - 1 (tests of them only where some are masked: they cost as much as the rest)
             const int from = kRole == kQueries ? 0 : (int)max(row - first, (int64_t)0) - 32 * t;
             const int to = (int)min((kRole == kQueries ? row + 1 : tile.end) - first, (int64_t)kStep) - 32 * t;
@@ -368,20 +399,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
                             if (kRole == kQueries ? only : e + 1 == one) w *= 0.0f;
                         }
                         dw[e / 2] = pack_bf16(u, w);
-                        if (kRole == kKeys) {
-                            pw[e / 2] = pack_bf16(a, b);
-                        } else {
+                        pw[e / 2] = pack_bf16(a, b);
+                        if (kRole == kQueries) {
+                            const F2 as = f2(__uint_as_float(dw[e / 2] << 16), __uint_as_float(dw[e / 2] & 0xFFFF0000u));
                             excess[h] = add2(excess[h], f2(u, w));
-                            split2(fma2(f2(__uint_as_float(dw[e / 2] << 16), __uint_as_float(dw[e / 2] & 0xFFFF0000u)), minus1, f2(u, w)), a, b);
-                            pw[e / 2] = pack_bf16(a, b);
+                            if (At::kWide) {
+                                rounded[h] = add2(rounded[h], as);
+                            } else {
+                                split2(fma2(as, minus1, f2(u, w)), a, b);
+                                left_w[e / 2] = pack_bf16(a, b);
+                            }
                         }
                     }
                 }
             };
             if (masked) weights(std::true_type{});
             else weights(std::false_type{});
-            tmem_store16(kRole == kKeys ? x_at : x_at + 144, pw);
-            tmem_store16(x_at + 128, dw);
+            tmem_store16(At::kWide ? y_at + 16 : x_at, pw);
+            tmem_store16(y_at, dw);
+            if (kRole == kQueries && !At::kWide) tmem_store16(y_at + 16, left_w);
             tmem_store_wait();
             if (partly && in < kStep) {      // rows of masked places are not multiplied, not even by 0
                 char* const b = base_ptr + (stages - base) + stage * 2 * kStepBytes;
@@ -395,53 +431,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         ok = ok && wait(sums_done, 0) && *static_cast<volatile int*>(&gave_up) == 0;     // whoever gave up
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
+        float off = 0.0f;
         if (kRole == kQueries) {
             // sum_j p_ij dP_ij is delta_i, and sum_j dS_ij = 0 with it: what is left of the sum is how far off the rounding of out made
-            // delta.  The keys' gradients take the better one.
+            // delta.  The keys' gradients take the better one; dq is rid of off sum_j p_ij k_j.
             float a, b;
             split2(add2(excess[0], excess[1]), a, b);
-            float* const halves = reinterpret_cast<float*>(base_ptr);          // over the operands, which are done with
+            float* const halves = reinterpret_cast<float*>(base_ptr);          // over Q, which is done with
             halves[kTile * t + in] = a + b;
+            if (At::kWide) {
+                split2(add2(rounded[0], rounded[1]), a, b);
+                halves[kTile * (2 + t) + in] = a + b;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(halves_ready);
-            if (t == 0 || exact) {
-                const bool both = wait(halves_ready, 0) && ok;
-                const float off = halves[in] + halves[kTile + in];
-                if (t == 0) {
-                    // tiles of 128 start at a block of 64
-                    RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
-                    if (tile.first + in / kStep * kStep < tile.end) {
-                        to.lse[in % kStep] = my_lse;
-                        to.delta[in % kStep] = row >= tile.end ? 0.0f : both ? my_delta - off : __builtin_nanf("");
-                    }
+            ok = wait(halves_ready, 0) && ok;
+            off = halves[in] + halves[kTile + in];
+            if (t == 0) {
+                // tiles of 128 start at a block of 64
+                RowBlock& to = p.rows[head * p.row_slots + (tile.start / kStep + tile.segment) + (tile.first - tile.start) / kStep + in / kStep];
+                if (tile.first + in / kStep * kStep < tile.end) {
+                    to.lse[in % kStep] = my_lse;
+                    to.delta[in % kStep] = row >= tile.end ? 0.0f : ok ? my_delta - off : __builtin_nanf("");
                 }
-                ok = __all_sync(0xFFFFFFFFu, both);
             }
-            if (exact && ok) {
-                // the first block's scores are still there (a sequence's first tile has two blocks at most), and its keys
-                const uint32_t x_at = tmem + lanes + 32 * t;
-                uint32_t x[32], w[16];
-                tmem_load32(x_at, x);
-                tmem_wait(x);
-                const int to = in < kStep ? in + 1 - 32 * t : 0;
-                const float e = -(halves[in] + halves[kTile + in]);
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float y[2];
-                    split2(fma2(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, my_lse2), y[0], y[1]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) y[i] = k + i < to ? e * exp2_approx(y[i]) : 0.0f;
-                    w[k / 2] = pack_bf16(y[0], y[1]);
-                }
-                tmem_store16(x_at + 128, w);
-                tmem_store_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ready);
-                ok = wait(sums_done, 1) && *static_cast<volatile int*>(&gave_up) == 0;
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                tc_fence_after();
-            }
+            if (At::kWide) off = halves[2 * kTile + in] + halves[3 * kTile + in];
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
         // the first four warps take half of dq or dk out, the others the other half or dv
         const bool live = row < tile.end;
@@ -450,15 +465,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_attn_backward(const __grid_
         uint16_t* const to = static_cast<uint16_t*>(o.p) + head * o.head + row * o.row;
         const bool sectors = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
         const float f = !ok ? __builtin_nanf("") : which ? 1.0f : p.scale;
-        const uint32_t sum_at = tmem + lanes + 256 + 128 * which;
+        const uint32_t sum_at = tmem + lanes + (which ? At::kDv : At::kSum);
 #pragma unroll 1
         for (int q = kRole == kQueries ? 32 * t : 0; q < p.dim; q += kRole == kQueries ? 64 : 32) {
-            uint32_t r[32];
+            uint32_t r[32], mean[32];
             tmem_load32(sum_at + q, r);
+            if (kRole == kQueries) tmem_load32(tmem + lanes + At::kMean + q, mean);
             tmem_wait(r);
+            if (kRole == kQueries) tmem_wait(mean);
             float z[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) z[k] = blocks ? __uint_as_float(r[k]) * f : 0.0f;
+            for (int k = 0; k < 32; ++k) {
+                z[k] = __uint_as_float(r[k]);
+                if (kRole == kQueries) z[k] = fmaf(-off, __uint_as_float(mean[k]), z[k]);
+                z[k] = blocks ? z[k] * f : 0.0f;
+            }
             if (splits > 1) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
