@@ -382,8 +382,10 @@ def _matrix(t: torch.Tensor, name: str):
 
 
 def pack_activation(x: torch.Tensor, *, stream=None) -> PackedActivation:
-    """x (bf16 or fp32) in 8 bits: off by at most half a step, 2^-7 of the largest magnitude among its block of 32
-    elements of the last dimension.  A block with an infinity or a NaN comes back as NaN."""
+    """x (bf16 or fp32) in 8 bits: off by at most half a step of its block of 32 elements of the last dimension, which is 1/127.5
+    (0.784 %) of the block's largest magnitude at most.  At the ends of the range a step has other limits: it is 2^-133 at least (blocks below 2^-126,
+    of fp32), and in blocks from 127.5 2^121 on, where it cannot grow, their largest are off by less than a whole one.  A
+    block with an infinity or a NaN comes back as NaN."""
     if stream is not None:
         return _on_stream(stream, pack_activation, x)
     dtype = _type(x, "x")

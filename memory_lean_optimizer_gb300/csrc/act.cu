@@ -3,7 +3,8 @@
 // A row is cut into blocks of 32 elements; a block keeps one exponent byte E and 32 codes c from -127 to 127:
 // x = c 2^(E - 133).  E is the smallest with which no element of the block rounds past 127 (E = 127 + the
 // exponent of the largest magnitude, one more if that rounds to 128), so an element is off by half a
-// step, at most 2^-7 (0.78 %) of its block's largest.  Steps are powers of two: codes are exact roundings (to
+// step at most, and the largest is 63.75 steps at least: 1 / 127.5 of it (0.784 %).  (Below 2^-126 the step stays 2^-133; from 127.5 2^121 on it
+// cannot grow, and the largest take the code 127, off by less than a step.)  Steps are powers of two: codes are exact roundings (to
 // nearest even) whatever arithmetic forms them, and c 2^(E - 133) is exact in bf16 and fp32.  A block that holds
 // an infinity or a NaN has E = 255 and comes back as NaN.
 //
