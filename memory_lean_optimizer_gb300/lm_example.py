@@ -17,14 +17,23 @@ import torch
 from . import block, head, hooks
 
 
+def block_heads(dim: int) -> tuple[int, int]:
+    """(heads, kv_heads) of a block of this width: heads of 64 elements or the next more that divide it, else of fewer, of the
+    sizes that attention takes."""
+    first = max(dim // 64, 1)
+    for heads in (*range(first, 0, -1), *range(first + 1, dim + 1)):
+        if dim % heads == 0 and dim // heads % 8 == 0 and dim // heads <= 128:
+            return heads, heads // 2 if heads % 2 == 0 else heads
+    raise ValueError(f"a width of {dim} does not make heads of a multiple of 8 up to 128")
+
+
 class TinyLM(torch.nn.Module):
     def __init__(self, vocab: int, dim: int, blocks: int = 0):
         super().__init__()
+        heads = block_heads(dim) if blocks else (1, 1)
         self.embed = torch.nn.Embedding(vocab, dim, device="cuda", dtype=torch.bfloat16)
         self.tail = head.LMTail(dim, vocab)
-        heads = next(h for h in range(max(dim // 64, 1), 0, -1) if dim % h == 0)
-        kv_heads = heads // 2 if heads % 2 == 0 else heads
-        self.blocks = torch.nn.ModuleList(block.TransformerBlock(dim, heads, kv_heads) for _ in range(blocks))
+        self.blocks = torch.nn.ModuleList(block.TransformerBlock(dim, *heads) for _ in range(blocks))
 
     def forward(self, tokens: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
         x = self.embed(tokens)
