@@ -500,7 +500,8 @@ def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch
     the gate and up values in 8 bits (x for w_in's gradient; gate and up for everything else: h is formed again)."""
     if x.dim() < 2 or w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or x.shape[-1] != w_in.shape[1]:
         raise ValueError(f"x {list(x.shape)}, w_in {list(w_in.shape)} and w_out {list(w_out.shape)} do not fit")
-    return _GatedMLP.apply(x, w_in, w_out, torch.is_grad_enabled())
+    keep = torch.is_grad_enabled() and (x.requires_grad or w_in.requires_grad or w_out.requires_grad)
+    return _GatedMLP.apply(x, w_in, w_out, keep)
 
 
 class TransformerBlock(torch.nn.Module):

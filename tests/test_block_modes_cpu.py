@@ -41,3 +41,16 @@ def test_forward_mode_is_refused(on_host, grad):
                 call()
         # what carries no tangent runs
         assert block.swiglu(torch.randn(3, 16)).shape == (3, 8) and block.gated_mlp(x, w1, w2).shape == (3, 4)
+
+
+@pytest.mark.parametrize("needs", [(), (0,), (1,), (2,), (0, 1, 2)])
+def test_only_what_a_backward_pass_needs_is_packed(on_host, needs):
+    """gated_mlp keeps gate and up if any input wants a gradient, x if w_in does; nothing without grad mode or without such an input."""
+    ts = [t.requires_grad_(i in needs) for i, t in enumerate((torch.randn(3, 4), torch.randn(16, 4), torch.randn(4, 8)))]
+    y = block.gated_mlp(*ts)
+    assert on_host == (["swiglu_keep"] if needs else ["swiglu"]) + (["pack"] if 1 in needs else [])
+    assert y.requires_grad == bool(needs)
+    on_host.clear()
+    with torch.no_grad():
+        block.gated_mlp(*ts)
+    assert on_host == ["swiglu"]
