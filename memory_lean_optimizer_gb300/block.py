@@ -497,10 +497,16 @@ class _GatedMLP(torch.autograd.Function):
 
 def gated_mlp(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor) -> torch.Tensor:
     """swiglu(x w_in^T) w_out^T with autograd, w_in [2 n, dim], w_out [dim, n].  What is kept for the backward pass is x and
-    the gate and up values in 8 bits (x for w_in's gradient; gate and up for everything else: h is formed again)."""
+    the gate and up values in 8 bits (x for w_in's gradient; gate and up for everything else: h is formed again).  Under autocast
+    (bf16) the three are cast first."""
     if x.dim() < 2 or w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape[0] != 2 * w_out.shape[1] or x.shape[-1] != w_in.shape[1]:
         raise ValueError(f"x {list(x.shape)}, w_in {list(w_in.shape)} and w_out {list(w_out.shape)} do not fit")
     keep = torch.is_grad_enabled() and (x.requires_grad or w_in.requires_grad or w_out.requires_grad)
+    if torch.is_autocast_enabled("cuda"):      # the casts are autograd's, outside of the Function, whose backward pass runs without autocast
+        to = torch.get_autocast_dtype("cuda")
+        x, w_in, w_out = (t.to(to) if t.dtype in (torch.float32, torch.bfloat16, torch.float16) else t for t in (x, w_in, w_out))
+        with torch.autocast("cuda", enabled=False):
+            return _GatedMLP.apply(x, w_in, w_out, keep)
     return _GatedMLP.apply(x, w_in, w_out, keep)
 
 
