@@ -536,6 +536,10 @@ class TransformerBlock(torch.nn.Module):
         h, kv = self.heads, self.kv_heads
         qkv = torch.nn.functional.linear(layer_norm(x, self.norm1, None, self.eps), self.qkv).view(x.shape[0], h + 2 * kv, self.head_dim)
         q, k = rotary(qkv[:, :h], qkv[:, h:h + kv], positions, self.rotary)
-        y = attention(q, k, qkv[:, h + kv:], cu_seqlens)
+        v = qkv[:, h + kv:]
+        if v.requires_grad:
+            v = v.contiguous()                 # kept for the backward pass: a view would keep q and k as they were, too
+        y = attention(q, k, v, cu_seqlens)
+        del qkv, q, k, v
         x = x + torch.nn.functional.linear(y.flatten(1), self.proj)
         return x + gated_mlp(layer_norm(x, self.norm2, None, self.eps), self.w_in, self.w_out)
