@@ -12,6 +12,7 @@ eager autograd graph of the same leaves live on at that time: its gradient accum
 """
 from __future__ import annotations
 
+import copy
 import functools
 import math
 from fractions import Fraction
@@ -244,7 +245,16 @@ class RotaryPlan:
             num, den = f.as_integer_ratio()            # den is a power of two: the quotient is a shift
             shift = den.bit_length() - 1 + _TURN_BITS - 64
             turns.append((num * _TURNS_PER_RADIAN + (1 << shift - 1) >> shift) % 2 ** 64)
-        self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device=device)
+        self._turns = [t - (t >> 63 << 64) for t in turns]
+        self.turns = torch.tensor(self._turns, dtype=torch.int64, device=device)
+
+    def to(self, device) -> RotaryPlan:
+        """The plan on a device: itself, or one like it."""
+        if self.turns.device == torch.device(device):
+            return self
+        plan = copy.copy(self)
+        plan.turns = torch.tensor(self._turns, dtype=torch.int64, device=device)
+        return plan
 
     def tensors(self):
         return (self.turns,)
@@ -531,6 +541,11 @@ class TransformerBlock(torch.nn.Module):
         self.proj = torch.nn.Parameter(torch.zeros(dim, dim, **bf16))
         self.w_in = new(2 * hidden, dim)
         self.w_out = torch.nn.Parameter(torch.zeros(dim, hidden, **bf16))
+
+    def _apply(self, fn, *args, **kw):
+        super()._apply(fn, *args, **kw)
+        self.rotary = self.rotary.to(fn(self.rotary.turns).device)      # where the parameters go
+        return self
 
     def forward(self, x: torch.Tensor, positions: torch.Tensor, cu_seqlens: torch.Tensor | None = None) -> torch.Tensor:
         h, kv = self.heads, self.kv_heads
