@@ -528,7 +528,7 @@ int act_swiglu_backward(const void* dh, int64_t lddh, const int8_t* codes, int64
  * lse is fp32 [heads][rows].  Rows of no sequence (before the first, behind the last) are set to 0 in both.  Nothing that a row
  * does not see reaches it, NaN and infinities included.  Products and sums are fp32, p is rounded to bf16 for its
  * product; two runs of one call agree bit for bit.  Values of cu_seqlens outside [0, rows] are taken as the nearest of them; what falls
- * gives undefined values, within the buffers.  scale > 0.  One enqueued kernel; its waits are bounded (seconds): should
+ * gives undefined values, within the buffers.  scale > 0, scale log2(e) finite.  One enqueued kernel; its waits are bounded (seconds): should
  * one run out, the results it held up are NaN. */
 int attn_forward(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
                  int64_t v_head, void* out, int64_t out_row, int64_t out_head, float* lse, const int32_t* cu_seqlens, int64_t sequences,

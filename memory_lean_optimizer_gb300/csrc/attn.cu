@@ -13,7 +13,8 @@ int check_attn(const AttnCall& c) {
     if (c.dim < 8 || c.dim > 128 || c.dim % 8) return set_error(OPTIM_EINVAL, "heads must have 8 to 128 elements, a multiple of 8, not %lld", (long long)c.dim);
     if (c.heads < 1 || c.kv_heads < 1 || c.heads > 65536 || c.heads % c.kv_heads)
         return set_error(OPTIM_EINVAL, "%lld query heads cannot share %lld key heads", (long long)c.heads, (long long)c.kv_heads);
-    if (!(c.scale > 0.0f && c.scale <= FLT_MAX)) return set_error(OPTIM_EINVAL, "scale must be positive and finite");
+    if (!(c.scale > 0.0f && c.scale * kLog2e <= FLT_MAX))      // scores are taken in powers of two
+        return set_error(OPTIM_EINVAL, "scale must be positive and finite, times log2(e) too");
     if (tile_slots(c.seq, 64) > (((int64_t)1 << 31) - 1) / c.heads) return set_error(OPTIM_EINVAL, "too many rows, sequences and heads");
     return OPTIM_OK;
 }
