@@ -512,7 +512,8 @@ int act_unpack_i8(const int8_t* codes, int64_t ldc, const uint8_t* exponents, in
                   int64_t cols, int32_t type, void* stream);
 
 /* The gated activation h = g s(g) u, s(g) = 1 / (1 + e^-g), of rows that hold g (cols elements) and then u.
- * codes, exponents (both or neither NULL): g and u of row r in the form above, as rows 2r and 2r + 1. */
+ * codes, exponents (both or neither NULL): g and u of row r in the form above, as rows 2r and 2r + 1.  g below -87.3 (bf16) or -88.7
+ * (fp32) give h = 0. */
 int act_swiglu_forward(const void* gate_up, int64_t ldg, void* h, int64_t ldh, int8_t* codes, int64_t ldc, uint8_t* exponents,
                        int64_t lde, int64_t rows, int64_t cols, int32_t type, void* stream);
 /* Its gradients at the g and u that the codes stand for: d_gate_up (dg, then du) with dg = dh u s(g) (1 + g (1 - s(g))) and

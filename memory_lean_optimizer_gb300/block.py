@@ -148,7 +148,7 @@ def attention_backward(d_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
                        cu_seqlens: torch.Tensor | None = None, scale: float | None = None, need_q: bool = True, need_kv: bool = True, *,
                        stream=None):
     """(dq, dk, dv) from the gradient of out and what the forward call was given and returned; None for those that are not
-    needed (dk and dv go together).  Rows of no sequence get 0."""
+    needed (dk and dv go together; dq's kernel runs for them too, they need what it sums).  Rows of no sequence get 0."""
     if stream is not None:
         return _on_stream(stream, attention_backward, d_out, q, k, v, out, lse, cu_seqlens, scale, need_q, need_kv)
     if d_out.shape != q.shape or out.shape != q.shape:

@@ -1,6 +1,7 @@
 // attn_forward.cu -- causal attention over packed sequences, grouped heads, forward.
 //   s_ij = scale q_i k_j (j <= i, of i's sequence),  lse_i = log sum_j exp s_ij,  o_i = sum_j exp(s_ij - lse_i) v_j
-// One pass over the keys with a running reference m and sum: p_ij = 2^(s_ij log2 e - m), o and the sum are in units of 2^m.
+// One pass over the keys with a running reference m and sum (Milakov and Gimelshein, Online normalizer calculation for softmax, 2018): p_ij = 2^(s_ij
+// log2 e - m), o and the sum are in units of 2^m.
 //
 // A CTA takes 256 rows of one head as two tiles of 128, which share the keys' and values' blocks of 128 rows
 // in shared memory.  Scores and outputs are accumulators in tensor memory (2 x 128 and 2 x 128 columns, all 512); a
